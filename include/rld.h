@@ -433,6 +433,118 @@ int rld_moe_grouped_pair(const rld_moe_route* route_a, const rld_moe_route* rout
                          uint32_t xa_rows_cap, void* workspace, size_t workspace_bytes,
                          void* stream);
 
+/* Bytes of workspace rld_proj needs: the fp32 low-rank rows [n][max_rank] and,
+ * above k_in 512, their partial sums [ceil(k_in / 512)][n][max_rank].  16-byte
+ * aligned device memory; nothing in it must start at any value or is carried
+ * between calls; calls that share it must be ordered (captured graphs that
+ * share one included). */
+size_t rld_proj_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t max_rank);
+
+/* The shared projection with each row's adapter, in one output rounding:
+ *   out_i = bf16(x_i W^T + scale_s (x_i A_s^T) B_s^T),  s = seq_slot[i],
+ * and out_i = bf16(x_i W^T) for base rows.  Products and sums are fp32 (the
+ * low-rank row stays fp32; it is not rounded to BF16 as the folds above round
+ * xa and delta, so results differ from a projection followed by rld_bgmv by
+ * those roundings).  Overwrites out; unlike the folds it writes base rows.
+ *   w        device BF16 [n_out, k_in] row-major, row j at w + j*w_row_stride
+ *   x        device BF16, row i at x + i*x_row_stride, k_in elements read
+ *   seq_slot device int32 [n]; contents may change between calls
+ *   out      device BF16, n_out elements written of row i at
+ *            out + i*out_row_stride; the rest of the row is left alone.  out
+ *            must not overlap w or x
+ * n == 0 is a no-op.  RLD_EUNSUPPORTED for row strides of w and x above 2^21,
+ * k_in or n_out above 2^24, or more than 2^23 tiles of 64 x 64 outputs.
+ * Results do not change from run to run; a row's summation order may depend on
+ * n (the tile shape does). */
+int rld_proj(const rld_route* route, const void* w, uint32_t w_row_stride, const void* x,
+             uint32_t x_row_stride, const int32_t* seq_slot, uint32_t n, void* out,
+             uint32_t out_row_stride, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace rld_proj_grad needs, under the contract of rld_proj's. */
+size_t rld_proj_grad_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t n_out,
+                                     uint32_t max_rank, uint32_t max_loras);
+
+/* Gradient of rld_proj with W frozen.  With u_i = scale_s x_i A_s^T and
+ * g_i = scale_s dy_i B_s (fp32):
+ *   dx_i = bf16(dy_i W + g_i A_s)                          (base rows: dy_i W)
+ *   dA_s = sum of g_i^T x_i, dB_s = sum of dy_i^T u_i over the rows i of slot s
+ *   dy       device BF16, row i at dy + i*dy_row_stride, n_out elements read
+ *   dx       device BF16, written like out above; NULL: not wanted (w is then
+ *            not read and may be NULL)
+ *   da_table device array of max_loras device addresses: slot s's gradient of A,
+ *            fp32 [max_rank, k_in], 16-byte aligned; 0: not wanted for the slot.
+ *            db_table likewise, fp32 [n_out, max_rank].  NULL: none wanted (x
+ *            may be NULL if neither is).  Gradients of different slots must not
+ *            overlap
+ *   accumulate  0: da and db are overwritten (with zeros for a slot without
+ *            rows); nonzero: the gradient is added to what they hold
+ * Every routed row of a slot adds to the slot's gradient in ascending row order
+ * of fixed groups: results do not change from run to run.  n == 0: zeros, or
+ * nothing with accumulate.  Errors as rld_proj; RLD_EINVAL if nothing is
+ * wanted; RLD_EUNSUPPORTED if max_loras * ceil(max(k_in, n_out) / 64) reaches
+ * 2^23. */
+int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_row_stride, const void* x,
+                  uint32_t x_row_stride, const void* dy, uint32_t dy_row_stride,
+                  const int32_t* seq_slot, uint32_t n, void* dx, uint32_t dx_row_stride,
+                  const uint64_t* da_table, const uint64_t* db_table, int accumulate,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace rld_moe_router needs, under the contract of rld_proj's:
+ * a count and a partial sum per expert and block of 64 tokens. */
+size_t rld_moe_router_workspace_bytes(uint32_t num_tokens, uint32_t num_experts,
+                                      uint32_t top_k);
+
+/* The MoE router: from each token's logits the routing that rld_moe_gather
+ * (indices) and rld_moe_grouped (expert_offsets, sorted_token_ids) take, the
+ * weights of the combine, and the balance loss.
+ *   logits   device, fp32 (logits_f32 != 0) or BF16; token t at
+ *            logits + t*logits_row_stride elements, num_experts read; aligned to
+ *            the element, any num_experts up to 1024 and stride >= num_experts
+ *   token_mask  device int32 [num_tokens], 0 = the token is padding; or NULL
+ *   top_k    1..min(num_experts, 32)
+ *   norm_topk   nonzero: a token's weights are divided by their sum
+ *   indices  int32 [num_tokens, top_k]: experts by falling logit, the lower
+ *            index first among equals
+ *   weights  fp32 [num_tokens, top_k]: the softmax over all experts at indices
+ *   counts   int32 [num_experts + 1]: rows of each expert, then the number of
+ *            tokens that route; or NULL
+ *   expert_offsets  int32 [num_experts + 1]: prefix sum of the counts; or NULL
+ *   sorted_token_ids, sorted_rows  int32 [num_tokens * top_k]: the rows by
+ *            (expert, token): each row's token and its place t*top_k + j in
+ *            indices; -1 from expert_offsets[num_experts] on; or NULL
+ *   loss     fp32 [1]: num_experts / (top_k N^2) * sum_e counts[e] * sum_t p_te
+ *            with N = counts[num_experts], 1 for an even load, 0 if N is 0; or
+ *            NULL
+ * An expert whose logit is -Inf is never chosen; places left over hold index -1
+ * and weight 0.  A token that is masked, or whose logits are all -Inf, is empty:
+ * indices -1, weights 0, in no count.  A token with a NaN or +Inf logit gets
+ * indices -1 and NaN weights, counts in N and makes the loss NaN.
+ * num_tokens == 0 writes zero counts, offsets and loss.
+ * RLD_EINVAL on top_k 0 or above num_experts; RLD_EUNSUPPORTED on num_experts
+ * above 1024, top_k above 32, num_tokens * top_k of 2^31 or num_tokens of 2^26
+ * and more. */
+int rld_moe_router(const void* logits, int logits_f32, uint32_t logits_row_stride,
+                   const int32_t* token_mask, uint32_t num_tokens, uint32_t num_experts,
+                   uint32_t top_k, int norm_topk, int32_t* indices, float* weights,
+                   int32_t* counts, int32_t* expert_offsets, int32_t* sorted_token_ids,
+                   int32_t* sorted_rows, float* loss, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/* Gradient of rld_moe_router to the logits, from its indices and counts:
+ *   dweights fp32 [num_tokens, top_k], the gradient of weights; NULL: none
+ *            (indices may then be NULL); entries at index -1 are not read into it
+ *   dloss    fp32 [1] on the device, the gradient of loss; NULL: none (counts
+ *            may then be NULL).  The counts themselves have no gradient
+ *   dlogits  of the logits' type, row t at dlogits + t*dlogits_row_stride,
+ *            num_experts written; zeros for empty tokens, NaN for a token with a
+ *            NaN or +Inf logit.  May be the logits themselves
+ * RLD_EINVAL if both gradients are NULL; otherwise errors as rld_moe_router. */
+int rld_moe_router_grad(const void* logits, int logits_f32, uint32_t logits_row_stride,
+                        const int32_t* token_mask, uint32_t num_tokens, uint32_t num_experts,
+                        uint32_t top_k, int norm_topk, const int32_t* indices,
+                        const int32_t* counts, const float* dweights, const float* dloss,
+                        void* dlogits, uint32_t dlogits_row_stride, void* stream);
+
 /* ------------------------------------------------------------ diagnostics -- */
 
 const char* rld_status_string(int status);

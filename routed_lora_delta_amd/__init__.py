@@ -104,6 +104,18 @@ _SIGS = {
     "rld_lora_shrink": (c_int, [_L, _P, c_uint32, c_uint32, _P, _P, c_size_t, _P]),
     "rld_lora_expand_fold": (c_int, [_L, _P, c_uint32, _P, c_uint32, _P]),
     "rld_lora_delta": (c_int, [_L, _P, c_uint32, c_uint32, _P, c_uint32, _P, _P, c_size_t, _P]),
+    "rld_proj_workspace_bytes": (c_size_t, [c_uint32, c_uint32, c_uint32]),
+    "rld_proj": (c_int, [_R, _P, c_uint32, _P, c_uint32, _P, c_uint32, _P, c_uint32, _P,
+                         c_size_t, _P]),
+    "rld_proj_grad_workspace_bytes": (c_size_t, [c_uint32, c_uint32, c_uint32, c_uint32,
+                                                 c_uint32]),
+    "rld_proj_grad": (c_int, [_R, _P, c_uint32, _P, c_uint32, _P, c_uint32, _P, c_uint32, _P,
+                              c_uint32, _P, _P, c_int, _P, c_size_t, _P]),
+    "rld_moe_router_workspace_bytes": (c_size_t, [c_uint32, c_uint32, c_uint32]),
+    "rld_moe_router": (c_int, [_P, c_int, c_uint32, _P, c_uint32, c_uint32, c_uint32, c_int, _P,
+                               _P, _P, _P, _P, _P, _P, _P, c_size_t, _P]),
+    "rld_moe_router_grad": (c_int, [_P, c_int, c_uint32, _P, c_uint32, c_uint32, c_uint32, c_int,
+                                    _P, _P, _P, _P, _P, c_uint32, _P]),
     "rld_moe_gather_shrink": (c_int, [_M, _P, c_uint32, _P, _P, c_uint32, c_uint32, _P, _P]),
     "rld_moe_gather_expand_fold": (c_int, [_M, _P, _P, _P, c_uint32, c_uint32, _P, c_uint32,
                                            _P]),
@@ -305,6 +317,54 @@ def rld_lora_delta(pair, x, x_row_stride, m, base_out, out_row_stride, xa, works
     return _lib.rld_lora_delta(ctypes.byref(pair), ptr(x), x_row_stride, m, ptr(base_out),
                                out_row_stride, ptr(xa), ptr(workspace), workspace_bytes,
                                stream_handle(stream))
+
+
+def rld_proj_workspace_bytes(n, k_in, max_rank):
+    return _lib.rld_proj_workspace_bytes(n, k_in, max_rank)
+
+
+def rld_proj(route, w, w_row_stride, x, x_row_stride, seq_slot, n, out, out_row_stride,
+             workspace, workspace_bytes, stream=None):
+    return _lib.rld_proj(ctypes.byref(route), ptr(w), w_row_stride, ptr(x), x_row_stride,
+                         ptr(seq_slot), n, ptr(out), out_row_stride, ptr(workspace),
+                         workspace_bytes, stream_handle(stream))
+
+
+def rld_proj_grad_workspace_bytes(n, k_in, n_out, max_rank, max_loras):
+    return _lib.rld_proj_grad_workspace_bytes(n, k_in, n_out, max_rank, max_loras)
+
+
+def rld_proj_grad(route, w, w_row_stride, x, x_row_stride, dy, dy_row_stride, seq_slot, n, dx,
+                  dx_row_stride, da_table, db_table, accumulate, workspace, workspace_bytes,
+                  stream=None):
+    return _lib.rld_proj_grad(ctypes.byref(route), ptr(w), w_row_stride, ptr(x), x_row_stride,
+                              ptr(dy), dy_row_stride, ptr(seq_slot), n, ptr(dx), dx_row_stride,
+                              ptr(da_table), ptr(db_table), int(accumulate), ptr(workspace),
+                              workspace_bytes, stream_handle(stream))
+
+
+def rld_moe_router_workspace_bytes(num_tokens, num_experts, top_k):
+    return _lib.rld_moe_router_workspace_bytes(num_tokens, num_experts, top_k)
+
+
+def rld_moe_router(logits, logits_f32, logits_row_stride, token_mask, num_tokens, num_experts,
+                   top_k, norm_topk, indices, weights, counts, expert_offsets, sorted_token_ids,
+                   sorted_rows, loss, workspace, workspace_bytes, stream=None):
+    return _lib.rld_moe_router(ptr(logits), int(logits_f32), logits_row_stride, ptr(token_mask),
+                               num_tokens, num_experts, top_k, int(norm_topk), ptr(indices),
+                               ptr(weights), ptr(counts), ptr(expert_offsets),
+                               ptr(sorted_token_ids), ptr(sorted_rows), ptr(loss),
+                               ptr(workspace), workspace_bytes, stream_handle(stream))
+
+
+def rld_moe_router_grad(logits, logits_f32, logits_row_stride, token_mask, num_tokens,
+                        num_experts, top_k, norm_topk, indices, counts, dweights, dloss, dlogits,
+                        dlogits_row_stride, stream=None):
+    return _lib.rld_moe_router_grad(ptr(logits), int(logits_f32), logits_row_stride,
+                                    ptr(token_mask), num_tokens, num_experts, top_k,
+                                    int(norm_topk), ptr(indices), ptr(counts), ptr(dweights),
+                                    ptr(dloss), ptr(dlogits), dlogits_row_stride,
+                                    stream_handle(stream))
 
 
 def rld_moe_gather_shrink(route, x, x_row_stride, indices, row_adapter, top_k, n_rows, xa,

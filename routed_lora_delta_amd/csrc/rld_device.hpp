@@ -61,6 +61,7 @@ __device__ __forceinline__ RLD_GLOBAL T* gp(uint64_t addr) {
 }
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int uint2v __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ uint4 load16(const RLD_GLOBAL uint16_t* p) {
   const u32x4 v = *reinterpret_cast<const RLD_GLOBAL u32x4*>(p);
@@ -70,6 +71,10 @@ __device__ __forceinline__ uint4 load16(const RLD_GLOBAL uint16_t* p) {
 __device__ __forceinline__ void store16(RLD_GLOBAL uint16_t* p, const uint4& v) {
   const u32x4 w = {v.x, v.y, v.z, v.w};
   *reinterpret_cast<RLD_GLOBAL u32x4*>(p) = w;
+}
+
+__device__ __forceinline__ uint32_t div_ceil_dev(uint32_t a, uint32_t b) {
+  return a / b + (a % b != 0u ? 1u : 0u);
 }
 
 __device__ __forceinline__ uint4 zero16() { return make_uint4(0u, 0u, 0u, 0u); }

@@ -452,7 +452,7 @@ size_t rld_proj_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t max_rank);
  *   out      device BF16, n_out elements written of row i at
  *            out + i*out_row_stride; the rest of the row is left alone.  out
  *            must not overlap w or x
- * n == 0 is a no-op.  RLD_EUNSUPPORTED for row strides of w and x above 2^21,
+ * n == 0 is a no-op.  RLD_EUNSUPPORTED for row strides above 2^21,
  * k_in or n_out above 2^24, or more than 2^23 tiles of 64 x 64 outputs.
  * Results do not change from run to run; a row's summation order may depend on
  * n (the tile shape does). */
@@ -480,7 +480,7 @@ size_t rld_proj_grad_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t n_out,
  *            rows); nonzero: the gradient is added to what they hold
  * Every routed row of a slot adds to the slot's gradient in ascending row order
  * of fixed groups: results do not change from run to run.  n == 0: zeros, or
- * nothing with accumulate.  Errors as rld_proj; RLD_EINVAL if nothing is
+ * nothing with accumulate.  Errors as rld_proj (the stride of x is not limited); RLD_EINVAL if nothing is
  * wanted; RLD_EUNSUPPORTED if max_loras * ceil(max(k_in, n_out) / 64) reaches
  * 2^23. */
 int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_row_stride, const void* x,

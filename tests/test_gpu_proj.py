@@ -254,6 +254,32 @@ def test_proj_large(n, k, m, r):
     c.check_grads()
 
 
+@pytest.mark.parametrize("n,k,m,r,slots,layout", [
+    (2500, 200, 4360, 16, 3, "runs"),     # K of three steps and an eighth
+    (2100, 72, 4872, 40, 40, "mixed"),    # one step and a tail, many slots a tile
+    (2600, 328, 4104, 128, 2, "wild"),
+    (4100, 64, 2568, 8, 5, "runs"),
+])
+def test_proj_many_tiles(n, k, m, r, slots, layout):
+    """Grids of 256 x 256 tiles, forward and (k and m exchanged) backward."""
+    say(f"case: proj many tiles {n} {k} {m} {r} {layout}")
+    Case(n, k, m, r, slots, layout, 8, 16, 8, seed=21).check_proj()
+    Case(n, m, k, r, slots, layout, 8, 16, 8, seed=22).check_grads()
+
+
+def test_many_tiles_rows_apart():
+    """A slot's NaN and infinities stay with its rows where a wave's tile holds
+    rows of several slots."""
+    say("case: proj many tiles, rows apart")
+    c = Case(2304, 136, 4608, 16, 4, seed=23)
+    out = c.proj()
+    c.bd[1] = 0x7F80
+    c.ad[1, 0] = NAN16
+    out2 = c.proj()
+    keep = c.slot != 1
+    assert np.array_equal(out[keep], out2[keep]) and not np.array_equal(out, out2)
+
+
 def test_unadapted_slots_are_base_rows():
     c = Case(70, 136, 200, 16, 4, adapted=[True, False, True, False], seed=3)
     c.check_proj()

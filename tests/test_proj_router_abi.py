@@ -55,6 +55,7 @@ def test_route_refusals(kw, status):
     (dict(w=FAKE + 8), R.RLD_EALIGN), (dict(x=FAKE + 2), R.RLD_EALIGN),
     (dict(out=FAKE + 8), R.RLD_EALIGN), (dict(wk=FAKE + 8), R.RLD_EALIGN),
     (dict(ws=(1 << 21) + 8), R.RLD_EUNSUPPORTED), (dict(xs=(1 << 21) + 8), R.RLD_EUNSUPPORTED),
+    (dict(os=(1 << 21) + 8), R.RLD_EUNSUPPORTED),
     (dict(n=1 << 30), R.RLD_EUNSUPPORTED), (dict(wb=255), R.RLD_ENOSPACE),
 ])
 def test_proj_refusals(kw, status):
@@ -71,6 +72,7 @@ def test_proj_refusals(kw, status):
     (dict(dx=FAKE + 8), R.RLD_EALIGN), (dict(wk=FAKE + 4), R.RLD_EALIGN),
     (dict(da=FAKE + 4), R.RLD_EALIGN), (dict(db=FAKE + 4), R.RLD_EALIGN),
     (dict(dys=(1 << 21) + 8), R.RLD_EUNSUPPORTED), (dict(ws=(1 << 21) + 8), R.RLD_EUNSUPPORTED),
+    (dict(dxs=(1 << 21) + 8), R.RLD_EUNSUPPORTED),
     (dict(n=1 << 30), R.RLD_EUNSUPPORTED), (dict(wb=512), R.RLD_ENOSPACE),
 ])
 def test_proj_grad_refusals(kw, status):

@@ -433,12 +433,13 @@ int rld_moe_grouped_pair(const rld_moe_route* route_a, const rld_moe_route* rout
                          uint32_t xa_rows_cap, void* workspace, size_t workspace_bytes,
                          void* stream);
 
-/* Bytes of workspace rld_proj needs: the fp32 low-rank rows [n][max_rank] and,
- * above k_in 512, their partial sums [ceil(k_in / 512)][n][max_rank].  16-byte
- * aligned device memory; nothing in it must start at any value or is carried
+/* Bytes of workspace rld_proj needs: the rows' order by slot, the fp32 low-rank
+ * rows [n][max_rank] and their partial sums [ceil(k_in / 512)][n][max_rank].
+ * 16-byte aligned device memory; nothing in it must start at any value or is carried
  * between calls; calls that share it must be ordered (captured graphs that
  * share one included). */
-size_t rld_proj_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t max_rank);
+size_t rld_proj_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t max_rank,
+                                uint32_t max_loras);
 
 /* The shared projection with each row's adapter, in one output rounding:
  *   out_i = bf16(x_i W^T + scale_s (x_i A_s^T) B_s^T),  s = seq_slot[i],
@@ -453,7 +454,8 @@ size_t rld_proj_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t max_rank);
  *            out + i*out_row_stride; the rest of the row is left alone.  out
  *            must not overlap w or x
  * n == 0 is a no-op.  RLD_EUNSUPPORTED for row strides above 2^21,
- * k_in or n_out above 2^24, or more than 2^23 tiles of 64 x 64 outputs.
+ * k_in or n_out above 2^24, and from 2^23 tiles of 64 x 64 outputs, 2^22
+ * pairs of a slot and 64 columns, or n * max_rank of 2^32 on.
  * Results do not change from run to run; a row's summation order may depend on
  * n (the tile shape does). */
 int rld_proj(const rld_route* route, const void* w, uint32_t w_row_stride, const void* x,
@@ -481,8 +483,7 @@ size_t rld_proj_grad_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t n_out,
  * Every routed row of a slot adds to the slot's gradient in ascending row order
  * of fixed groups: results do not change from run to run.  n == 0: zeros, or
  * nothing with accumulate.  Errors as rld_proj (the stride of x is not limited); RLD_EINVAL if nothing is
- * wanted; RLD_EUNSUPPORTED if max_loras * ceil(max(k_in, n_out) / 64) reaches
- * 2^23. */
+ * wanted. */
 int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_row_stride, const void* x,
                   uint32_t x_row_stride, const void* dy, uint32_t dy_row_stride,
                   const int32_t* seq_slot, uint32_t n, void* dx, uint32_t dx_row_stride,

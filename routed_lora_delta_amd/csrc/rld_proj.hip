@@ -4,19 +4,25 @@
 //   dx_i = dy_i W  + g_i A_s,     g_i = scale_s dy_i B_s
 //   dA_s = sum_{i in s} g_i^T x_i,   dB_s = sum_{i in s} dy_i^T u_i
 //
-// (W frozen).  Four kernels:
+// (W frozen).  Kernels:
+//   sort     the rows by slot (stable; base rows last), so that a tile's rows name
+//            few slots and a slot's rows lie together.  The kernels below work on
+//            sorted positions and reach x, dy and the outputs through the order.
 //   low      the low-rank products u and g of every routed row, as fp32 partial
 //            sums of k chunks; low_reduce adds the chunks and applies the scale.
 //   tile     one output tile of x W^T (or dy W) on the matrix cores, with the
 //            low rows times the slots' second matrices added into the same
 //            accumulators, so the output is rounded once and written once.
-//   lists    each slot's rows in ascending order.
-//   wgrad    dA or dB: the products over a slot's rows.
+//   rows     the same for up to 64 rows, where reading W is all the time: blocks
+//            of 16 columns, K dealt to the waves, no sort and no reduce launch.
+//   wgrad    dA and dB: the products over a slot's rows.
 //
 // u and g stay in fp32 (bf16 copies would add a rounding of 2^-9 to every
 // term).  The matrix cores take bf16, so a low value enters as the sum of two
 // bf16 parts where the result is rounded to bf16 (16 significand bits, an
 // error of 2^-17) and of three where it is fp32 (24 bits: all of it).
+#include <type_traits>
+
 #include "rld_device.hpp"
 #include "rld_internal.hpp"
 
@@ -24,6 +30,7 @@ namespace rld {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 #define RLD_LDS __attribute__((address_space(3)))
+#define RLD_CONST __attribute__((address_space(4)))
 
 constexpr uint32_t kLowRows = 64;    // rows of a low item
 constexpr uint32_t kLowChunk = 512;  // k elements of a low item
@@ -55,60 +62,160 @@ __device__ __forceinline__ void bf16_parts(const float (&v)[8], uint4 (&out)[NP]
   }
 }
 
+// ------------------------------------------------------------------- sort ----
+
+struct SortArgs {
+  uint64_t seq_, atab_, btab_;
+  uint64_t order_, skey_;  // [n]: the row at a sorted position; its slot, -1 for base rows
+  uint64_t span_;          // [max_loras][2]: a slot's first position and rows
+  uint32_t n, max_loras, keep;  // keep: leave the rows in their order
+};
+
+constexpr uint32_t kSortBatch = 4096;  // rows of a pass: 16 a thread
+
+typedef int i32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+
+// Keys of this thread's 16 consecutive rows of a batch; past n: INT_MIN.
+__device__ __forceinline__ void sort_keys(const SortArgs& a, uint32_t r0, int (&key)[16]) {
+  const RLD_GLOBAL int32_t* seq = gp<const int32_t>(a.seq_);
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    if (r0 + 4 * v + 4 <= a.n) {
+      const i32x4_a4 k = *reinterpret_cast<const RLD_GLOBAL i32x4_a4*>(seq + r0 + 4 * v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) key[4 * v + e] = k[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        key[4 * v + e] = r0 + 4 * v + e < a.n ? seq[r0 + 4 * v + e] : (int)0x80000000;
+    }
+    // ids that name no slot sort as max_loras
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (key[4 * v + e] < 0 || (uint32_t)key[4 * v + e] >= a.max_loras)
+        key[4 * v + e] = r0 + 4 * v + e < a.n ? (int)a.max_loras : 0x7fffffff;
+  }
+}
+
+// Sum over the block before this thread, and the block's sum.
+__device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* wsum, uint32_t& total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t inc = v;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t u = __shfl_up(inc, o);
+    if (lane >= o) inc += u;
+  }
+  __syncthreads();
+  if (lane == 63) wsum[wave] = inc;
+  __syncthreads();
+  uint32_t at = inc - v;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    at += w < wave ? wsum[w] : 0;
+    total += wsum[w];
+  }
+  return at;
+}
+
+// One block per slot, and one for the base rows: its rows in ascending order,
+// behind those of the slots below it, which the block counts itself (no block
+// waits for another).
+__global__ void __launch_bounds__(256) sort_kernel(SortArgs a) {
+  __shared__ uint32_t wsum[4];
+  const int s = (int)blockIdx.x;
+  const bool base = (uint32_t)s == a.max_loras;
+  const bool active =
+      !base && gp<const uint64_t>(a.atab_)[s] != 0ull && gp<const uint64_t>(a.btab_)[s] != 0ull;
+  int key[16];
+  uint32_t below = 0, first;
+  for (uint32_t b0 = 0; b0 < a.n; b0 += kSortBatch) {
+    sort_keys(a, b0 + threadIdx.x * 16, key);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) below += key[e] < s;
+  }
+  block_prefix(below, wsum, first);
+  uint32_t cnt = 0;
+  for (uint32_t b0 = 0; b0 < a.n; b0 += kSortBatch) {
+    const uint32_t r0 = b0 + threadIdx.x * 16;
+    if (a.n > kSortBatch) sort_keys(a, r0, key);
+    uint32_t own = 0, tot;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) own += key[e] == s;
+    uint32_t at = first + cnt + block_prefix(own, wsum, tot);
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (key[e] == s) {
+        const uint32_t pos = a.keep ? r0 + e : at;
+        gp<int32_t>(a.order_)[pos] = (int)(r0 + e);
+        gp<int32_t>(a.skey_)[pos] = active ? s : -1;
+        ++at;
+      }
+    cnt += tot;
+  }
+  if (!base && threadIdx.x == 0) {
+    gp<uint32_t>(a.span_)[2 * s] = first;
+    gp<uint32_t>(a.span_)[2 * s + 1] = active ? cnt : 0u;
+  }
+}
+
 // -------------------------------------------------------------------- low ----
 
 struct LowArgs {
-  uint64_t x_, seq_, mtab_, otab_, stab_, partial_;
+  uint64_t x_, mtab_, otab_, stab_, partial_;
+  uint64_t order_;  // sorted positions' rows, or 0: positions are rows
+  uint64_t key_;    // slots by position
   uint64_t low_;    // fp32 [n][R], or 0: not wanted
   uint64_t parts_;  // bf16 [n][2][R]: the value's two parts, or 0
-  uint32_t xs, n, max_loras, K, R, nch, nz;
+  uint32_t xs, n, max_loras, K, R, nch, nz, tiles;
 };
 
 // Four columns of a low row, scaled, to where they are wanted.
-__device__ __forceinline__ void store_low(const LowArgs& a, uint32_t row, uint32_t col,
+__device__ __forceinline__ void store_low(const LowArgs& a, uint32_t pos, uint32_t col,
                                           const floatx4& v) {
-  if (a.low_) *gp<floatx4>(a.low_ + ((size_t)row * a.R + col) * 4) = v;
+  if (a.low_) *gp<floatx4>(a.low_ + ((size_t)pos * a.R + col) * 4) = v;
   if (a.parts_) {
     const uint2v hi = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
     const uint2v lo = {
         pack_bf16x2(v[0] - bf16_to_f32(hi.x & 0xffffu), v[1] - bf16_to_f32(hi.x >> 16)),
         pack_bf16x2(v[2] - bf16_to_f32(hi.y & 0xffffu), v[3] - bf16_to_f32(hi.y >> 16))};
-    RLD_GLOBAL uint16_t* p = gp<uint16_t>(a.parts_) + (size_t)row * 2 * a.R + col;
+    RLD_GLOBAL uint16_t* p = gp<uint16_t>(a.parts_) + (size_t)pos * 2 * a.R + col;
     *reinterpret_cast<RLD_GLOBAL uint2v*>(p) = hi;
     *reinterpret_cast<RLD_GLOBAL uint2v*>(p + a.R) = lo;
   }
 }
 
-// One block: 64 rows, one k chunk, every nz-th of the distinct slots that the
-// rows name.  The x fragments stay in registers over the slots; each wave
+typedef floatx4 LowSmem[2][4][4][kWave];
+
+// One item: 64 positions, one k chunk, every nz-th of the distinct slots that
+// they name.  The x fragments stay in registers over the slots; each wave
 // contracts every fourth 32-wide step and the four sums meet in LDS.
 // TRANS: the matrix is [K][R] (B_s) instead of [R][K] (A_s).
 template <bool TRANS>
-__global__ void __launch_bounds__(256) low_kernel(LowArgs a) {
-  __shared__ floatx4 red[2][4][4][kWave];
+__device__ __forceinline__ void low_item(const LowArgs& a, uint32_t item, LowSmem& red) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, c = lane & 15;
-  const uint32_t tiles = div_ceil_dev(a.n, kLowRows);
-  const uint32_t tile = blockIdx.x % tiles, ch = blockIdx.x / tiles % a.nch;
-  const uint32_t z = blockIdx.x / (tiles * a.nch);
-  const uint32_t row0 = tile * kLowRows;
+  const uint32_t tile = item % a.tiles, ch = item / a.tiles % a.nch;
+  const uint32_t z = item / (a.tiles * a.nch);
+  const uint32_t pos0 = tile * kLowRows;
   const uint32_t kb = ch * kLowChunk, ke = min(kb + kLowChunk, a.K);
 
-  const RLD_GLOBAL int32_t* seq = gp<const int32_t>(a.seq_);
-  const uint32_t myrow = row0 + lane;
-  const int key = myrow < a.n ? seq[myrow] : -1;
+  const int key = pos0 + lane < a.n ? gp<const int32_t>(a.key_)[pos0 + lane] : -1;
   uint64_t left = __ballot(key >= 0 && (uint32_t)key < a.max_loras);
   if (!left) return;
 
   uint4 xf[4][4];
 #pragma unroll
   for (int mi = 0; mi < 4; ++mi) {
-    const uint32_t row = row0 + mi * 16 + c;
-    const RLD_GLOBAL uint16_t* xr = gp<const uint16_t>(a.x_) + (size_t)min(row, a.n - 1) * a.xs;
+    const uint32_t pos = pos0 + mi * 16 + c;
+    const uint32_t at = min(pos, a.n - 1);
+    const uint32_t row = a.order_ ? (uint32_t)gp<const int32_t>(a.order_)[at] : at;
+    const RLD_GLOBAL uint16_t* xr = gp<const uint16_t>(a.x_) + (size_t)row * a.xs;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t k = kb + (wave + 4 * i) * 32 + g * 8;
-      xf[mi][i] = (row < a.n && k < ke) ? load16(xr + k) : zero16();
+      xf[mi][i] = (pos < a.n && k < ke) ? load16(xr + k) : zero16();
     }
   }
 
@@ -145,7 +252,7 @@ __global__ void __launch_bounds__(256) low_kernel(LowArgs a) {
 #pragma unroll
       for (int mi = 0; mi < 4; ++mi) red[buf][wave][mi][lane] = acc[mi];
       __syncthreads();
-      // wave w finishes rows 16w .. 16w+15: lane (g, c) holds columns 4g.. of row c
+      // wave w finishes positions 16w .. 16w+15: lane (g, c) holds columns 4g.. of c
       floatx4 sum = red[buf][0][wave][lane];
 #pragma unroll
       for (int v = 1; v < 4; ++v) sum += red[buf][v][wave][lane];
@@ -153,40 +260,53 @@ __global__ void __launch_bounds__(256) low_kernel(LowArgs a) {
       const int lr = wave * 16 + c;
       const uint32_t col = j0 + 4 * g;
       if (((mine >> lr) & 1) && col < a.R) {
-        if (a.nch == 1)
-          store_low(a, row0 + lr, col, sum * gp<const float>(a.stab_)[s]);
+        if (a.nch == 1 && !a.partial_)
+          store_low(a, pos0 + lr, col, sum * gp<const float>(a.stab_)[s]);
         else
-          *gp<floatx4>(a.partial_ + (((size_t)ch * a.n + row0 + lr) * a.R + col) * 4) = sum;
+          *gp<floatx4>(a.partial_ + (((size_t)ch * a.n + pos0 + lr) * a.R + col) * 4) = sum;
       }
     }
   }
 }
 
-__device__ __forceinline__ bool low_active(const LowArgs& a, int s) {
-  if (s < 0 || (uint32_t)s >= a.max_loras) return false;
-  const uint64_t t = gp<const uint64_t>(a.mtab_)[s], o = gp<const uint64_t>(a.otab_)[s];
-  return t != 0ull && o != 0ull;
+__global__ void __launch_bounds__(256) low_kernel(LowArgs a) {
+  __shared__ LowSmem red;
+  low_item<false>(a, blockIdx.x, red);
 }
 
-// low[i] = scale_s * (the chunks' sums in chunk order), routed rows only.
-__global__ void __launch_bounds__(256) low_reduce_kernel(LowArgs a) {
+// u = x A^T and g = dy B in one launch: the first `items` blocks make u.
+__global__ void __launch_bounds__(256) low_pair_kernel(LowArgs u, LowArgs gr, uint32_t items) {
+  __shared__ LowSmem red;
+  if (blockIdx.x < items) low_item<false>(u, blockIdx.x, red);
+  else low_item<true>(gr, blockIdx.x - items, red);
+}
+
+// low[p] = scale_s * (the chunks' sums in chunk order), routed rows only.
+__device__ __forceinline__ void low_sum(const LowArgs& a, uint32_t block) {
   const uint32_t q = a.R / 4;
-  const uint64_t t = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+  const uint64_t t = (uint64_t)block * 256 + threadIdx.x;
   if (t >= (uint64_t)a.n * q) return;
-  const uint32_t row = (uint32_t)(t / q);
-  const int s = gp<const int32_t>(a.seq_)[row];
-  if (!low_active(a, s)) return;
+  const uint32_t pos = (uint32_t)(t / q);
+  const int s = gp<const int32_t>(a.key_)[pos];
+  if (s < 0) return;
   floatx4 sum = {};
   for (uint32_t ch = 0; ch < a.nch; ++ch)
     sum += gp<const floatx4>(a.partial_)[(size_t)ch * a.n * q + t];
-  store_low(a, row, (uint32_t)(t % q) * 4, sum * gp<const float>(a.stab_)[s]);
+  store_low(a, pos, (uint32_t)(t % q) * 4, sum * gp<const float>(a.stab_)[s]);
+}
+
+__global__ void __launch_bounds__(256) low_reduce_kernel(LowArgs u, LowArgs gr, uint32_t blocks) {
+  if (blockIdx.x < blocks) low_sum(u, blockIdx.x);
+  else low_sum(gr, blockIdx.x - blocks);
 }
 
 // ------------------------------------------------------------------- tile ----
 
 struct TileArgs {
-  uint64_t x_, w_, out_, seq_, parts_, etab_, otab_;
-  uint32_t xs, ws, os, n, K, N, R, max_loras, tiles_m, tiles_n;
+  uint64_t x_, w_, out_, parts_, etab_;
+  uint64_t order_, skey_;  // by sorted position
+  uint32_t xs, ws, os, n, K, N, R, tiles_m, tiles_n;
+  uint32_t keep;  // rows in their own order: offsets are taken from a tile's first row
 };
 
 // Until at most N of this wave's loads and stores are in flight.
@@ -199,6 +319,11 @@ typedef int rsrc_t __attribute__((ext_vector_type(4)));
 
 // The size of the largest buffer, and so an offset behind every buffer.
 constexpr uint32_t kBufferEnd = 0x7ffffff0u;
+// Operands of a tile's product span at most 2^30 + 2^26 bytes from their base
+// (rows are kept in their own order where a batch spans more): an offset that is
+// behind them, also with the offset of a k step or another such offset added.
+constexpr uint32_t kOutside = 0x60000000u;
+constexpr uint64_t kGatherSpan = 1ull << 30;
 
 // A raw buffer of `bytes` at `base`, uniform over the wave:
 // a lane whose offset lies past it reads zeros.
@@ -223,6 +348,10 @@ __device__ __forceinline__ void dma16(const rsrc_t& r, uint32_t to, uint32_t vof
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(RLD_LDS const void*)p;
+}
+
+__device__ __forceinline__ RLD_LDS unsigned char* lds_at(uint32_t a) {
+  return (RLD_LDS unsigned char*)(uintptr_t)a;
 }
 
 __device__ __forceinline__ uint4 lds16(const RLD_LDS unsigned char* p) {
@@ -271,7 +400,8 @@ __device__ __forceinline__ void k_tail(const TileArgs& a, uint32_t k0, floatx4 (
                                        const uint32_t (&cols_at)[NI]) {
   const int lane = threadIdx.x & 63;
   const uint32_t rows = a.n - row0, cols = a.N - col0;
-  const uint64_t x = a.x_ + (uint64_t)row0 * a.xs * 2;
+  const uint32_t first = a.keep ? row0 : 0u;
+  const uint64_t x = a.x_ + (uint64_t)first * a.xs * 2;
   for (; k0 < a.K; k0 += 32) {
     int tl = lane;  // offsets are computed here, not before the loop and held
     asm volatile("" : "+v"(tl));
@@ -298,8 +428,9 @@ __device__ __forceinline__ void k_tail(const TileArgs& a, uint32_t k0, floatx4 (
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
       const uint32_t r = rows_at[mi] + c;
+      const uint32_t o = (uint32_t)gp<const int32_t>(a.order_)[row0 + min(r, rows - 1)] - first;
       const uint4 xf = buffer_load16(x, kBufferEnd,
-                                     (k < a.K && r < rows) ? (r * a.xs + k) * 2 : kBufferEnd);
+                                     (k < a.K && r < rows) ? (o * a.xs + k) * 2 : kBufferEnd);
 #pragma unroll
       for (int ni = 0; ni < NI; ++ni) acc[ni][mi] = mfma_bf16_16x16x32(wf[ni], xf, acc[ni][mi]);
       if (mi % 4 == 3) issue_point();
@@ -313,116 +444,144 @@ __device__ __forceinline__ uint64_t uniform64(uint64_t v) {
          (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) << 32;
 }
 
-// What follows a tile's main product: the low-rank part and the store.
-// acc[ni][mi] holds the 16 x 16 block of rows row0 + rows_at[mi] .. and columns
-// col0 + cols_at[ni] .. , transposed: lane (g, c) has columns 4g .. 4g + 3 of
-// row c.  No branch touches the accumulators (they fill the registers): every
-// slot of the wave's rows goes through all row blocks, with zeros for the rows
-// of other slots, which then leave its product out (a NaN or infinity of its
-// matrix would survive the zeros).
+// acc[ni][mi] of a wave holds the 16 x 16 block of positions row0 + rows_at[mi] ..
+// and columns col0 + cols_at[ni] .. , transposed: lane (g, c) has columns
+// 4g .. 4g + 3 of position c.
+
+// The rounded outputs to their rows.
+template <int MI, int NI>
+__device__ __forceinline__ void store_tile(const TileArgs& a, const floatx4 (&acc)[NI][MI],
+                                           uint32_t row0, uint32_t col0,
+                                           const uint32_t (&rows_at)[MI],
+                                           const uint32_t (&cols_at)[NI]) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t rows = a.n - row0, cols = a.N - col0;
+  const uint32_t first = a.keep ? row0 : 0u;
+  const uint64_t out = a.out_ + ((uint64_t)first * a.os + col0) * 2;
+  uint32_t at[MI];
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) {
+    const uint32_t r = rows_at[mi] + (lane & 15);
+    at[mi] = (uint32_t)gp<const int32_t>(a.order_)[row0 + min(r, rows - 1)] - first;
+  }
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) {
+    int tl = lane;  // offsets are computed here, not ahead and held
+    asm volatile("" : "+v"(tl));
+    const uint32_t r = rows_at[mi] + (tl & 15);
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) {
+      const uint32_t col = cols_at[ni] + 4 * (tl >> 4);
+      const floatx4 v = acc[ni][mi];
+      buffer_store8(out, kBufferEnd,
+                    (r < rows && col < cols) ? (at[mi] * a.os + col) * 2 : kBufferEnd,
+                    uint2v{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])});
+    }
+    issue_point();
+  }
+}
+
+// The low-rank part of the smaller tiles: every slot that the wave's rows name
+// goes through all its row blocks, with zeros for the rows of other slots,
+// which then leave its product out (a NaN or infinity of its matrix would
+// survive the zeros).  The operands of the next 32 of rank are loaded while
+// the current ones multiply.
 template <int MI, int NI, bool TRANS>
-__device__ __forceinline__ void finish_tile(const TileArgs& a, floatx4 (&acc)[NI][MI],
-                                            uint32_t row0, uint32_t col0,
-                                            const uint32_t (&rows_at)[MI],
-                                            const uint32_t (&cols_at)[NI]) {
-  constexpr int MH = MI < 4 ? MI : 4;  // row blocks whose low rows are held at once
+__device__ __forceinline__ void add_low(const TileArgs& a, floatx4 (&acc)[NI][MI], uint32_t row0,
+                                        uint32_t col0, const uint32_t (&rows_at)[MI],
+                                        const uint32_t (&cols_at)[NI]) {
   const int lane = threadIdx.x & 63;
   const int g = lane >> 4, c = lane & 15;
-  const uint32_t rows = a.n - row0, cols = a.N - col0;  // at least one tile's, or up to the end
-
-  int key[MI];  // the slot of a routed row, -1 for base rows and rows done
+  const uint32_t rows = a.n - row0, cols = a.N - col0;
+  const uint32_t R = a.R;
+  int key[MI], left[MI];
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
     const uint32_t r = rows_at[mi] + c;
-    int k = r < rows ? gp<const int32_t>(a.seq_)[row0 + r] : -1;
-    if (k < 0 || (uint32_t)k >= a.max_loras) k = -1;
-    const uint64_t e = gp<const uint64_t>(a.etab_)[k < 0 ? 0 : k];
-    const uint64_t o = gp<const uint64_t>(a.otab_)[k < 0 ? 0 : k];
-    key[mi] = (e != 0ull && o != 0ull) ? k : -1;
+    key[mi] = r < rows ? gp<const int32_t>(a.skey_)[row0 + r] : -1;
+    left[mi] = key[mi];
   }
-  const uint64_t low = a.parts_ + (uint64_t)row0 * a.R * 4;
-  const uint32_t R = a.R;
-  int s = -1;
-  uint64_t et = 0;
-  for (uint32_t k0 = R;; k0 += 32) {
-    if (k0 >= R) {  // on to the first slot that is left
-      int first = -1;
+  const uint64_t low = a.parts_ + (uint64_t)row0 * R * 4;
+
+  struct Step {
+    int s;
+    uint32_t k0;
+    uint64_t e;
+  };
+  // On to the next 32 of rank, or to the first slot that is left; false: done.
+  auto next = [&](Step& st) {
+    st.k0 += 32;
+    if (st.k0 < R) return true;
+    int first = -1;
 #pragma unroll
-      for (int mi = 0; mi < MI; ++mi) {
-        key[mi] = key[mi] == s ? -1 : key[mi];
-        first = first < 0 ? key[mi] : first;
-      }
-      const uint64_t m = __ballot(first >= 0);
-      if (!m) break;
-      s = __builtin_amdgcn_readlane(first, __builtin_ctzll(m));
-      et = uniform64(gp<const uint64_t>(a.etab_)[s]);
-      k0 = 0;
-    }
-    // the lane through an empty asm: offsets are computed here, not before the
-    // loop and held
-    int tl = lane;
-    asm volatile("" : "+v"(tl));
-    const int g = tl >> 4, c = tl & 15;
-    const uint32_t k = k0 + 8 * g;
-    uint4 ef[NI];
+    for (int mi = 0; mi < MI; ++mi) first = first < 0 ? left[mi] : first;
+    const uint64_t m = __ballot(first >= 0);
+    if (!m) return false;
+    st.s = __builtin_amdgcn_readlane(first, __builtin_ctzll(m));
+    st.e = uniform64(gp<const uint64_t>(a.etab_)[st.s]);
+    st.k0 = 0;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) left[mi] = left[mi] == st.s ? -1 : left[mi];
+    return true;
+  };
+  struct Operands {
+    uint4 e[NI], hi[MI], lo[MI];
+  };
+  auto load = [&](const Step& st, Operands& o) {
+    const uint32_t k = st.k0 + 8 * g;
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) {
       const uint32_t col = cols_at[ni] + c;
       const bool in = k < R && col < cols;
       if constexpr (!TRANS) {
-        ef[ni] = buffer_load16(et + (uint64_t)col0 * R * 2, kBufferEnd,
-                               in ? (col * R + k) * 2 : kBufferEnd);
+        o.e[ni] = buffer_load16(st.e + (uint64_t)col0 * R * 2, kBufferEnd,
+                                in ? (col * R + k) * 2 : kBufferEnd);
       } else {
         uint32_t e[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          e[q] = buffer_load2(et + ((uint64_t)(k0 + q) * a.N + col0) * 2, kBufferEnd,
+          e[q] = buffer_load2(st.e + ((uint64_t)(st.k0 + q) * a.N + col0) * 2, kBufferEnd,
                               in ? 16 * g * a.N + col * 2 : kBufferEnd);
-        ef[ni] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16,
-                            e[6] | e[7] << 16);
+        o.e[ni] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16,
+                             e[6] | e[7] << 16);
       }
     }
 #pragma unroll
-    for (int h = 0; h < MI; h += MH) {
-      uint4 hi[MH], lo[MH];
-#pragma unroll
-      for (int mi = 0; mi < MH; ++mi) {
-        const uint32_t at = (rows_at[h + mi] + c) * R * 4 + k * 2;
-        const uint32_t off = (key[h + mi] == s && k < R) ? at : kBufferEnd;
-        hi[mi] = buffer_load16(low, kBufferEnd, off);
-        lo[mi] = buffer_load16(low + R * 2, kBufferEnd, off);
-      }
-#pragma unroll
-      for (int mi = 0; mi < MH; ++mi) {
-        const bool mine = key[h + mi] == s;
-#pragma unroll
-        for (int ni = 0; ni < NI; ++ni) {
-          floatx4 t = mfma_bf16_16x16x32(ef[ni], lo[mi], floatx4{0.f, 0.f, 0.f, 0.f});
-          t = mfma_bf16_16x16x32(ef[ni], hi[mi], t);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[ni][h + mi][i] += mine ? t[i] : 0.f;
-        }
-      }
-      issue_point();
+    for (int mi = 0; mi < MI; ++mi) {
+      const uint32_t off = (key[mi] == st.s && k < R) ? (rows_at[mi] + c) * R * 4 + k * 2
+                                                      : kBufferEnd;
+      o.hi[mi] = buffer_load16(low, kBufferEnd, off);
+      o.lo[mi] = buffer_load16(low + R * 2, kBufferEnd, off);
     }
-  }
-
-  const uint64_t out = a.out_ + ((uint64_t)row0 * a.os + col0) * 2;
+  };
+  auto multiply = [&](const Step& st, const Operands& o) {
 #pragma unroll
-  for (int mi = 0; mi < MI; ++mi) {
-    int tl = lane;
-    asm volatile("" : "+v"(tl));
-    const int g = tl >> 4, c = tl & 15;
-    const uint32_t r = rows_at[mi] + c;
-    const uint32_t at = r * a.os * 2;
+    for (int mi = 0; mi < MI; ++mi) {
+      const bool mine = key[mi] == st.s;
 #pragma unroll
-    for (int ni = 0; ni < NI; ++ni) {
-      const uint32_t col = cols_at[ni] + 4 * g;
-      const floatx4 v = acc[ni][mi];
-      buffer_store8(out, kBufferEnd, (r < rows && col < cols) ? at + col * 2 : kBufferEnd,
-                    uint2v{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])});
+      for (int ni = 0; ni < NI; ++ni) {
+        floatx4 t = mfma_bf16_16x16x32(o.e[ni], o.lo[mi], floatx4{0.f, 0.f, 0.f, 0.f});
+        t = mfma_bf16_16x16x32(o.e[ni], o.hi[mi], t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[ni][mi][i] += mine ? t[i] : 0.f;
+      }
     }
-    issue_point();
+  };
+  Step sa = {-1, R, 0}, sb;
+  Operands oa, ob;
+  if (!next(sa)) return;
+  load(sa, oa);
+  for (;;) {
+    sb = sa;
+    const bool more = next(sb);
+    if (more) load(sb, ob);
+    multiply(sa, oa);
+    if (!more) return;
+    sa = sb;
+    const bool again = next(sa);
+    if (again) load(sa, oa);
+    multiply(sb, ob);
+    if (!again) return;
   }
 }
 
@@ -450,9 +609,10 @@ __device__ __forceinline__ void tile_body(const TileArgs& a) {
   const uint32_t tm = blockIdx.x % a.tiles_m, tn = blockIdx.x / a.tiles_m;
   const uint32_t row0 = tm * BM, col0 = tn * BN;
   const uint32_t rows = min((uint32_t)BM, a.n - row0);
+  const uint32_t first = a.keep ? row0 : 0u;
 
-  const rsrc_t rx = buffer(a.x_ + (uint64_t)row0 * a.xs * 2,
-                           ((uint64_t)(rows - 1) * a.xs + a.K) * 2);
+  const rsrc_t rx = buffer(a.x_ + (uint64_t)first * a.xs * 2,
+                           ((uint64_t)((a.keep ? rows : a.n) - 1) * a.xs + a.K) * 2);
   const uint32_t wrows = min((uint32_t)BN, a.N - col0);
   const rsrc_t rw0 = buffer(a.w_ + (uint64_t)col0 * a.ws * 2,
                             ((uint64_t)(wrows - 1) * a.ws + a.K) * 2);
@@ -461,7 +621,8 @@ __device__ __forceinline__ void tile_body(const TileArgs& a) {
 #pragma unroll
   for (int p = 0; p < PA; ++p) {
     const uint32_t r = (wave * PA + p) * 8 + (lane >> 3);
-    va[p] = r * a.xs * 2 + (((lane & 7) ^ ((r >> 1) & 7)) * 16);
+    const uint32_t o = (uint32_t)gp<const int32_t>(a.order_)[row0 + min(r, rows - 1)] - first;
+    va[p] = r < rows ? o * a.xs * 2 + (((lane & 7) ^ ((r >> 1) & 7)) * 16) : kOutside;
   }
 #pragma unroll
   for (int p = 0; p < PB; ++p) {
@@ -488,7 +649,7 @@ __device__ __forceinline__ void tile_body(const TileArgs& a) {
       if (tail) {
         const uint32_t r = (wave * PA + p) * 8 + (lane >> 3);
         const uint32_t k = k0 + (((lane & 7) ^ ((r >> 1) & 7)) * 8);
-        if (k >= a.K) v = kBufferEnd;
+        if (k >= a.K) v = kOutside;
       }
       dma16(rx, st + (wave * PA + p) * 1024, v, k0 * 2);
     }
@@ -499,7 +660,7 @@ __device__ __forceinline__ void tile_body(const TileArgs& a) {
         if (tail) {
           const uint32_t r = (wave * PB + p) * 8 + (lane >> 3);
           const uint32_t k = k0 + (((lane & 7) ^ ((r >> 1) & 7)) * 8);
-          if (k >= a.K) v = kBufferEnd;
+          if (k >= a.K) v = kOutside;
         }
         dma16(rw0, st + BM * 128 + (wave * PB + p) * 1024, v, k0 * 2);
       }
@@ -567,7 +728,8 @@ __device__ __forceinline__ void tile_body(const TileArgs& a) {
   for (int mi = 0; mi < MI; ++mi) rows_at[mi] = (wr * MI + mi) * 16;
 #pragma unroll
   for (int ni = 0; ni < NI; ++ni) cols_at[ni] = (wc * NI + ni) * 16;
-  finish_tile<MI, NI, TRANS>(a, acc, row0, col0, rows_at, cols_at);
+  add_low<MI, NI, TRANS>(a, acc, row0, col0, rows_at, cols_at);
+  store_tile<MI, NI>(a, acc, row0, col0, rows_at, cols_at);
 }
 
 template <int BM, int BN, int WR, int WC, int STAGES, bool TRANS>
@@ -613,10 +775,17 @@ __device__ __forceinline__ void big_tile_body(const TileArgs& a) {
   const uint32_t row0 = (patch * 4 + in % high) * 256, col0 = in / high * 256;
 
   const uint32_t rows = min(256u, a.n - row0), cols = min(256u, a.N - col0);
-  const rsrc_t rx =
-      buffer(a.x_ + (uint64_t)row0 * a.xs * 2, ((uint64_t)(rows - 1) * a.xs + a.K) * 2);
+  const uint32_t first = a.keep ? row0 : 0u;
+  const rsrc_t rx = buffer(a.x_ + (uint64_t)first * a.xs * 2,
+                           ((uint64_t)((a.keep ? rows : a.n) - 1) * a.xs + a.K) * 2);
   const rsrc_t rw0 =
       buffer(a.w_ + (uint64_t)col0 * a.ws * 2, ((uint64_t)(cols - 1) * a.ws + a.K) * 2);
+  // The slot of the first row: its low rows and second matrix are loaded as if
+  // they were steps behind K (a scalar load, the same for the whole block).
+  const int slot0 = *(const RLD_CONST int*)(a.skey_ + (uint64_t)row0 * 4);
+  uint64_t e0 = 0;
+  if (slot0 >= 0) e0 = *(const RLD_CONST uint64_t*)(a.etab_ + (uint64_t)slot0 * 8);
+
   uint32_t vx[2][2], vw[2][2];  // [half][load]
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
@@ -624,7 +793,9 @@ __device__ __forceinline__ void big_tile_body(const TileArgs& a) {
     const uint32_t q = (lane & 7) ^ ((r >> 1) & 7);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      vx[h][p] = (h * 128 + r) * a.xs * 2 + q * 16;
+      const uint32_t hr = h * 128 + r;
+      const uint32_t o = (uint32_t)gp<const int32_t>(a.order_)[row0 + min(hr, rows - 1)] - first;
+      vx[h][p] = hr < rows ? o * a.xs * 2 + q * 16 : kOutside;
       if constexpr (!TRANS) {
         vw[h][p] = (h * 128 + r) * a.ws * 2 + q * 16;
       } else {
@@ -636,30 +807,68 @@ __device__ __forceinline__ void big_tile_body(const TileArgs& a) {
     }
   }
   // Whole steps; the last K % 64 are added from global memory after the loop.
-  // Loads of steps past the end are sent behind the buffers' ends.
-  const uint32_t nk = a.K / 64;
+  // Steps go in pairs: with an odd number, step 0 has operands of zeros.
+  const uint32_t nk = a.K / 64, odd = nk & 1, steps = nk + odd;
   const uint32_t lds0 = lds_addr(lds);
   const uint32_t put = lds0 + wave * 2048;
   // places of the halves in a step's 64 KB: X0, X1, W0, W1
-  auto load_x = [&](int h, uint32_t kt, int buf) {
-    const uint32_t at = kt < nk ? kt * 128 : 0x7f000000u;
+  auto load_x = [&](int h, uint32_t t, int buf) {
+    const uint32_t at = t < odd ? kOutside : (t - odd) * 128;
 #pragma unroll
     for (int p = 0; p < 2; ++p)
       dma16(rx, put + buf * 65536 + h * 16384 + p * 1024, vx[h][p], at);
   };
-  auto load_w = [&](int h, uint32_t kt, int buf) {
+  auto load_w = [&](int h, uint32_t t, int buf) {
     const uint32_t to = put + buf * 65536 + 32768 + h * 16384;
     if constexpr (TRANS) {
-      const uint32_t k0 = kt < nk ? kt * 64 : 0;
+      const uint32_t k0 = t < odd ? 0 : (t - odd) * 64;
       const rsrc_t rw =
           buffer(a.w_ + ((uint64_t)k0 * a.ws + col0) * 2,
-                 kt < nk ? ((uint64_t)(a.K - k0 - 1) * a.ws + a.N - col0) * 2 : 0);
+                 t < odd ? 0 : ((uint64_t)(a.K - k0 - 1) * a.ws + a.N - col0) * 2);
 #pragma unroll
       for (int p = 0; p < 2; ++p) dma16(rw, to + p * 1024, vw[h][p], 0);
     } else {
-      const uint32_t at = kt < nk ? kt * 128 : 0x7f000000u;
+      const uint32_t at = t < odd ? kOutside : (t - odd) * 128;
 #pragma unroll
       for (int p = 0; p < 2; ++p) dma16(rw0, to + p * 1024, vw[h][p], at);
+    }
+  };
+  // Low operands, 64 of rank from k0: half h of the rows' part `lo` (0 or 1) into
+  // the X places, half h of a slot's second matrix into the W places.
+  const rsrc_t rlow = buffer(a.parts_ + (uint64_t)row0 * a.R * 4, (uint64_t)rows * a.R * 4);
+  auto load_low = [&](int h, int lo, uint32_t k0, int buf) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const uint32_t r = (wave * 2 + p) * 8 + (lane >> 3);
+      const uint32_t k = k0 + ((lane & 7) ^ ((r >> 1) & 7)) * 8;
+      dma16(rlow, put + buf * 65536 + h * 16384 + p * 1024,
+            k < a.R ? ((h * 128 + r) * 2 + lo) * a.R * 2 + k * 2 : kOutside, 0);
+    }
+  };
+  auto load_e = [&](int h, uint64_t e, uint32_t k0, int buf) {
+    const uint32_t to = put + buf * 65536 + 32768 + h * 16384;
+    if constexpr (TRANS) {
+      const rsrc_t re =
+          buffer(e + ((uint64_t)k0 * a.N + col0) * 2,
+                 e == 0 || k0 >= a.R ? 0 : ((uint64_t)(a.R - k0 - 1) * a.N + a.N - col0) * 2);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const uint32_t k = (wave * 2 + p) * 4 + (lane >> 4);
+        const uint32_t sw = ((k & 3) | ((k >> 3) & 3) << 2) & 7;
+        const uint32_t slot = lane & 15;
+        dma16(re, to + p * 1024,
+              k0 + k < a.R ? k * a.N * 2 + h * 256 + (((slot >> 1) ^ sw) * 2 + (slot & 1)) * 16
+                           : kOutside, 0);
+      }
+    } else {
+      const rsrc_t re = buffer(e + (uint64_t)col0 * a.R * 2,
+                               e == 0 ? 0 : (uint64_t)cols * a.R * 2);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const uint32_t r = (wave * 2 + p) * 8 + (lane >> 3);
+        const uint32_t k = k0 + ((lane & 7) ^ ((r >> 1) & 7)) * 8;
+        dma16(re, to + p * 1024, k < a.R ? (h * 128 + r) * a.R * 2 + k * 2 : kOutside, 0);
+      }
     }
   };
 
@@ -672,7 +881,7 @@ __device__ __forceinline__ void big_tile_body(const TileArgs& a) {
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       const RLD_LDS unsigned char* st =
-          (const RLD_LDS unsigned char*)((gx ^ (ks * 64)) + buf * 65536);
+          lds_at((gx ^ (ks * 64)) + buf * 65536);
 #pragma unroll
       for (int mi = 0; mi < 4; ++mi) xf[ks][mi] = lds16(st + h * 16384 + mi * 2048);
     }
@@ -684,11 +893,11 @@ __device__ __forceinline__ void big_tile_body(const TileArgs& a) {
       for (int ni = 0; ni < 2; ++ni) {
         if constexpr (!TRANS) {
           const RLD_LDS unsigned char* st =
-              (const RLD_LDS unsigned char*)((gw ^ (ks * 64)) + buf * 65536);
+              lds_at((gw ^ (ks * 64)) + buf * 65536);
           f[ks][ni] = lds16(st + h * 16384 + ni * 2048);
         } else {
           RLD_LDS unsigned char* st =
-              (RLD_LDS unsigned char*)(tw + ((wc * 2 + ni) ^ tsw) * 32 + buf * 65536);
+              lds_at(tw + ((wc * 2 + ni) ^ tsw) * 32 + buf * 65536);
           f[ks][ni] = lds_tr16(st + h * 16384 + ks * 8192, 1024);
         }
       }
@@ -724,54 +933,67 @@ __device__ __forceinline__ void big_tile_body(const TileArgs& a) {
     __builtin_amdgcn_sched_barrier(0);
   };
   // One step from buffer `buf`: w0 holds W0 of this step, w0next gets the next's.
-  auto step = [&](uint32_t kt, int buf, uint4 (&w0)[2][2], uint4 (&w0next)[2][2]) {
+  // LAST: behind this step come no more of K; the loads are the low operands.
+  auto step = [&](auto last, uint32_t t, int buf, uint4 (&w0)[2][2], uint4 (&w0next)[2][2]) {
+    constexpr bool LAST = decltype(last)::value;
     read_x(0, buf);
-    load_w(0, kt + 2, buf);
+    LAST ? load_e(0, e0, 0, buf) : load_w(0, t + 2, buf);
     settle();
     multiply(0, 0, w0);
     meet();
     read_w(1, buf, wf[1]);
-    load_x(0, kt + 2, buf);
+    LAST ? load_low(0, buf, 0, buf) : load_x(0, t + 2, buf);
     settle();
     multiply(0, 1, wf[1]);
     meet();
     read_x(1, buf);
-    load_w(1, kt + 2, buf);
+    LAST ? load_e(1, e0, 0, buf) : load_w(1, t + 2, buf);
     settle();
     multiply(1, 1, wf[1]);
     meet();
     read_w(0, buf ^ 1, w0next);
-    load_x(1, kt + 2, buf);
+    LAST ? load_low(1, buf, 0, buf) : load_x(1, t + 2, buf);
     settle();
     multiply(1, 0, w0);
     meet();
   };
 
+  if (steps) {
 #pragma unroll
-  for (int kt = 0; kt < 2; ++kt) {
-    load_w(0, kt, kt);
-    load_x(0, kt, kt);
-    load_w(1, kt, kt);
-    load_x(1, kt, kt);
+    for (int t = 0; t < 2; ++t) {
+      load_w(0, t, t);
+      load_x(0, t, t);
+      load_w(1, t, t);
+      load_x(1, t, t);
+    }
+    asm volatile("s_waitcnt vmcnt(12)" ::: "memory");  // W0 and X0 of step 0
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    read_w(0, 0, wf[0]);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    if (wave >= 4) __builtin_amdgcn_s_barrier();  // half a phase behind
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    uint32_t t = 0;
+    for (; t + 2 < steps; t += 2) {
+      step(std::false_type{}, t, 0, wf[0], w0n);
+      step(std::false_type{}, t + 1, 1, w0n, wf[0]);
+    }
+    step(std::true_type{}, t, 0, wf[0], w0n);
+    step(std::true_type{}, t + 1, 1, w0n, wf[0]);
+    if (wave < 4) __builtin_amdgcn_s_barrier();  // as many barriers as the others
+  } else {
+    load_e(0, e0, 0, 0);
+    load_e(1, e0, 0, 0);
+#pragma unroll
+    for (int lo = 0; lo < 2; ++lo) {
+      load_low(0, lo, 0, lo);
+      load_low(1, lo, 0, lo);
+    }
   }
-  asm volatile("s_waitcnt vmcnt(12)" ::: "memory");  // W0 and X0 of step 0
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  read_w(0, 0, wf[0]);
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-  if (wave >= 4) __builtin_amdgcn_s_barrier();  // half a phase behind
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-  // steps in pairs; past the last the operands are zeros
-  for (uint32_t kt = 0; kt < nk; kt += 2) {
-    step(kt, 0, wf[0], w0n);
-    step(kt + 1, 1, w0n, wf[0]);
-  }
-  if (wave < 4) __builtin_amdgcn_s_barrier();  // as many barriers as the others
-  wait_vm<0>();
 
   uint32_t rows_at[8], cols_at[4];
 #pragma unroll
@@ -781,7 +1003,109 @@ __device__ __forceinline__ void big_tile_body(const TileArgs& a) {
   for (int ni = 0; ni < 4; ++ni)
     cols_at[ni] = (ni >> 1) * 128 + wc * 32 + (ni & 1) * 16;
   k_tail<8, 4, TRANS>(a, nk * 64, acc, row0, col0, rows_at, cols_at);
-  finish_tile<8, 4, TRANS>(a, acc, row0, col0, rows_at, cols_at);
+
+  // The low-rank part.  The rows' first parts lie in the X places of buffer 0,
+  // their second parts in buffer 1's; the slots' matrices take turns in the two
+  // W places.  A slot's product is made apart and added to its own rows alone
+  // (a NaN or infinity of its matrix would survive zeros in the others).
+  int key[8], left[4];
+#pragma unroll
+  for (int mi = 0; mi < 8; ++mi) {
+    const uint32_t r = rows_at[mi] + c;
+    key[mi] = r < rows ? gp<const int32_t>(a.skey_)[row0 + r] : -1;
+  }
+  auto all_rows = [&]() {  // the tile's slots, in every wave alike
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t r = j * 64 + lane;
+      left[j] = r < rows ? gp<const int32_t>(a.skey_)[row0 + r] : -1;
+    }
+  };
+  auto next_slot = [&]() {
+    int s = -1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t m = __ballot(left[j] >= 0);
+      const int first_j = __builtin_amdgcn_readlane(left[j], m ? __builtin_ctzll(m) : 0);
+      s = (s < 0 && m) ? first_j : s;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) left[j] = left[j] == s ? -1 : left[j];
+    return s;
+  };
+  auto landed = [&]() {  // this wave's loads, then everyone's
+    wait_vm<0>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  for (uint32_t k0 = 0; k0 < a.R; k0 += 64) {
+    all_rows();
+    int s = next_slot();
+    if (s < 0) break;
+    if (k0 != 0) {
+      __builtin_amdgcn_s_barrier();  // everyone has read what is overwritten
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int lo = 0; lo < 2; ++lo) {
+        load_low(0, lo, k0, lo);
+        load_low(1, lo, k0, lo);
+      }
+    }
+    if (k0 != 0 || s != slot0) {  // not loaded behind K
+      const uint64_t e = uniform64(gp<const uint64_t>(a.etab_)[s]);
+      if (k0 == 0) landed();  // what was loaded there has landed
+      load_e(0, e, k0, 0);
+      load_e(1, e, k0, 0);
+    }
+    landed();
+    for (int buf = 0; s >= 0; buf ^= 1) {
+      const int following = next_slot();
+      if (following >= 0) {
+        const uint64_t e = uniform64(gp<const uint64_t>(a.etab_)[following]);
+        load_e(0, e, k0, buf ^ 1);
+        load_e(1, e, k0, buf ^ 1);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        bool any = false;
+#pragma unroll
+        for (int mi = 0; mi < 4; ++mi) any |= key[h * 4 + mi] == s;
+        if (__ballot(any) == 0) continue;
+#pragma unroll
+        for (int wh = 0; wh < 2; ++wh) {
+          uint4 ef[2][2];
+          read_w(wh, buf, ef);
+          floatx4 t[2][4];
+#pragma unroll
+          for (int ni = 0; ni < 2; ++ni)
+#pragma unroll
+            for (int mi = 0; mi < 4; ++mi) t[ni][mi] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int lo = 1; lo >= 0; --lo) {
+            read_x(h, lo);
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+              for (int ni = 0; ni < 2; ++ni)
+#pragma unroll
+                for (int mi = 0; mi < 4; ++mi)
+                  t[ni][mi] = mfma_bf16_16x16x32(ef[ks][ni], xf[ks][mi], t[ni][mi]);
+          }
+#pragma unroll
+          for (int ni = 0; ni < 2; ++ni)
+#pragma unroll
+            for (int mi = 0; mi < 4; ++mi)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                acc[wh * 2 + ni][h * 4 + mi][i] += key[h * 4 + mi] == s ? t[ni][mi][i] : 0.f;
+        }
+      }
+      s = following;
+      landed();
+    }
+  }
+  wait_vm<0>();
+  store_tile<8, 4>(a, acc, row0, col0, rows_at, cols_at);
 }
 
 template <bool TRANS>
@@ -789,37 +1113,145 @@ __global__ void __launch_bounds__(512) big_tile_kernel(TileArgs a) {
   big_tile_body<TRANS>(a);
 }
 
-// ------------------------------------------------------------------ lists ----
+// ------------------------------------------------------------------- rows ----
 
-struct ListArgs {
-  uint64_t seq_, atab_, btab_, order_, span_;
-  uint32_t n, max_loras;
+struct RowsArgs {
+  uint64_t x_, w_, out_, seq_, partial_, atab_, btab_, stab_;
+  uint32_t xs, ws, os, n, K, N, R, nch, max_loras;
 };
 
-// One wave per slot: its rows in ascending order at order[span[2s]] ..,
-// span[2s+1] of them.  A slot's rows begin behind those of the slots below
-// it, which the wave counts itself (no wave waits for another).
-__global__ void __launch_bounds__(64) lists_kernel(ListArgs a) {
-  const int s = blockIdx.x, lane = threadIdx.x;
-  const RLD_GLOBAL int32_t* seq = gp<const int32_t>(a.seq_);
-  uint32_t below = 0, cnt = 0;
-  for (uint32_t r0 = 0; r0 < a.n; r0 += 64) {
-    const int key = r0 + lane < a.n ? seq[r0 + lane] : -1;
-    below += __popcll(__ballot(key >= 0 && key < s));
+constexpr int kRowsWaves = 8;
+constexpr uint32_t kRowsMax = 64;  // rows of the calls that take this kernel
+
+// Up to 16 * MI <= 64 rows: a block makes 16 output columns of all of them.  W
+// is read once, straight into fragments (nothing of it is shared); its waves
+// take every eighth pair of 32-wide k steps, so that a wave reads whole cache
+// lines.  While the first loads fly the block adds up the low rows' chunks
+// into LDS; the slots are dealt to the waves, which add their products to
+// their own partial sums, and the eight sums meet in LDS.
+template <int MI>
+__global__ void __launch_bounds__(64 * kRowsWaves) rows_kernel(RowsArgs a) {
+  constexpr int U = MI == 1 ? 8 : 4;  // k steps loaded at once
+  constexpr int kRed = kRowsWaves * MI * kWave * 16;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // kRed, or the low parts
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, c = lane & 15;
+  const uint32_t col0 = blockIdx.x * 16;
+  const uint32_t cols = min(16u, a.N - col0);
+  const uint64_t wb = a.w_ + (uint64_t)col0 * a.ws * 2;
+
+  uint4 wf[U], xf[U][MI], wn[U], xn[U][MI];
+  auto load = [&](uint32_t ks0, uint4 (&w)[U], uint4 (&x)[U][MI]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t k = (ks0 + ((u >> 1) * kRowsWaves + wave) * 2 + (u & 1)) * 32 + g * 8;
+      w[u] = buffer_load16(wb, kBufferEnd,
+                           (k < a.K && (uint32_t)c < cols) ? (c * a.ws + k) * 2 : kBufferEnd);
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) {
+        const uint32_t r = mi * 16 + c;
+        x[u][mi] = buffer_load16(a.x_, kBufferEnd,
+                                 (k < a.K && r < a.n) ? (r * a.xs + k) * 2 : kBufferEnd);
+      }
+    }
+  };
+  const uint32_t nks = (a.K + 31) / 32;
+  load(0, wf, xf);
+
+  // a lane's slot, -1 for base rows and behind the last
+  int key = (uint32_t)lane < a.n ? gp<const int32_t>(a.seq_)[lane] : -1;
+  if (key < 0 || (uint32_t)key >= a.max_loras) key = -1;
+  {
+    const uint64_t ta = gp<const uint64_t>(a.atab_)[key < 0 ? 0 : key];
+    const uint64_t tb = gp<const uint64_t>(a.btab_)[key < 0 ? 0 : key];
+    if (ta == 0ull || tb == 0ull) key = -1;
   }
-  if (gp<const uint64_t>(a.atab_)[s] != 0ull && gp<const uint64_t>(a.btab_)[s] != 0ull) {
-    RLD_GLOBAL int32_t* order = gp<int32_t>(a.order_);
-    for (uint32_t r0 = 0; r0 < a.n; r0 += 64) {
-      const bool hit = r0 + lane < a.n && seq[r0 + lane] == s;
-      const uint64_t m = __ballot(hit);
-      if (hit) order[below + cnt + __popcll(m & lanemask_lt(lane))] = (int)(r0 + lane);
-      cnt += __popcll(m);
+  __shared__ int keys[kRowsMax];
+  __shared__ float scales[kRowsMax];
+  if (wave == 0) {
+    keys[lane] = key;
+    scales[lane] = key >= 0 ? gp<const float>(a.stab_)[key] : 0.f;
+  }
+  __syncthreads();
+  // the low rows' parts, [row][2][R + 8] bf16 behind the waves' sums
+  uint16_t* const parts = reinterpret_cast<uint16_t*>(smem + kRed);
+  const uint32_t ps = a.R + 8;
+  const uint32_t q = a.R / 4;
+  for (uint32_t t = threadIdx.x; t < a.n * q; t += 64 * kRowsWaves) {
+    const uint32_t row = t / q, col = t % q * 4;
+    floatx4 v = {};
+    if (keys[row] >= 0) {
+      for (uint32_t ch = 0; ch < a.nch; ++ch)
+        v += gp<const floatx4>(a.partial_)[(size_t)ch * a.n * q + t];
+    }
+    v *= scales[row];
+    const uint32_t h0 = pack_bf16x2(v[0], v[1]), h1 = pack_bf16x2(v[2], v[3]);
+    *reinterpret_cast<uint2*>(parts + row * 2 * ps + col) = make_uint2(h0, h1);
+    *reinterpret_cast<uint2*>(parts + (row * 2 + 1) * ps + col) = make_uint2(
+        pack_bf16x2(v[0] - bf16_to_f32(h0 & 0xffffu), v[1] - bf16_to_f32(h0 >> 16)),
+        pack_bf16x2(v[2] - bf16_to_f32(h1 & 0xffffu), v[3] - bf16_to_f32(h1 >> 16)));
+  }
+
+  floatx4 acc[MI];
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) acc[mi] = floatx4{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const uint4 (&w)[U], const uint4 (&x)[U][MI]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) acc[mi] = mfma_bf16_16x16x32(w[u], x[u][mi], acc[mi]);
+  };
+  constexpr uint32_t kStep = kRowsWaves * U;
+  for (uint32_t ks = 0; ks < nks; ks += 2 * kStep) {
+    load(ks + kStep, wn, xn);  // zeros past K
+    multiply(wf, xf);
+    load(ks + 2 * kStep, wf, xf);
+    multiply(wn, xn);
+  }
+
+  __syncthreads();
+  uint64_t left = __ballot(key >= 0);
+  for (int idx = 0; left; ++idx) {
+    const int s = __builtin_amdgcn_readlane(key, __builtin_ctzll(left));
+    const uint64_t mine = __ballot(key == s);
+    left &= ~mine;
+    if (idx % kRowsWaves != wave) continue;
+    const uint64_t e = uniform64(gp<const uint64_t>(a.btab_)[s]) + (uint64_t)col0 * a.R * 2;
+    for (uint32_t k0 = 0; k0 < a.R; k0 += 32) {
+      const uint32_t k = k0 + 8 * g;
+      const bool in = k < a.R;
+      const uint4 ef = buffer_load16(e, kBufferEnd,
+                                     (in && (uint32_t)c < cols) ? (c * a.R + k) * 2 : kBufferEnd);
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) {
+        const uint32_t r = mi * 16 + c;
+        const bool own = (mine >> r) & 1;
+        uint4 hi = zero16(), lo = zero16();
+        if (own && in) {
+          hi = *reinterpret_cast<const uint4*>(parts + r * 2 * ps + k);
+          lo = *reinterpret_cast<const uint4*>(parts + (r * 2 + 1) * ps + k);
+        }
+        floatx4 t = mfma_bf16_16x16x32(ef, lo, floatx4{0.f, 0.f, 0.f, 0.f});
+        t = mfma_bf16_16x16x32(ef, hi, t);
+        // its own rows alone: a NaN or infinity of the matrix survives the zeros
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[mi][i] += own ? t[i] : 0.f;
+      }
     }
   }
-  if (lane == 0) {
-    gp<uint32_t>(a.span_)[2 * s] = below;
-    gp<uint32_t>(a.span_)[2 * s + 1] = cnt;
-  }
+  floatx4* const red = reinterpret_cast<floatx4*>(smem);
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) red[(wave * MI + mi) * kWave + lane] = acc[mi];
+  __syncthreads();
+  if (wave >= MI) return;
+  floatx4 v = red[wave * kWave + lane];
+#pragma unroll
+  for (int w = 1; w < kRowsWaves; ++w) v += red[(w * MI + wave) * kWave + lane];
+  const uint32_t r = wave * 16 + c, col = 4 * g;
+  if (r < a.n && col < cols)
+    *gp<uint2v>(a.out_ + ((size_t)r * a.os + col0 + col) * 2) =
+        uint2v{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
 // ------------------------------------------------------------------ wgrad ----
@@ -829,26 +1261,31 @@ struct WgradArgs {
   uint32_t vs, width, R, tiles, accumulate;
 };
 
+struct WgradSmem {
+  __attribute__((aligned(1024))) unsigned char stage[4][4096];
+  floatx4 red[4][4][kWave];
+};
+
 // Slot s, 64 columns of the wide operand (x for dA, dy for dB): the sum over
-// the slot's rows of low[row][r] * wide[row][col].  Each of four waves takes
-// every fourth 32-row group, staged in LDS of its own (no barrier in the
-// loop) and read transposed; the waves' sums meet in LDS at the end.
+// the slot's positions of low[pos][r] * wide[row][col].  Each of four waves
+// takes every fourth 32-position group, staged in LDS of its own (no barrier
+// in the loop) and read transposed; the waves' sums meet in LDS at the end.
 // DB: the result is [col][R] instead of [R][col].
 template <int RT, bool DB>
-__global__ void __launch_bounds__(256) wgrad_kernel(WgradArgs a) {
-  __shared__ __attribute__((aligned(1024))) unsigned char stage[4][4096];
-  __shared__ floatx4 red[4][4][kWave];
+__device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, WgradSmem& sm) {
+  auto& stage = sm.stage;
+  auto& red = sm.red;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, c = lane & 15;
-  const int s = blockIdx.x / a.tiles;
-  const uint32_t col0 = blockIdx.x % a.tiles * 64;
+  const int s = item / a.tiles;
+  const uint32_t col0 = item % a.tiles * 64;
   const uint64_t dst = gp<const uint64_t>(a.dtab_)[s];
   if (dst == 0ull) return;
   const uint32_t begin = gp<const uint32_t>(a.span_)[2 * s];
   const uint32_t cnt = gp<const uint32_t>(a.span_)[2 * s + 1];
   const RLD_GLOBAL int32_t* order = gp<const int32_t>(a.order_) + begin;
-  const RLD_GLOBAL float* low = gp<const float>(a.low_);
+  const RLD_GLOBAL float* low = gp<const float>(a.low_) + (size_t)begin * a.R;
 
   floatx4 acc[RT][4];
 #pragma unroll
@@ -868,20 +1305,16 @@ __global__ void __launch_bounds__(256) wgrad_kernel(WgradArgs a) {
       __builtin_amdgcn_global_load_lds((const void*)(in ? src : (uint64_t)&g_zero16[0]),
                                        (RLD_LDS void*)(&stage[wave][p * 1024]), 16, 0, 0);
     }
-    uint32_t row[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t i = i0 + 8 * g + e;
-      row[e] = i < cnt ? (uint32_t)order[i] : 0xffffffffu;
-    }
     uint4 lf[RT][3];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const uint32_t r = rt * 16 + c;
       float v[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        v[e] = (row[e] != 0xffffffffu && r < a.R) ? low[(size_t)row[e] * a.R + r] : 0.f;
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t i = i0 + 8 * g + e;
+        v[e] = (i < cnt && r < a.R) ? low[(size_t)i * a.R + r] : 0.f;
+      }
       bf16_parts<3>(v, lf[rt]);
     }
     wait_vm<0>();
@@ -926,10 +1359,20 @@ __global__ void __launch_bounds__(256) wgrad_kernel(WgradArgs a) {
   }
 }
 
+// dA and dB in one launch: the first `items` blocks make dA.
+template <int RT>
+__global__ void __launch_bounds__(256) wgrad_kernel(WgradArgs da, WgradArgs db, uint32_t items) {
+  __shared__ WgradSmem sm;
+  if (blockIdx.x < items) wgrad_item<RT, false>(da, blockIdx.x, sm);
+  else wgrad_item<RT, true>(db, blockIdx.x - items, sm);
+}
+
 // ------------------------------------------------------------------- host ----
 
 static inline size_t round16(size_t v) { return (v + 15) & ~(size_t)15; }
 
+// The workspace: [order][slots by position][spans] and, for u and g, [low rows
+// (fp32 or two bf16 parts: 4 bytes a value)][chunk sums].
 struct LowPlan {
   uint32_t nch;
   size_t low, partial;  // bytes
@@ -938,56 +1381,88 @@ struct LowPlan {
 static LowPlan low_plan(uint32_t n, uint32_t K, uint32_t R) {
   LowPlan p;
   p.nch = div_ceil(K, kLowChunk);
-  p.low = (size_t)n * R * 4;
-  p.partial = p.nch == 1 ? 0 : (size_t)p.nch * n * R * 4;
+  p.low = round16((size_t)n * R * 4);
+  p.partial = (size_t)p.nch * n * R * 4;
   return p;
 }
 
-static int launch_low(const rld_route* r, bool trans, const void* x, uint32_t xs,
-                      const int32_t* seq, uint32_t n, uint64_t low, uint64_t parts,
-                      uint64_t partial, hipStream_t st) {
+static size_t sort_bytes(uint32_t n, uint32_t max_loras) {
+  return 2 * round16((size_t)n * 4) + round16((size_t)max_loras * 8);
+}
+
+struct Sorted {
+  uint64_t order, key, span;
+  bool keep;
+};
+
+// Sorts the rows; wide: the largest row stride that the tiles reach through
+// 32-bit offsets.
+static int launch_sort(const rld_route* r, const int32_t* seq, uint32_t n, uint32_t wide,
+                       uint64_t workspace, Sorted* out, hipStream_t st) {
+  out->order = workspace;
+  out->key = out->order + round16((size_t)n * 4);
+  out->span = out->key + round16((size_t)n * 4);
+  out->keep = (uint64_t)n * wide * 2 > kGatherSpan;
+  SortArgs a;
+  a.seq_ = (uint64_t)seq;
+  a.atab_ = (uint64_t)r->a_table;
+  a.btab_ = (uint64_t)r->b_table;
+  a.order_ = out->order;
+  a.skey_ = out->key;
+  a.span_ = out->span;
+  a.n = n;
+  a.max_loras = r->max_loras;
+  a.keep = out->keep ? 1u : 0u;
+  sort_kernel<<<r->max_loras + 1, 256, 0, st>>>(a);
+  return launch_status();
+}
+
+static LowArgs low_args(const rld_route* r, bool trans, const void* x, uint32_t xs, uint32_t n,
+                        uint64_t order, uint64_t key, uint64_t low, uint64_t parts,
+                        uint64_t partial) {
   LowArgs a;
   a.x_ = (uint64_t)x;
-  a.seq_ = (uint64_t)seq;
   a.mtab_ = (uint64_t)(trans ? r->b_table : r->a_table);
   a.otab_ = (uint64_t)(trans ? r->a_table : r->b_table);
   a.stab_ = (uint64_t)r->scale_table;
+  a.partial_ = partial;
+  a.order_ = order;
+  a.key_ = key;
   a.low_ = low;
   a.parts_ = parts;
-  a.partial_ = partial;
   a.xs = xs;
   a.n = n;
   a.max_loras = r->max_loras;
   a.K = trans ? r->n_out : r->k_in;
   a.R = r->max_rank;
   a.nch = div_ceil(a.K, kLowChunk);
-  const uint32_t items = div_ceil(n, kLowRows) * a.nch;
+  a.tiles = div_ceil(n, kLowRows);
   // few items: the slots of a tile go to several blocks
+  const uint32_t items = a.tiles * a.nch;
   a.nz = items >= 1024u ? 1u : div_ceil(1024u, items);
   if (a.nz > r->max_loras) a.nz = r->max_loras;
   if (a.nz > n) a.nz = n;
   if (a.nz > kLowRows) a.nz = kLowRows;
-  if (trans) low_kernel<true><<<items * a.nz, 256, 0, st>>>(a);
-  else low_kernel<false><<<items * a.nz, 256, 0, st>>>(a);
-  const int e = launch_status();
-  if (e || a.nch == 1) return e;
-  const uint64_t thr = (uint64_t)n * (a.R / 4);
-  low_reduce_kernel<<<(uint32_t)((thr + 255) / 256), 256, 0, st>>>(a);
-  return launch_status();
+  return a;
+}
+
+static uint32_t low_items(const LowArgs& a) { return a.tiles * a.nch * a.nz; }
+static uint32_t sum_blocks(const LowArgs& a) {
+  return (uint32_t)(((uint64_t)a.n * (a.R / 4) + 255) / 256);
 }
 
 template <bool TRANS>
 static int launch_tiles(const rld_route* r, const void* w, uint32_t ws, const void* x,
-                        uint32_t xs, const int32_t* seq, uint32_t n, uint64_t parts, void* out,
+                        uint32_t xs, const Sorted& so, uint32_t n, uint64_t parts, void* out,
                         uint32_t os, hipStream_t st) {
   TileArgs a;
   a.x_ = (uint64_t)x;
   a.w_ = (uint64_t)w;
   a.out_ = (uint64_t)out;
-  a.seq_ = (uint64_t)seq;
   a.parts_ = parts;
   a.etab_ = (uint64_t)(TRANS ? r->a_table : r->b_table);
-  a.otab_ = (uint64_t)(TRANS ? r->b_table : r->a_table);
+  a.order_ = so.order;
+  a.skey_ = so.key;
   a.xs = xs;
   a.ws = ws;
   a.os = os;
@@ -995,7 +1470,7 @@ static int launch_tiles(const rld_route* r, const void* w, uint32_t ws, const vo
   a.K = TRANS ? r->n_out : r->k_in;
   a.N = TRANS ? r->k_in : r->n_out;
   a.R = r->max_rank;
-  a.max_loras = r->max_loras;
+  a.keep = so.keep ? 1u : 0u;
   const uint32_t big = div_ceil(n, 256) * div_ceil(a.N, 256);
   if (big >= kBigTiles) {
     a.tiles_m = div_ceil(n, 256);
@@ -1013,26 +1488,10 @@ static int launch_tiles(const rld_route* r, const void* w, uint32_t ws, const vo
   return launch_status();
 }
 
-template <bool DB>
-static int launch_wgrad(const rld_route* r, const void* v, uint32_t vs, uint64_t low,
-                        uint64_t order, uint64_t span, const uint64_t* dtab, int accumulate,
-                        hipStream_t st) {
-  WgradArgs a;
-  a.v_ = (uint64_t)v;
-  a.low_ = low;
-  a.order_ = order;
-  a.span_ = span;
-  a.dtab_ = (uint64_t)dtab;
-  a.vs = vs;
-  a.width = DB ? r->n_out : r->k_in;
-  a.R = r->max_rank;
-  a.tiles = div_ceil(a.width, 64);
-  a.accumulate = accumulate ? 1u : 0u;
-  const uint32_t grid = a.tiles * r->max_loras;
-  if (a.R <= 16) wgrad_kernel<1, DB><<<grid, 256, 0, st>>>(a);
-  else if (a.R <= 32) wgrad_kernel<2, DB><<<grid, 256, 0, st>>>(a);
-  else if (a.R <= 64) wgrad_kernel<4, DB><<<grid, 256, 0, st>>>(a);
-  else wgrad_kernel<8, DB><<<grid, 256, 0, st>>>(a);
+template <int MI>
+static int launch_rows(const RowsArgs& a, hipStream_t st) {
+  const uint32_t lds = kRowsWaves * MI * kWave * 16 + a.n * 2 * (a.R + 8) * 2;
+  rows_kernel<MI><<<div_ceil(a.N, 16), 64 * kRowsWaves, lds, st>>>(a);
   return launch_status();
 }
 
@@ -1043,7 +1502,7 @@ static int check_items(const rld_route* r, uint32_t n) {
   const uint64_t k = r->k_in > r->n_out ? r->k_in : r->n_out;
   const uint64_t tiles = (k + 63) / 64;
   if (k > (1u << 24) || div_ceil(n, 64) * tiles >= (1u << 23) ||
-      r->max_loras * tiles >= (1u << 23) || (uint64_t)n * (r->max_rank / 4) >= (1u << 31))
+      r->max_loras * tiles >= (1u << 22) || (uint64_t)n * (r->max_rank / 4) >= (1u << 30))
     return RLD_EUNSUPPORTED;
   return RLD_OK;
 }
@@ -1052,10 +1511,11 @@ static int check_items(const rld_route* r, uint32_t n) {
 
 using namespace rld;
 
-extern "C" size_t rld_proj_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t max_rank) {
-  if (n == 0 || k_in == 0 || max_rank == 0) return 0;
+extern "C" size_t rld_proj_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t max_rank,
+                                           uint32_t max_loras) {
+  if (n == 0 || k_in == 0 || max_rank == 0 || max_loras == 0) return 0;
   const LowPlan p = low_plan(n, k_in, max_rank);
-  return round16(p.low) + p.partial;
+  return sort_bytes(n, max_loras) + p.low + p.partial;
 }
 
 extern "C" int rld_proj(const rld_route* route, const void* w, uint32_t w_row_stride,
@@ -1074,14 +1534,49 @@ extern "C" int rld_proj(const rld_route* route, const void* w, uint32_t w_row_st
       (e = check_wide(out_row_stride)))
     return e;
   if ((e = check_items(route, n))) return e;
-  if (workspace_bytes < rld_proj_workspace_bytes(n, route->k_in, route->max_rank))
+  if (workspace_bytes < rld_proj_workspace_bytes(n, route->k_in, route->max_rank, route->max_loras))
     return RLD_ENOSPACE;
   const LowPlan p = low_plan(n, route->k_in, route->max_rank);
-  const uint64_t low = (uint64_t)workspace;
+  const uint64_t parts = (uint64_t)workspace + sort_bytes(n, route->max_loras);
+  const uint64_t partial = parts + p.low;
   const hipStream_t st = (hipStream_t)stream;
-  e = launch_low(route, false, x, x_row_stride, seq_slot, n, 0, low, low + round16(p.low), st);
-  if (e) return e;
-  return launch_tiles<false>(route, w, w_row_stride, x, x_row_stride, seq_slot, n, low, out,
+  if (n <= kRowsMax) {
+    const LowArgs l = low_args(route, false, x, x_row_stride, n, 0, (uint64_t)seq_slot, 0, 0,
+                               partial);
+    low_kernel<<<low_items(l), 256, 0, st>>>(l);
+    if ((e = launch_status())) return e;
+    RowsArgs a;
+    a.x_ = (uint64_t)x;
+    a.w_ = (uint64_t)w;
+    a.out_ = (uint64_t)out;
+    a.seq_ = (uint64_t)seq_slot;
+    a.partial_ = partial;
+    a.atab_ = (uint64_t)route->a_table;
+    a.btab_ = (uint64_t)route->b_table;
+    a.stab_ = (uint64_t)route->scale_table;
+    a.xs = x_row_stride;
+    a.ws = w_row_stride;
+    a.os = out_row_stride;
+    a.n = n;
+    a.K = route->k_in;
+    a.N = route->n_out;
+    a.R = route->max_rank;
+    a.nch = p.nch;
+    a.max_loras = route->max_loras;
+    return n <= 16 ? launch_rows<1>(a, st) : n <= 32 ? launch_rows<2>(a, st) : launch_rows<4>(a, st);
+  }
+  Sorted so;
+  const uint32_t wide = x_row_stride > out_row_stride ? x_row_stride : out_row_stride;
+  if ((e = launch_sort(route, seq_slot, n, wide, (uint64_t)workspace, &so, st))) return e;
+  const LowArgs l = low_args(route, false, x, x_row_stride, n, so.order, so.key, 0, parts,
+                             p.nch == 1 ? 0 : partial);
+  low_kernel<<<low_items(l), 256, 0, st>>>(l);
+  if ((e = launch_status())) return e;
+  if (p.nch > 1) {
+    low_reduce_kernel<<<sum_blocks(l), 256, 0, st>>>(l, l, sum_blocks(l));
+    if ((e = launch_status())) return e;
+  }
+  return launch_tiles<false>(route, w, w_row_stride, x, x_row_stride, so, n, parts, out,
                              out_row_stride, st);
 }
 
@@ -1089,8 +1584,7 @@ extern "C" size_t rld_proj_grad_workspace_bytes(uint32_t n, uint32_t k_in, uint3
                                                 uint32_t max_rank, uint32_t max_loras) {
   if (k_in == 0 || n_out == 0 || max_rank == 0 || max_loras == 0) return 0;
   const LowPlan u = low_plan(n, k_in, max_rank), g = low_plan(n, n_out, max_rank);
-  return round16(u.low) + u.partial + 2 * round16(g.low) + g.partial + round16((size_t)n * 4) +
-         round16((size_t)max_loras * 8);
+  return sort_bytes(n, max_loras) + u.low + u.partial + 2 * g.low + g.partial;
 }
 
 extern "C" int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_row_stride,
@@ -1124,43 +1618,62 @@ extern "C" int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_r
   if (workspace_bytes < rld_proj_grad_workspace_bytes(n, route->k_in, route->n_out,
                                                       route->max_rank, route->max_loras))
     return RLD_ENOSPACE;
+  if (n == 0 && !adapters) return RLD_OK;
   const LowPlan pu = low_plan(n, route->k_in, route->max_rank);
   const LowPlan pg = low_plan(n, route->n_out, route->max_rank);
-  const uint64_t u = (uint64_t)workspace;
-  const uint64_t up = u + round16(pu.low);
-  const uint64_t gl = up + pu.partial;
-  const uint64_t gparts = gl + round16(pg.low);
-  const uint64_t gpart = gparts + round16(pg.low);
-  const uint64_t order = gpart + pg.partial;
-  const uint64_t span = order + round16((size_t)n * 4);
+  const uint64_t ul = (uint64_t)workspace + sort_bytes(n, route->max_loras);
+  const uint64_t usum = ul + pu.low;
+  const uint64_t gl = usum + pu.partial;
+  const uint64_t gparts = gl + pg.low;
+  const uint64_t gsum = gparts + pg.low;
   const hipStream_t st = (hipStream_t)stream;
+  Sorted so;
+  uint32_t wide = dy_row_stride;
+  if (dx && dx_row_stride > wide) wide = dx_row_stride;
+  if ((e = launch_sort(route, seq_slot, n, wide, (uint64_t)workspace, &so, st))) return e;
   if (n != 0) {
-    if (db_table && (e = launch_low(route, false, x, x_row_stride, seq_slot, n, u, 0, up, st)))
-      return e;
-    if ((dx || da_table) &&
-        (e = launch_low(route, true, dy, dy_row_stride, seq_slot, n, da_table ? gl : 0,
-                        dx ? gparts : 0, gpart, st)))
-      return e;
-    if (dx && (e = launch_tiles<true>(route, w, w_row_stride, dy, dy_row_stride, seq_slot, n,
-                                      gparts, dx, dx_row_stride, st)))
+    // u for dB; g for dx (as parts) and dA
+    const LowArgs u = low_args(route, false, x, x_row_stride, n, so.order, so.key, ul, 0,
+                               pu.nch == 1 ? 0 : usum);
+    const LowArgs g = low_args(route, true, dy, dy_row_stride, n, so.order, so.key,
+                               da_table ? gl : 0, dx ? gparts : 0, pg.nch == 1 ? 0 : gsum);
+    const bool want_u = db_table != nullptr, want_g = dx || da_table;
+    const uint32_t iu = want_u ? low_items(u) : 0u, ig = want_g ? low_items(g) : 0u;
+    low_pair_kernel<<<iu + ig, 256, 0, st>>>(u, g, iu);
+    if ((e = launch_status())) return e;
+    const uint32_t bu = want_u && pu.nch > 1 ? sum_blocks(u) : 0u;
+    const uint32_t bg = want_g && pg.nch > 1 ? sum_blocks(g) : 0u;
+    if (bu + bg) {
+      low_reduce_kernel<<<bu + bg, 256, 0, st>>>(u, g, bu);
+      if ((e = launch_status())) return e;
+    }
+    if (dx && (e = launch_tiles<true>(route, w, w_row_stride, dy, dy_row_stride, so, n, gparts, dx,
+                                      dx_row_stride, st)))
       return e;
   }
   if (!adapters) return RLD_OK;
-  ListArgs l;
-  l.seq_ = (uint64_t)seq_slot;
-  l.atab_ = (uint64_t)route->a_table;
-  l.btab_ = (uint64_t)route->b_table;
-  l.order_ = order;
-  l.span_ = span;
-  l.n = n;
-  l.max_loras = route->max_loras;
-  lists_kernel<<<route->max_loras, 64, 0, st>>>(l);
-  if ((e = launch_status())) return e;
-  if (da_table && (e = launch_wgrad<false>(route, x, x_row_stride, gl, order, span, da_table,
-                                           accumulate, st)))
-    return e;
-  if (db_table && (e = launch_wgrad<true>(route, dy, dy_row_stride, u, order, span, db_table,
-                                          accumulate, st)))
-    return e;
-  return RLD_OK;
+  WgradArgs a, b;
+  a.v_ = (uint64_t)x;
+  b.v_ = (uint64_t)dy;
+  a.vs = x_row_stride;
+  b.vs = dy_row_stride;
+  a.low_ = gl;
+  b.low_ = ul;
+  a.dtab_ = (uint64_t)da_table;
+  b.dtab_ = (uint64_t)db_table;
+  a.width = route->k_in;
+  b.width = route->n_out;
+  a.order_ = b.order_ = so.order;
+  a.span_ = b.span_ = so.span;
+  a.R = b.R = route->max_rank;
+  a.accumulate = b.accumulate = accumulate ? 1u : 0u;
+  a.tiles = div_ceil(a.width, 64);
+  b.tiles = div_ceil(b.width, 64);
+  const uint32_t ia = da_table ? a.tiles * route->max_loras : 0u;
+  const uint32_t ib = db_table ? b.tiles * route->max_loras : 0u;
+  if (a.R <= 16) wgrad_kernel<1><<<ia + ib, 256, 0, st>>>(a, b, ia);
+  else if (a.R <= 32) wgrad_kernel<2><<<ia + ib, 256, 0, st>>>(a, b, ia);
+  else if (a.R <= 64) wgrad_kernel<4><<<ia + ib, 256, 0, st>>>(a, b, ia);
+  else wgrad_kernel<8><<<ia + ib, 256, 0, st>>>(a, b, ia);
+  return launch_status();
 }

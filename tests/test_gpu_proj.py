@@ -156,12 +156,12 @@ class Case:
         return h[1:-1, :width]
 
     def call_proj(self, out, ws, stream=None):
-        need = R.rld_proj_workspace_bytes(self.n, self.k, self.r)
+        need = R.rld_proj_workspace_bytes(self.n, self.k, self.r, self.slots)
         return R.rld_proj(self.route, self.wd, self.ws, self.xd, self.xs, self.slotd, self.n,
                           out.data_ptr() + 2 * self.os, self.os, ws, need, stream)
 
     def proj(self):
-        need = R.rld_proj_workspace_bytes(self.n, self.k, self.r)
+        need = R.rld_proj_workspace_bytes(self.n, self.k, self.r, self.slots)
         ws, out = self.scratch(need), self.out_rows(self.os)
         R.check(self.call_proj(out, ws), "rld_proj")
         torch.cuda.synchronize()
@@ -424,7 +424,7 @@ def test_graph_replays_with_new_routing():
     turn with new routing, with eager calls and host waits between the replays."""
     say("case: proj graphs")
     c = Case(96, 520, 264, 16, 6, seed=11)
-    need = max(R.rld_proj_workspace_bytes(c.n, c.k, c.r),
+    need = max(R.rld_proj_workspace_bytes(c.n, c.k, c.r, c.slots),
                R.rld_proj_grad_workspace_bytes(c.n, c.k, c.m, c.r, c.slots))
     ws, out, dx = c.scratch(need), c.out_rows(c.os), c.out_rows(c.xs)
     c.tables()
@@ -459,7 +459,7 @@ def test_on_another_stream():
     c = Case(200, 264, 136, 16, 4, seed=13)
     want = c.proj()
     s = torch.cuda.Stream()
-    ws, out = c.scratch(R.rld_proj_workspace_bytes(c.n, c.k, c.r)), c.out_rows(c.os)
+    ws, out = c.scratch(R.rld_proj_workspace_bytes(c.n, c.k, c.r, c.slots)), c.out_rows(c.os)
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):
         R.check(c.call_proj(out, ws), "rld_proj")
@@ -480,7 +480,7 @@ def test_far_rows():
     want, grads = c.proj(), c.grad()
     c.xd, c.xs = far, stride
     out = c.out_rows(c.os)
-    ws = c.scratch(R.rld_proj_workspace_bytes(n, k, r))
+    ws = c.scratch(R.rld_proj_workspace_bytes(n, k, r, 3))
     R.check(c.call_proj(out, ws), "rld_proj")
     torch.cuda.synchronize()
     assert np.array_equal(c.body(out, m, c.os), want)

@@ -434,11 +434,13 @@ int rld_moe_grouped_pair(const rld_moe_route* route_a, const rld_moe_route* rout
                          void* stream);
 
 /* Bytes of workspace rld_proj needs: the rows' order by slot, the fp32 low-rank
- * rows [n][max_rank] and their partial sums [ceil(k_in / 512)][n][max_rank].
- * 16-byte aligned device memory; nothing in it must start at any value or is carried
+ * rows [n][max_rank], their partial sums [ceil(k_in / 512)][n][max_rank] and,
+ * for calls too small to fill the chip with large tiles, up to 16 partial sums
+ * of the product [n][n_out].  It does not grow steadily with n: ask for the
+ * largest call of each kind.  16-byte aligned device memory; nothing in it must start at any value or is carried
  * between calls; calls that share it must be ordered (captured graphs that
  * share one included). */
-size_t rld_proj_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t max_rank,
+size_t rld_proj_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t n_out, uint32_t max_rank,
                                 uint32_t max_loras);
 
 /* The shared projection with each row's adapter, in one output rounding:
@@ -454,7 +456,7 @@ size_t rld_proj_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t max_rank,
  *            out + i*out_row_stride; the rest of the row is left alone.  out
  *            must not overlap w or x
  * n == 0 is a no-op.  RLD_EUNSUPPORTED for row strides above 2^21,
- * k_in or n_out above 2^24, and from 2^23 tiles of 64 x 64 outputs, 2^22
+ * n above 2^26, k_in or n_out above 2^24, and from 2^23 tiles of 64 x 64 outputs, 2^21
  * pairs of a slot and 64 columns, or n * max_rank of 2^32 on.
  * Results do not change from run to run; a row's summation order may depend on
  * n (the tile shape does). */

@@ -104,7 +104,7 @@ _SIGS = {
     "rld_lora_shrink": (c_int, [_L, _P, c_uint32, c_uint32, _P, _P, c_size_t, _P]),
     "rld_lora_expand_fold": (c_int, [_L, _P, c_uint32, _P, c_uint32, _P]),
     "rld_lora_delta": (c_int, [_L, _P, c_uint32, c_uint32, _P, c_uint32, _P, _P, c_size_t, _P]),
-    "rld_proj_workspace_bytes": (c_size_t, [c_uint32, c_uint32, c_uint32, c_uint32]),
+    "rld_proj_workspace_bytes": (c_size_t, [c_uint32, c_uint32, c_uint32, c_uint32, c_uint32]),
     "rld_proj": (c_int, [_R, _P, c_uint32, _P, c_uint32, _P, c_uint32, _P, c_uint32, _P,
                          c_size_t, _P]),
     "rld_proj_grad_workspace_bytes": (c_size_t, [c_uint32, c_uint32, c_uint32, c_uint32,
@@ -319,8 +319,8 @@ def rld_lora_delta(pair, x, x_row_stride, m, base_out, out_row_stride, xa, works
                                stream_handle(stream))
 
 
-def rld_proj_workspace_bytes(n, k_in, max_rank, max_loras):
-    return _lib.rld_proj_workspace_bytes(n, k_in, max_rank, max_loras)
+def rld_proj_workspace_bytes(n, k_in, n_out, max_rank, max_loras):
+    return _lib.rld_proj_workspace_bytes(n, k_in, n_out, max_rank, max_loras)
 
 
 def rld_proj(route, w, w_row_stride, x, x_row_stride, seq_slot, n, out, out_row_stride,

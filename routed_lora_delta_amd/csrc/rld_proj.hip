@@ -67,8 +67,9 @@ __device__ __forceinline__ void bf16_parts(const float (&v)[8], uint4 (&out)[NP]
 struct SortArgs {
   uint64_t seq_, atab_, btab_;
   uint64_t order_, skey_;  // [n]: the row at a sorted position; its slot, -1 for base rows
+  uint64_t rkey_;          // [n]: the same slots by row
   uint64_t span_;          // [max_loras][2]: a slot's first position and rows
-  uint32_t n, max_loras, keep;  // keep: leave the rows in their order
+  uint32_t n, max_loras;
 };
 
 constexpr uint32_t kSortBatch = 4096;  // rows of a pass: 16 a thread
@@ -122,9 +123,8 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* wsum, uin
 // One block per slot, and one for the base rows: its rows in ascending order,
 // behind those of the slots below it, which the block counts itself (no block
 // waits for another).
-__global__ void __launch_bounds__(256) sort_kernel(SortArgs a) {
-  __shared__ uint32_t wsum[4];
-  const int s = (int)blockIdx.x;
+__device__ __forceinline__ void sort_item(const SortArgs& a, uint32_t item, uint32_t* wsum) {
+  const int s = (int)item;
   const bool base = (uint32_t)s == a.max_loras;
   const bool active =
       !base && gp<const uint64_t>(a.atab_)[s] != 0ull && gp<const uint64_t>(a.btab_)[s] != 0ull;
@@ -147,9 +147,9 @@ __global__ void __launch_bounds__(256) sort_kernel(SortArgs a) {
 #pragma unroll
     for (int e = 0; e < 16; ++e)
       if (key[e] == s) {
-        const uint32_t pos = a.keep ? r0 + e : at;
-        gp<int32_t>(a.order_)[pos] = (int)(r0 + e);
-        gp<int32_t>(a.skey_)[pos] = active ? s : -1;
+        gp<int32_t>(a.order_)[at] = (int)(r0 + e);
+        gp<int32_t>(a.skey_)[at] = active ? s : -1;
+        gp<int32_t>(a.rkey_)[r0 + e] = active ? s : -1;
         ++at;
       }
     cnt += tot;
@@ -158,6 +158,11 @@ __global__ void __launch_bounds__(256) sort_kernel(SortArgs a) {
     gp<uint32_t>(a.span_)[2 * s] = first;
     gp<uint32_t>(a.span_)[2 * s + 1] = active ? cnt : 0u;
   }
+}
+
+__global__ void __launch_bounds__(256) sort_kernel(SortArgs a) {
+  __shared__ uint32_t wsum[4];
+  sort_item(a, blockIdx.x, wsum);
 }
 
 // -------------------------------------------------------------------- low ----
@@ -288,7 +293,7 @@ __device__ __forceinline__ void low_sum(const LowArgs& a, uint32_t block) {
   if (t >= (uint64_t)a.n * q) return;
   const uint32_t pos = (uint32_t)(t / q);
   const int s = gp<const int32_t>(a.key_)[pos];
-  if (s < 0) return;
+  if (s < 0 || (uint32_t)s >= a.max_loras) return;
   floatx4 sum = {};
   for (uint32_t ch = 0; ch < a.nch; ++ch)
     sum += gp<const floatx4>(a.partial_)[(size_t)ch * a.n * q + t];
@@ -304,10 +309,16 @@ __global__ void __launch_bounds__(256) low_reduce_kernel(LowArgs u, LowArgs gr, 
 
 struct TileArgs {
   uint64_t x_, w_, out_, parts_, etab_;
-  uint64_t order_, skey_;  // by sorted position
+  uint64_t order_;  // sorted positions' rows, or 0: rows in their own order, their
+                    // offsets taken from a tile's first row
+  uint64_t skey_;   // slots by position
   uint32_t xs, ws, os, n, K, N, R, tiles_m, tiles_n;
-  uint32_t keep;  // rows in their own order: offsets are taken from a tile's first row
 };
+
+// The row at position p, less the row that offsets are taken from.
+__device__ __forceinline__ uint32_t tile_row(const TileArgs& a, uint32_t p, uint32_t first) {
+  return (a.order_ ? (uint32_t)gp<const int32_t>(a.order_)[p] : p) - first;
+}
 
 // Until at most N of this wave's loads and stores are in flight.
 template <int N>
@@ -400,7 +411,7 @@ __device__ __forceinline__ void k_tail(const TileArgs& a, uint32_t k0, floatx4 (
                                        const uint32_t (&cols_at)[NI]) {
   const int lane = threadIdx.x & 63;
   const uint32_t rows = a.n - row0, cols = a.N - col0;
-  const uint32_t first = a.keep ? row0 : 0u;
+  const uint32_t first = a.order_ ? 0u : row0;
   const uint64_t x = a.x_ + (uint64_t)first * a.xs * 2;
   for (; k0 < a.K; k0 += 32) {
     int tl = lane;  // offsets are computed here, not before the loop and held
@@ -428,7 +439,7 @@ __device__ __forceinline__ void k_tail(const TileArgs& a, uint32_t k0, floatx4 (
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) {
       const uint32_t r = rows_at[mi] + c;
-      const uint32_t o = (uint32_t)gp<const int32_t>(a.order_)[row0 + min(r, rows - 1)] - first;
+      const uint32_t o = tile_row(a, row0 + min(r, rows - 1), first);
       const uint4 xf = buffer_load16(x, kBufferEnd,
                                      (k < a.K && r < rows) ? (o * a.xs + k) * 2 : kBufferEnd);
 #pragma unroll
@@ -456,13 +467,13 @@ __device__ __forceinline__ void store_tile(const TileArgs& a, const floatx4 (&ac
                                            const uint32_t (&cols_at)[NI]) {
   const int lane = threadIdx.x & 63;
   const uint32_t rows = a.n - row0, cols = a.N - col0;
-  const uint32_t first = a.keep ? row0 : 0u;
+  const uint32_t first = a.order_ ? 0u : row0;
   const uint64_t out = a.out_ + ((uint64_t)first * a.os + col0) * 2;
   uint32_t at[MI];
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
     const uint32_t r = rows_at[mi] + (lane & 15);
-    at[mi] = (uint32_t)gp<const int32_t>(a.order_)[row0 + min(r, rows - 1)] - first;
+    at[mi] = tile_row(a, row0 + min(r, rows - 1), first);
   }
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
@@ -481,196 +492,85 @@ __device__ __forceinline__ void store_tile(const TileArgs& a, const floatx4 (&ac
   }
 }
 
-// The low-rank part of the smaller tiles: every slot that the wave's rows name
-// goes through all its row blocks, with zeros for the rows of other slots,
-// which then leave its product out (a NaN or infinity of its matrix would
-// survive the zeros).  The operands of the next 32 of rank are loaded while
-// the current ones multiply.
-template <int MI, int NI, bool TRANS>
-__device__ __forceinline__ void add_low(const TileArgs& a, floatx4 (&acc)[NI][MI], uint32_t row0,
-                                        uint32_t col0, const uint32_t (&rows_at)[MI],
-                                        const uint32_t (&cols_at)[NI]) {
-  const int lane = threadIdx.x & 63;
-  const int g = lane >> 4, c = lane & 15;
-  const uint32_t rows = a.n - row0, cols = a.N - col0;
-  const uint32_t R = a.R;
-  int key[MI], left[MI];
-#pragma unroll
-  for (int mi = 0; mi < MI; ++mi) {
-    const uint32_t r = rows_at[mi] + c;
-    key[mi] = r < rows ? gp<const int32_t>(a.skey_)[row0 + r] : -1;
-    left[mi] = key[mi];
-  }
-  const uint64_t low = a.parts_ + (uint64_t)row0 * R * 4;
+// ------------------------------------------------------------------- part ----
 
-  struct Step {
-    int s;
-    uint32_t k0;
-    uint64_t e;
-  };
-  // On to the next 32 of rank, or to the first slot that is left; false: done.
-  auto next = [&](Step& st) {
-    st.k0 += 32;
-    if (st.k0 < R) return true;
-    int first = -1;
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi) first = first < 0 ? left[mi] : first;
-    const uint64_t m = __ballot(first >= 0);
-    if (!m) return false;
-    st.s = __builtin_amdgcn_readlane(first, __builtin_ctzll(m));
-    st.e = uniform64(gp<const uint64_t>(a.etab_)[st.s]);
-    st.k0 = 0;
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi) left[mi] = left[mi] == st.s ? -1 : left[mi];
-    return true;
-  };
-  struct Operands {
-    uint4 e[NI], hi[MI], lo[MI];
-  };
-  auto load = [&](const Step& st, Operands& o) {
-    const uint32_t k = st.k0 + 8 * g;
-#pragma unroll
-    for (int ni = 0; ni < NI; ++ni) {
-      const uint32_t col = cols_at[ni] + c;
-      const bool in = k < R && col < cols;
-      if constexpr (!TRANS) {
-        o.e[ni] = buffer_load16(st.e + (uint64_t)col0 * R * 2, kBufferEnd,
-                                in ? (col * R + k) * 2 : kBufferEnd);
-      } else {
-        uint32_t e[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          e[q] = buffer_load2(st.e + ((uint64_t)(st.k0 + q) * a.N + col0) * 2, kBufferEnd,
-                              in ? 16 * g * a.N + col * 2 : kBufferEnd);
-        o.e[ni] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16,
-                             e[6] | e[7] << 16);
-      }
-    }
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi) {
-      const uint32_t off = (key[mi] == st.s && k < R) ? (rows_at[mi] + c) * R * 4 + k * 2
-                                                      : kBufferEnd;
-      o.hi[mi] = buffer_load16(low, kBufferEnd, off);
-      o.lo[mi] = buffer_load16(low + R * 2, kBufferEnd, off);
-    }
-  };
-  auto multiply = [&](const Step& st, const Operands& o) {
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi) {
-      const bool mine = key[mi] == st.s;
-#pragma unroll
-      for (int ni = 0; ni < NI; ++ni) {
-        floatx4 t = mfma_bf16_16x16x32(o.e[ni], o.lo[mi], floatx4{0.f, 0.f, 0.f, 0.f});
-        t = mfma_bf16_16x16x32(o.e[ni], o.hi[mi], t);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[ni][mi][i] += mine ? t[i] : 0.f;
-      }
-    }
-  };
-  Step sa = {-1, R, 0}, sb;
-  Operands oa, ob;
-  if (!next(sa)) return;
-  load(sa, oa);
-  for (;;) {
-    sb = sa;
-    const bool more = next(sb);
-    if (more) load(sb, ob);
-    multiply(sa, oa);
-    if (!more) return;
-    sa = sb;
-    const bool again = next(sa);
-    if (again) load(sa, oa);
-    multiply(sb, ob);
-    if (!again) return;
-  }
-}
+struct PartArgs {
+  uint64_t x_, w_, sum_;  // sum_: fp32 [splits][n][N]
+  uint32_t xs, ws, n, K, N;
+  uint32_t tiles_m, tiles_n, splits, steps;  // steps of 64 of K in a split
+};
 
-// A BM x BN output tile by WR x WC waves.  K goes by in steps of 64 through
-// STAGES LDS buffers that buffer loads fill directly (16 bytes a lane; lanes
-// past the operand's end get zeros).  Rows of 128 bytes are swizzled: chunk q
-// of row r lies at q ^ (r/2 % 8), so that the 16 rows of a fragment read fall
-// on all banks.  TRANS: W is [K][N]; its tile keeps that order, 32-byte
-// column pairs swizzled by the row, and transposing LDS reads make the
-// fragments.
+// A BM x BN tile of x W^T over one split of K, for calls too small to fill the
+// chip with large tiles: K is split until a grid does, and finish adds the
+// splits.  Four waves (WR x WC); K goes by in steps of 64 through STAGES LDS
+// buffers that buffer loads fill directly, 16 bytes a lane in whole 128-byte
+// pieces of a row (lanes past the operand's end get zeros).  Chunk q of row r
+// lies at q ^ (r/2 % 8), so that the 16 rows of a fragment read fall on all
+// banks.  TRANS: W is [K][N]; its tile keeps that order, 32-byte column pairs
+// swizzled by the row, and transposing LDS reads make the fragments.
 // The product is computed transposed (W as the first operand), so a lane
 // holds four consecutive output columns of one row.
 template <int BM, int BN, int WR, int WC, int STAGES, bool TRANS>
-__device__ __forceinline__ void tile_body(const TileArgs& a) {
-  constexpr int NW = WR * WC;
+__device__ __forceinline__ void part_item(const PartArgs& a, uint32_t item, unsigned char* lds) {
   constexpr int MI = BM / (16 * WR), NI = BN / (16 * WC);
-  constexpr int PA = BM / (8 * NW), PB = BN / (8 * NW);
+  constexpr int LA = BM / 8, LB = BN / 8;       // 1 KB loads of a stage
+  constexpr int PL = (LA + LB + 3) / 4;         // of a wave
   constexpr int kStageB = (BM + BN) * 128;
   constexpr int kPairs = BN / 16;
-  __shared__ __attribute__((aligned(1024))) unsigned char lds[STAGES * kStageB];
+  static_assert(WR * WC == 4, "four waves");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, c = lane & 15;
   const int wr = wave / WC, wc = wave % WC;
-  const uint32_t tm = blockIdx.x % a.tiles_m, tn = blockIdx.x / a.tiles_m;
-  const uint32_t row0 = tm * BM, col0 = tn * BN;
-  const uint32_t rows = min((uint32_t)BM, a.n - row0);
-  const uint32_t first = a.keep ? row0 : 0u;
+  const uint32_t tiles = a.tiles_m * a.tiles_n;
+  const uint32_t split = item / tiles, tile = item % tiles;
+  const uint32_t row0 = tile % a.tiles_m * BM, col0 = tile / a.tiles_m * BN;
+  const uint32_t rows = min((uint32_t)BM, a.n - row0), cols = min((uint32_t)BN, a.N - col0);
+  const uint32_t kt0 = split * a.steps;
+  const uint32_t nk = min(a.steps, (a.K + 63) / 64 - kt0);
 
-  const rsrc_t rx = buffer(a.x_ + (uint64_t)first * a.xs * 2,
-                           ((uint64_t)((a.keep ? rows : a.n) - 1) * a.xs + a.K) * 2);
-  const uint32_t wrows = min((uint32_t)BN, a.N - col0);
-  const rsrc_t rw0 = buffer(a.w_ + (uint64_t)col0 * a.ws * 2,
-                            ((uint64_t)(wrows - 1) * a.ws + a.K) * 2);
-
-  uint32_t va[PA], vb[PB];
+  const rsrc_t rx =
+      buffer(a.x_ + (uint64_t)row0 * a.xs * 2, ((uint64_t)(rows - 1) * a.xs + a.K) * 2);
+  const rsrc_t rw0 =
+      buffer(a.w_ + (uint64_t)col0 * a.ws * 2, ((uint64_t)(cols - 1) * a.ws + a.K) * 2);
+  // Load j of this wave is load wave + 4 j of the stage (the last again where
+  // there is none: every wave counts the same number of loads).
+  uint32_t off[PL], kq[PL], to[PL];
+  bool is_x[PL];
 #pragma unroll
-  for (int p = 0; p < PA; ++p) {
-    const uint32_t r = (wave * PA + p) * 8 + (lane >> 3);
-    const uint32_t o = (uint32_t)gp<const int32_t>(a.order_)[row0 + min(r, rows - 1)] - first;
-    va[p] = r < rows ? o * a.xs * 2 + (((lane & 7) ^ ((r >> 1) & 7)) * 16) : kOutside;
-  }
-#pragma unroll
-  for (int p = 0; p < PB; ++p) {
-    if constexpr (!TRANS) {
-      const uint32_t r = (wave * PB + p) * 8 + (lane >> 3);
-      vb[p] = r * a.ws * 2 + (((lane & 7) ^ ((r >> 1) & 7)) * 16);
-    } else {
+  for (int j = 0; j < PL; ++j) {
+    const int i = min(wave + 4 * j, LA + LB - 1);
+    is_x[j] = i < LA;
+    to[j] = i * 1024;
+    const uint32_t r = (is_x[j] ? i : i - LA) * 8 + (lane >> 3);
+    const uint32_t q = (lane & 7) ^ ((r >> 1) & 7);
+    kq[j] = q * 8;
+    off[j] = r * (is_x[j] ? a.xs : a.ws) * 2 + q * 16;
+    if (TRANS && !is_x[j]) {
       constexpr int CPR = BN / 8;  // chunks of a row
-      const uint32_t k = (wave * PB + p) * (64 / CPR) + lane / CPR;
+      const uint32_t k = (i - LA) * (64 / CPR) + lane / CPR;
       const uint32_t slot = lane % CPR;
       const uint32_t h = ((k & 3) | ((k >> 3) & 3) << 2) & (kPairs - 1);
-      vb[p] = k * a.ws * 2 + (((slot >> 1) ^ h) * 2 + (slot & 1)) * 16;
+      off[j] = k * a.ws * 2 + (((slot >> 1) ^ h) * 2 + (slot & 1)) * 16;
+      kq[j] = 0;
     }
   }
-  const uint32_t nk = (a.K + 63) / 64;
   const uint32_t lds0 = lds_addr(lds);
   auto issue = [&](uint32_t kt) {
-    const uint32_t st = __builtin_amdgcn_readfirstlane(lds0 + (kt % STAGES) * kStageB);
-    const uint32_t k0 = kt * 64;
-    const bool tail = k0 + 64 > a.K;
+    const uint32_t st = lds0 + (kt % STAGES) * kStageB;
+    const uint32_t k0 = (kt0 + kt) * 64;
+    const bool in = kt < nk;
+    rsrc_t rw = rw0;
+    if constexpr (TRANS)
+      rw = buffer(a.w_ + ((uint64_t)(in ? k0 : 0) * a.ws + col0) * 2,
+                  in ? ((uint64_t)(a.K - k0 - 1) * a.ws + a.N - col0) * 2 : 0);
 #pragma unroll
-    for (int p = 0; p < PA; ++p) {
-      uint32_t v = va[p];
-      if (tail) {
-        const uint32_t r = (wave * PA + p) * 8 + (lane >> 3);
-        const uint32_t k = k0 + (((lane & 7) ^ ((r >> 1) & 7)) * 8);
-        if (k >= a.K) v = kOutside;
-      }
-      dma16(rx, st + (wave * PA + p) * 1024, v, k0 * 2);
-    }
-    if constexpr (!TRANS) {
-#pragma unroll
-      for (int p = 0; p < PB; ++p) {
-        uint32_t v = vb[p];
-        if (tail) {
-          const uint32_t r = (wave * PB + p) * 8 + (lane >> 3);
-          const uint32_t k = k0 + (((lane & 7) ^ ((r >> 1) & 7)) * 8);
-          if (k >= a.K) v = kOutside;
-        }
-        dma16(rw0, st + BM * 128 + (wave * PB + p) * 1024, v, k0 * 2);
-      }
-    } else {
-      const bool in = k0 < a.K;
-      const rsrc_t rw = buffer(a.w_ + ((uint64_t)(in ? k0 : 0) * a.ws + col0) * 2,
-                               in ? ((uint64_t)(a.K - k0 - 1) * a.ws + a.N - col0) * 2 : 0);
-#pragma unroll
-      for (int p = 0; p < PB; ++p)
-        dma16(rw, st + BM * 128 + (wave * PB + p) * 1024, vb[p], 0);
+    for (int j = 0; j < PL; ++j) {
+      uint32_t v = off[j];
+      if (k0 + 64 > a.K && k0 + kq[j] >= a.K && (is_x[j] || !TRANS)) v = kOutside;
+      const bool rows_of_k = !is_x[j] && TRANS;
+      const uint32_t at = rows_of_k ? 0u : in ? k0 * 2 : kOutside;
+      dma16(is_x[j] ? rx : rw, st + to[j], v, at);
     }
   };
 
@@ -679,38 +579,31 @@ __device__ __forceinline__ void tile_body(const TileArgs& a) {
   for (int ni = 0; ni < NI; ++ni)
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi) acc[ni][mi] = floatx4{0.f, 0.f, 0.f, 0.f};
-
 #pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) issue(s);
+  for (int t = 0; t < STAGES - 1; ++t) issue(t);
 
   for (uint32_t kt = 0; kt < nk; ++kt) {
-    wait_vm<(STAGES - 2) * (PA + PB)>();
+    wait_vm<(STAGES - 2) * PL>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     issue(kt + STAGES - 1);
-    const unsigned char* st = lds + (kt % STAGES) * kStageB;
+    const uint32_t st = lds0 + (kt % STAGES) * kStageB;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       uint4 xf[MI], wf[NI];
+      const uint32_t sw = ((ks * 4 + g) ^ (c >> 1)) * 16;
 #pragma unroll
       for (int mi = 0; mi < MI; ++mi)
-        xf[mi] = *reinterpret_cast<const uint4*>(st + ((wr * MI + mi) * 16 + c) * 128 +
-                                                 ((ks * 4 + g) ^ (c >> 1)) * 16);
+        xf[mi] = lds16(lds_at(st + (wr * MI * 16 + c) * 128 + sw) + mi * 2048);
 #pragma unroll
       for (int ni = 0; ni < NI; ++ni) {
         if constexpr (!TRANS) {
-          wf[ni] = *reinterpret_cast<const uint4*>(st + BM * 128 +
-                                                   ((wc * NI + ni) * 16 + c) * 128 +
-                                                   ((ks * 4 + g) ^ (c >> 1)) * 16);
+          wf[ni] = lds16(lds_at(st + BM * 128 + (wc * NI * 16 + c) * 128 + sw) + ni * 2048);
         } else {
           const int h = ((c >> 2) | g << 2) & (kPairs - 1);
-          const unsigned char* p = st + BM * 128 + (ks * 32 + 8 * g + (c >> 2)) * (BN * 2) +
-                                   ((wc * NI + ni) ^ h) * 32 + (c & 3) * 8;
-          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((RLD_LDS s16x4*)p);
-          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (RLD_LDS s16x4*)(p + 4 * BN * 2));
-          const uint2 l2 = __builtin_bit_cast(uint2, lo), h2 = __builtin_bit_cast(uint2, hi);
-          wf[ni] = make_uint4(l2.x, l2.y, h2.x, h2.y);
+          wf[ni] = lds_tr16(lds_at(st + BM * 128 + (ks * 32 + 8 * g + (c >> 2)) * (BN * 2) +
+                                   ((wc * NI + ni) ^ h) * 32 + (c & 3) * 8),
+                            4 * BN * 2);
         }
       }
 #pragma unroll
@@ -720,22 +613,186 @@ __device__ __forceinline__ void tile_body(const TileArgs& a) {
           acc[ni][mi] = mfma_bf16_16x16x32(wf[ni], xf[mi], acc[ni][mi]);
     }
   }
+  wait_vm<0>();  // the loads past the end, of zeros
 
-  wait_vm<0>();  // the loads past K, of zeros
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) {
+    const uint32_t r = (wr * MI + mi) * 16 + c;
+    if (r >= rows) continue;
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) {
+      const uint32_t col = col0 + (wc * NI + ni) * 16 + 4 * g;
+      if (col < a.N)
+        *gp<floatx4>(a.sum_ + (((uint64_t)split * a.n + row0 + r) * a.N + col) * 4) = acc[ni][mi];
+    }
+  }
+}
 
-  uint32_t rows_at[MI], cols_at[NI];
+// ----------------------------------------------------------------- finish ----
+
+struct FinishArgs {
+  uint64_t sum_, out_;     // fp32 [splits][n][N]; the output
+  uint64_t order_;         // sorted positions' rows, or 0: positions are rows
+  uint64_t key_;           // slots by position (raw ids if order_ is 0)
+  uint64_t etab_, otab_, stab_;
+  uint64_t parts_;         // bf16 [n][2][R], or 0: from
+  uint64_t partial_;       // fp32 [nch][n][R]; by row, or by position with low_sorted
+  uint32_t os, n, N, R, splits, nch, max_loras, tiles;  // tiles: of 64 columns
+  uint32_t low_sorted;
+};
+
+// 16 positions x 64 columns, 16 columns a wave: the splits of the product, in
+// order, plus the low rows times their slots' second matrices.  A slot's
+// product is made apart and added to its own rows alone (a NaN or infinity of
+// its matrix would survive zeros in the others).  KS: 32-wide steps of rank.
+template <int KS, bool TRANS>
+__device__ __forceinline__ void finish_item(const FinishArgs& a, uint32_t item) {
+  constexpr int SB = KS == 1 ? 8 : KS == 2 ? 4 : 2;  // slots whose matrices are loaded at once
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, c = lane & 15;
+  const uint32_t col0 = item % a.tiles * 64 + wave * 16;
+  const uint32_t pos0 = item / a.tiles * 16;
+  if (col0 >= a.N) return;
+  const uint32_t pos = pos0 + c, at = min(pos, a.n - 1);
+  int key = gp<const int32_t>(a.key_)[at];
+  const uint32_t row = a.order_ ? (uint32_t)gp<const int32_t>(a.order_)[at] : at;
+  if (pos >= a.n || key < 0 || (uint32_t)key >= a.max_loras) key = -1;
+  const uint32_t col = col0 + 4 * g;
+  const bool in_col = col < a.N;
+
+  floatx4 acc = floatx4{0.f, 0.f, 0.f, 0.f};
+  for (uint32_t sp = 0; sp < a.splits; sp += 4) {
+    floatx4 v[4];
 #pragma unroll
-  for (int mi = 0; mi < MI; ++mi) rows_at[mi] = (wr * MI + mi) * 16;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = min(sp + i, a.splits - 1);
+      v[i] = gp<const floatx4>(
+          a.sum_ + (((uint64_t)w * a.n + row) * a.N + (in_col ? col : 0u)) * 4)[0];
+    }
 #pragma unroll
-  for (int ni = 0; ni < NI; ++ni) cols_at[ni] = (wc * NI + ni) * 16;
-  add_low<MI, NI, TRANS>(a, acc, row0, col0, rows_at, cols_at);
-  store_tile<MI, NI>(a, acc, row0, col0, rows_at, cols_at);
+    for (int i = 0; i < 4; ++i)
+      if (sp + i < a.splits) acc += v[i];
+  }
+  uint64_t e = 0;
+  if (key >= 0) {
+    e = gp<const uint64_t>(a.etab_)[key];
+    if (e == 0ull || gp<const uint64_t>(a.otab_)[key] == 0ull) key = -1;
+  }
+  const uint32_t lat = a.low_sorted ? pos : row;
+  uint64_t left = __ballot(key >= 0 && lane < 16);
+  if (left) {
+    uint4 hi[KS], lo[KS];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const uint32_t k = ks * 32 + 8 * g;
+      hi[ks] = lo[ks] = zero16();
+      if (key >= 0 && k < a.R) {
+        if (a.parts_) {
+          const RLD_GLOBAL uint16_t* p = gp<const uint16_t>(a.parts_) + (size_t)lat * 2 * a.R + k;
+          hi[ks] = load16(p);
+          lo[ks] = load16(p + a.R);
+        } else {
+          floatx4 u = {}, v = {};
+          for (uint32_t ch = 0; ch < a.nch; ++ch) {
+            const RLD_GLOBAL floatx4* p =
+                gp<const floatx4>(a.partial_ + (((size_t)ch * a.n + lat) * a.R + k) * 4);
+            u += p[0];
+            v += p[1];
+          }
+          const float sc = gp<const float>(a.stab_)[key];
+          float f[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f[i] = u[i] * sc;
+            f[4 + i] = v[i] * sc;
+          }
+          uint4 two[2];
+          bf16_parts<2>(f, two);
+          hi[ks] = two[0];
+          lo[ks] = two[1];
+        }
+      }
+    }
+    while (left) {
+      int s[SB];
+      uint4 ef[SB][KS];
+#pragma unroll
+      for (int b = 0; b < SB; ++b) {
+        // none left: the last slot again, its product not added
+        const int from = left ? __builtin_ctzll(left) : 0;
+        s[b] = left ? __builtin_amdgcn_readlane(key, from) : -2;
+        const uint64_t eb = left ? (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)e, from) |
+                                       (uint64_t)(uint32_t)__builtin_amdgcn_readlane(
+                                           (int)(uint32_t)(e >> 32), from) << 32
+                                 : 0ull;
+        left &= ~__ballot(key == s[b]);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint32_t k = ks * 32 + 8 * g;
+          const bool in = s[b] >= 0 && k < a.R && col0 + c < a.N;
+          if constexpr (!TRANS) {
+            ef[b][ks] = buffer_load16(eb + (uint64_t)col0 * a.R * 2, s[b] >= 0 ? kBufferEnd : 0u,
+                                      in ? (c * a.R + k) * 2 : kBufferEnd);
+          } else {
+            uint32_t w[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              w[q] = buffer_load2(eb + ((uint64_t)(ks * 32 + q) * a.N + col0) * 2,
+                                  s[b] >= 0 ? kBufferEnd : 0u,
+                                  in ? 16 * g * a.N + c * 2 : kBufferEnd);
+            ef[b][ks] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16,
+                                   w[6] | w[7] << 16);
+          }
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < SB; ++b) {
+        floatx4 t = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          t = mfma_bf16_16x16x32(ef[b][ks], lo[ks], t);
+          t = mfma_bf16_16x16x32(ef[b][ks], hi[ks], t);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] += key == s[b] ? t[i] : 0.f;
+      }
+    }
+  }
+  if (pos < a.n && in_col)
+    *gp<uint2v>(a.out_ + ((size_t)row * a.os + col) * 2) =
+        uint2v{pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3])};
+}
+
+// Work on a product that no other work of the call waits for goes out together:
+// first the product's tiles, then the low rows (u, g), then the sort.
+struct StartArgs {
+  PartArgs part;
+  LowArgs u, g;
+  SortArgs sort;
+  uint32_t parts, us, gs, sorts;  // blocks of each
+};
+
+template <int BM, int BN, int WR, int WC, int STAGES, bool TRANS>
+__device__ __forceinline__ void start_body(const StartArgs& a) {
+  constexpr int kTile = STAGES * (BM + BN) * 128, kLow = (int)sizeof(LowSmem);
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[kTile > kLow ? kTile : kLow];
+  uint32_t b = blockIdx.x;
+  if (b < a.parts) return part_item<BM, BN, WR, WC, STAGES, TRANS>(a.part, b, lds);
+  b -= a.parts;
+  if (b < a.us) return low_item<false>(a.u, b, *reinterpret_cast<LowSmem*>(lds));
+  b -= a.us;
+  if (TRANS && b < a.gs) return low_item<true>(a.g, b, *reinterpret_cast<LowSmem*>(lds));
+  b -= a.gs;
+  sort_item(a.sort, b, reinterpret_cast<uint32_t*>(lds));
 }
 
 template <int BM, int BN, int WR, int WC, int STAGES, bool TRANS>
-__global__ void __launch_bounds__(64 * WR * WC) tile_kernel(TileArgs a) {
-  tile_body<BM, BN, WR, WC, STAGES, TRANS>(a);
+__global__ void __launch_bounds__(256, 2) start_kernel(StartArgs a) {
+  start_body<BM, BN, WR, WC, STAGES, TRANS>(a);
 }
+
+// ------------------------------------------------------------- large tiles ----
 
 // A 256 x 256 tile by 2 x 4 waves of 128 x 64, for grids that fill the chip.
 //
@@ -775,9 +832,9 @@ __device__ __forceinline__ void big_tile_body(const TileArgs& a) {
   const uint32_t row0 = (patch * 4 + in % high) * 256, col0 = in / high * 256;
 
   const uint32_t rows = min(256u, a.n - row0), cols = min(256u, a.N - col0);
-  const uint32_t first = a.keep ? row0 : 0u;
+  const uint32_t first = a.order_ ? 0u : row0;
   const rsrc_t rx = buffer(a.x_ + (uint64_t)first * a.xs * 2,
-                           ((uint64_t)((a.keep ? rows : a.n) - 1) * a.xs + a.K) * 2);
+                           ((uint64_t)((a.order_ ? a.n : rows) - 1) * a.xs + a.K) * 2);
   const rsrc_t rw0 =
       buffer(a.w_ + (uint64_t)col0 * a.ws * 2, ((uint64_t)(cols - 1) * a.ws + a.K) * 2);
   // The slot of the first row: its low rows and second matrix are loaded as if
@@ -794,7 +851,7 @@ __device__ __forceinline__ void big_tile_body(const TileArgs& a) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t hr = h * 128 + r;
-      const uint32_t o = (uint32_t)gp<const int32_t>(a.order_)[row0 + min(hr, rows - 1)] - first;
+      const uint32_t o = tile_row(a, row0 + min(hr, rows - 1), first);
       vx[h][p] = hr < rows ? o * a.xs * 2 + q * 16 : kOutside;
       if constexpr (!TRANS) {
         vw[h][p] = (h * 128 + r) * a.ws * 2 + q * 16;
@@ -1113,152 +1170,12 @@ __global__ void __launch_bounds__(512) big_tile_kernel(TileArgs a) {
   big_tile_body<TRANS>(a);
 }
 
-// ------------------------------------------------------------------- rows ----
-
-struct RowsArgs {
-  uint64_t x_, w_, out_, seq_, partial_, atab_, btab_, stab_;
-  uint32_t xs, ws, os, n, K, N, R, nch, max_loras;
-};
-
-constexpr int kRowsWaves = 8;
-constexpr uint32_t kRowsMax = 64;  // rows of the calls that take this kernel
-
-// Up to 16 * MI <= 64 rows: a block makes 16 output columns of all of them.  W
-// is read once, straight into fragments (nothing of it is shared); its waves
-// take every eighth pair of 32-wide k steps, so that a wave reads whole cache
-// lines.  While the first loads fly the block adds up the low rows' chunks
-// into LDS; the slots are dealt to the waves, which add their products to
-// their own partial sums, and the eight sums meet in LDS.
-template <int MI>
-__global__ void __launch_bounds__(64 * kRowsWaves) rows_kernel(RowsArgs a) {
-  constexpr int U = MI == 1 ? 8 : 4;  // k steps loaded at once
-  constexpr int kRed = kRowsWaves * MI * kWave * 16;
-  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // kRed, or the low parts
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int g = lane >> 4, c = lane & 15;
-  const uint32_t col0 = blockIdx.x * 16;
-  const uint32_t cols = min(16u, a.N - col0);
-  const uint64_t wb = a.w_ + (uint64_t)col0 * a.ws * 2;
-
-  uint4 wf[U], xf[U][MI], wn[U], xn[U][MI];
-  auto load = [&](uint32_t ks0, uint4 (&w)[U], uint4 (&x)[U][MI]) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t k = (ks0 + ((u >> 1) * kRowsWaves + wave) * 2 + (u & 1)) * 32 + g * 8;
-      w[u] = buffer_load16(wb, kBufferEnd,
-                           (k < a.K && (uint32_t)c < cols) ? (c * a.ws + k) * 2 : kBufferEnd);
-#pragma unroll
-      for (int mi = 0; mi < MI; ++mi) {
-        const uint32_t r = mi * 16 + c;
-        x[u][mi] = buffer_load16(a.x_, kBufferEnd,
-                                 (k < a.K && r < a.n) ? (r * a.xs + k) * 2 : kBufferEnd);
-      }
-    }
-  };
-  const uint32_t nks = (a.K + 31) / 32;
-  load(0, wf, xf);
-
-  // a lane's slot, -1 for base rows and behind the last
-  int key = (uint32_t)lane < a.n ? gp<const int32_t>(a.seq_)[lane] : -1;
-  if (key < 0 || (uint32_t)key >= a.max_loras) key = -1;
-  {
-    const uint64_t ta = gp<const uint64_t>(a.atab_)[key < 0 ? 0 : key];
-    const uint64_t tb = gp<const uint64_t>(a.btab_)[key < 0 ? 0 : key];
-    if (ta == 0ull || tb == 0ull) key = -1;
-  }
-  __shared__ int keys[kRowsMax];
-  __shared__ float scales[kRowsMax];
-  if (wave == 0) {
-    keys[lane] = key;
-    scales[lane] = key >= 0 ? gp<const float>(a.stab_)[key] : 0.f;
-  }
-  __syncthreads();
-  // the low rows' parts, [row][2][R + 8] bf16 behind the waves' sums
-  uint16_t* const parts = reinterpret_cast<uint16_t*>(smem + kRed);
-  const uint32_t ps = a.R + 8;
-  const uint32_t q = a.R / 4;
-  for (uint32_t t = threadIdx.x; t < a.n * q; t += 64 * kRowsWaves) {
-    const uint32_t row = t / q, col = t % q * 4;
-    floatx4 v = {};
-    if (keys[row] >= 0) {
-      for (uint32_t ch = 0; ch < a.nch; ++ch)
-        v += gp<const floatx4>(a.partial_)[(size_t)ch * a.n * q + t];
-    }
-    v *= scales[row];
-    const uint32_t h0 = pack_bf16x2(v[0], v[1]), h1 = pack_bf16x2(v[2], v[3]);
-    *reinterpret_cast<uint2*>(parts + row * 2 * ps + col) = make_uint2(h0, h1);
-    *reinterpret_cast<uint2*>(parts + (row * 2 + 1) * ps + col) = make_uint2(
-        pack_bf16x2(v[0] - bf16_to_f32(h0 & 0xffffu), v[1] - bf16_to_f32(h0 >> 16)),
-        pack_bf16x2(v[2] - bf16_to_f32(h1 & 0xffffu), v[3] - bf16_to_f32(h1 >> 16)));
-  }
-
-  floatx4 acc[MI];
-#pragma unroll
-  for (int mi = 0; mi < MI; ++mi) acc[mi] = floatx4{0.f, 0.f, 0.f, 0.f};
-  auto multiply = [&](const uint4 (&w)[U], const uint4 (&x)[U][MI]) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int mi = 0; mi < MI; ++mi) acc[mi] = mfma_bf16_16x16x32(w[u], x[u][mi], acc[mi]);
-  };
-  constexpr uint32_t kStep = kRowsWaves * U;
-  for (uint32_t ks = 0; ks < nks; ks += 2 * kStep) {
-    load(ks + kStep, wn, xn);  // zeros past K
-    multiply(wf, xf);
-    load(ks + 2 * kStep, wf, xf);
-    multiply(wn, xn);
-  }
-
-  __syncthreads();
-  uint64_t left = __ballot(key >= 0);
-  for (int idx = 0; left; ++idx) {
-    const int s = __builtin_amdgcn_readlane(key, __builtin_ctzll(left));
-    const uint64_t mine = __ballot(key == s);
-    left &= ~mine;
-    if (idx % kRowsWaves != wave) continue;
-    const uint64_t e = uniform64(gp<const uint64_t>(a.btab_)[s]) + (uint64_t)col0 * a.R * 2;
-    for (uint32_t k0 = 0; k0 < a.R; k0 += 32) {
-      const uint32_t k = k0 + 8 * g;
-      const bool in = k < a.R;
-      const uint4 ef = buffer_load16(e, kBufferEnd,
-                                     (in && (uint32_t)c < cols) ? (c * a.R + k) * 2 : kBufferEnd);
-#pragma unroll
-      for (int mi = 0; mi < MI; ++mi) {
-        const uint32_t r = mi * 16 + c;
-        const bool own = (mine >> r) & 1;
-        uint4 hi = zero16(), lo = zero16();
-        if (own && in) {
-          hi = *reinterpret_cast<const uint4*>(parts + r * 2 * ps + k);
-          lo = *reinterpret_cast<const uint4*>(parts + (r * 2 + 1) * ps + k);
-        }
-        floatx4 t = mfma_bf16_16x16x32(ef, lo, floatx4{0.f, 0.f, 0.f, 0.f});
-        t = mfma_bf16_16x16x32(ef, hi, t);
-        // its own rows alone: a NaN or infinity of the matrix survives the zeros
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[mi][i] += own ? t[i] : 0.f;
-      }
-    }
-  }
-  floatx4* const red = reinterpret_cast<floatx4*>(smem);
-#pragma unroll
-  for (int mi = 0; mi < MI; ++mi) red[(wave * MI + mi) * kWave + lane] = acc[mi];
-  __syncthreads();
-  if (wave >= MI) return;
-  floatx4 v = red[wave * kWave + lane];
-#pragma unroll
-  for (int w = 1; w < kRowsWaves; ++w) v += red[(w * MI + wave) * kWave + lane];
-  const uint32_t r = wave * 16 + c, col = 4 * g;
-  if (r < a.n && col < cols)
-    *gp<uint2v>(a.out_ + ((size_t)r * a.os + col0 + col) * 2) =
-        uint2v{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-}
-
 // ------------------------------------------------------------------ wgrad ----
 
 struct WgradArgs {
   uint64_t v_, low_, order_, span_, dtab_;
   uint32_t vs, width, R, tiles, accumulate;
+  uint32_t low_sorted;  // low rows by position (else by row)
 };
 
 struct WgradSmem {
@@ -1285,7 +1202,7 @@ __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, Wg
   const uint32_t begin = gp<const uint32_t>(a.span_)[2 * s];
   const uint32_t cnt = gp<const uint32_t>(a.span_)[2 * s + 1];
   const RLD_GLOBAL int32_t* order = gp<const int32_t>(a.order_) + begin;
-  const RLD_GLOBAL float* low = gp<const float>(a.low_) + (size_t)begin * a.R;
+  const RLD_GLOBAL float* low = gp<const float>(a.low_);
 
   floatx4 acc[RT][4];
 #pragma unroll
@@ -1305,6 +1222,12 @@ __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, Wg
       __builtin_amdgcn_global_load_lds((const void*)(in ? src : (uint64_t)&g_zero16[0]),
                                        (RLD_LDS void*)(&stage[wave][p * 1024]), 16, 0, 0);
     }
+    uint32_t at[8];  // where the low rows of this lane's positions lie
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t i = min(i0 + 8 * g + e, cnt - 1);
+      at[e] = a.low_sorted ? begin + i : (uint32_t)order[i];
+    }
     uint4 lf[RT][3];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -1313,7 +1236,7 @@ __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, Wg
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const uint32_t i = i0 + 8 * g + e;
-        v[e] = (i < cnt && r < a.R) ? low[(size_t)i * a.R + r] : 0.f;
+        v[e] = (i < cnt && r < a.R) ? low[(size_t)at[e] * a.R + r] : 0.f;
       }
       bf16_parts<3>(v, lf[rt]);
     }
@@ -1359,20 +1282,27 @@ __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, Wg
   }
 }
 
-// dA and dB in one launch: the first `items` blocks make dA.
+// dA, dB and, behind them, the last part of dx in one launch: the first `ia`
+// blocks make dA, the next `ib` dB.
 template <int RT>
-__global__ void __launch_bounds__(256) wgrad_kernel(WgradArgs da, WgradArgs db, uint32_t items) {
+__global__ void __launch_bounds__(256) end_kernel(WgradArgs da, WgradArgs db, FinishArgs fin,
+                                                  uint32_t ia, uint32_t ib) {
   __shared__ WgradSmem sm;
-  if (blockIdx.x < items) wgrad_item<RT, false>(da, blockIdx.x, sm);
-  else wgrad_item<RT, true>(db, blockIdx.x - items, sm);
+  constexpr int KS = RT < 2 ? 1 : RT / 2;
+  if (blockIdx.x < ia) wgrad_item<RT, false>(da, blockIdx.x, sm);
+  else if (blockIdx.x < ia + ib) wgrad_item<RT, true>(db, blockIdx.x - ia, sm);
+  else finish_item<KS, true>(fin, blockIdx.x - ia - ib);
+}
+
+template <int KS>
+__global__ void __launch_bounds__(256) finish_kernel(FinishArgs a) {
+  finish_item<KS, false>(a, blockIdx.x);
 }
 
 // ------------------------------------------------------------------- host ----
 
 static inline size_t round16(size_t v) { return (v + 15) & ~(size_t)15; }
 
-// The workspace: [order][slots by position][spans] and, for u and g, [low rows
-// (fp32 or two bf16 parts: 4 bytes a value)][chunk sums].
 struct LowPlan {
   uint32_t nch;
   size_t low, partial;  // bytes
@@ -1382,41 +1312,63 @@ static LowPlan low_plan(uint32_t n, uint32_t K, uint32_t R) {
   LowPlan p;
   p.nch = div_ceil(K, kLowChunk);
   p.low = round16((size_t)n * R * 4);
-  p.partial = (size_t)p.nch * n * R * 4;
+  p.partial = round16((size_t)p.nch * n * R * 4);
+  return p;
+}
+
+// How a product of n rows, K and N columns is cut.
+struct TilePlan {
+  bool big;         // 256 x 256 tiles, which also finish their outputs
+  uint32_t bm, bn;  // otherwise: tiles of a part,
+  uint32_t tiles_m, tiles_n, splits, steps;  // and its splits of `steps` x 64 of K
+  size_t sums;      // bytes of the splits' sums
+};
+
+static TilePlan tile_plan(uint32_t n, uint32_t K, uint32_t N) {
+  TilePlan p = {};
+  const uint64_t big = (uint64_t)div_ceil(n, 256) * div_ceil(N, 256);
+  p.big = big >= kBigTiles && N > 128;
+  if (p.big) {
+    p.tiles_m = div_ceil(n, 256);
+    p.tiles_n = div_ceil(N, 256);
+    return p;
+  }
+  p.bm = n <= 16 ? 16 : n <= 32 ? 32 : n <= 128 ? 64 : 128;
+  p.bn = n <= 128 ? 64 : 128;
+  p.tiles_m = div_ceil(n, p.bm);
+  p.tiles_n = div_ceil(N, p.bn);
+  // two blocks a CU, of at least four steps each
+  const uint32_t tiles = p.tiles_m * p.tiles_n, steps = div_ceil(K, 64);
+  uint32_t s = tiles >= 512 ? 1 : 512 / tiles;
+  if (s > steps / 4) s = steps / 4;
+  if (s > 16) s = 16;
+  if (s < 1) s = 1;
+  p.steps = div_ceil(steps, s);
+  p.splits = div_ceil(steps, p.steps);
+  p.sums = round16((size_t)p.splits * n * N * 4);
   return p;
 }
 
 static size_t sort_bytes(uint32_t n, uint32_t max_loras) {
-  return 2 * round16((size_t)n * 4) + round16((size_t)max_loras * 8);
+  return 3 * round16((size_t)n * 4) + round16((size_t)max_loras * 8);
 }
 
-struct Sorted {
-  uint64_t order, key, span;
-  bool keep;
-};
-
-// Sorts the rows; wide: the largest row stride that the tiles reach through
-// 32-bit offsets.
-static int launch_sort(const rld_route* r, const int32_t* seq, uint32_t n, uint32_t wide,
-                       uint64_t workspace, Sorted* out, hipStream_t st) {
-  out->order = workspace;
-  out->key = out->order + round16((size_t)n * 4);
-  out->span = out->key + round16((size_t)n * 4);
-  out->keep = (uint64_t)n * wide * 2 > kGatherSpan;
+static SortArgs sort_args(const rld_route* r, const int32_t* seq, uint32_t n,
+                          uint64_t workspace) {
   SortArgs a;
   a.seq_ = (uint64_t)seq;
   a.atab_ = (uint64_t)r->a_table;
   a.btab_ = (uint64_t)r->b_table;
-  a.order_ = out->order;
-  a.skey_ = out->key;
-  a.span_ = out->span;
+  a.order_ = workspace;
+  a.skey_ = a.order_ + round16((size_t)n * 4);
+  a.rkey_ = a.skey_ + round16((size_t)n * 4);
+  a.span_ = a.rkey_ + round16((size_t)n * 4);
   a.n = n;
   a.max_loras = r->max_loras;
-  a.keep = out->keep ? 1u : 0u;
-  sort_kernel<<<r->max_loras + 1, 256, 0, st>>>(a);
-  return launch_status();
+  return a;
 }
 
+// order 0: low rows by row, key slots by row.
 static LowArgs low_args(const rld_route* r, bool trans, const void* x, uint32_t xs, uint32_t n,
                         uint64_t order, uint64_t key, uint64_t low, uint64_t parts,
                         uint64_t partial) {
@@ -1439,7 +1391,7 @@ static LowArgs low_args(const rld_route* r, bool trans, const void* x, uint32_t 
   a.tiles = div_ceil(n, kLowRows);
   // few items: the slots of a tile go to several blocks
   const uint32_t items = a.tiles * a.nch;
-  a.nz = items >= 1024u ? 1u : div_ceil(1024u, items);
+  a.nz = items >= 1024u ? 1u : div_ceil(1024u, items ? items : 1u);
   if (a.nz > r->max_loras) a.nz = r->max_loras;
   if (a.nz > n) a.nz = n;
   if (a.nz > kLowRows) a.nz = kLowRows;
@@ -1451,18 +1403,80 @@ static uint32_t sum_blocks(const LowArgs& a) {
   return (uint32_t)(((uint64_t)a.n * (a.R / 4) + 255) / 256);
 }
 
+// Whether the low products are worth waiting for the sort.  Unsorted, every 64
+// rows may name every slot and read its matrix again (from cache); the sort
+// takes 5 us by itself, in which some 50 MB are read so.
+static bool sort_first(const rld_route* r, uint32_t n, uint32_t K) {
+  const uint64_t slots = r->max_loras < kLowRows ? r->max_loras : kLowRows;
+  return (uint64_t)(div_ceil(n, kLowRows) - 1) * slots * r->max_rank * K * 2 > (50ull << 20);
+}
+
 template <bool TRANS>
-static int launch_tiles(const rld_route* r, const void* w, uint32_t ws, const void* x,
-                        uint32_t xs, const Sorted& so, uint32_t n, uint64_t parts, void* out,
-                        uint32_t os, hipStream_t st) {
+static int launch_start(const TilePlan& p, const StartArgs& a, hipStream_t st) {
+  const uint32_t grid = a.parts + a.us + a.gs + a.sorts;
+  if (p.bm == 16) start_kernel<16, 64, 1, 4, 4, TRANS><<<grid, 256, 0, st>>>(a);
+  else if (p.bm == 32) start_kernel<32, 64, 1, 4, 4, TRANS><<<grid, 256, 0, st>>>(a);
+  else if (p.bm == 64) start_kernel<64, 64, 2, 2, 4, TRANS><<<grid, 256, 0, st>>>(a);
+  else start_kernel<128, 128, 2, 2, 2, TRANS><<<grid, 256, 0, st>>>(a);
+  return launch_status();
+}
+
+template <bool TRANS>
+static PartArgs part_args(const TilePlan& p, const void* w, uint32_t ws, const void* x,
+                          uint32_t xs, uint32_t n, uint32_t K, uint32_t N, uint64_t sums) {
+  PartArgs a;
+  a.x_ = (uint64_t)x;
+  a.w_ = (uint64_t)w;
+  a.sum_ = sums;
+  a.xs = xs;
+  a.ws = ws;
+  a.n = n;
+  a.K = K;
+  a.N = N;
+  a.tiles_m = p.tiles_m;
+  a.tiles_n = p.tiles_n;
+  a.splits = p.splits;
+  a.steps = p.steps;
+  return a;
+}
+
+static FinishArgs finish_args(const rld_route* r, bool trans, const TilePlan& p, uint64_t sums,
+                              uint64_t order, uint64_t key, uint64_t parts, uint64_t partial,
+                              uint32_t nch, bool low_sorted, void* out, uint32_t os, uint32_t n) {
+  FinishArgs a;
+  a.sum_ = sums;
+  a.out_ = (uint64_t)out;
+  a.order_ = order;
+  a.key_ = key;
+  a.etab_ = (uint64_t)(trans ? r->a_table : r->b_table);
+  a.otab_ = (uint64_t)(trans ? r->b_table : r->a_table);
+  a.stab_ = (uint64_t)r->scale_table;
+  a.parts_ = parts;
+  a.partial_ = partial;
+  a.os = os;
+  a.n = n;
+  a.N = trans ? r->k_in : r->n_out;
+  a.R = r->max_rank;
+  a.splits = p.splits;
+  a.nch = nch;
+  a.max_loras = r->max_loras;
+  a.tiles = div_ceil(a.N, 64);
+  a.low_sorted = low_sorted ? 1u : 0u;
+  return a;
+}
+
+template <bool TRANS>
+static int launch_big(const rld_route* r, const TilePlan& p, const void* w, uint32_t ws,
+                      const void* x, uint32_t xs, uint64_t order, uint64_t key, uint32_t n,
+                      uint64_t parts, void* out, uint32_t os, hipStream_t st) {
   TileArgs a;
   a.x_ = (uint64_t)x;
   a.w_ = (uint64_t)w;
   a.out_ = (uint64_t)out;
   a.parts_ = parts;
   a.etab_ = (uint64_t)(TRANS ? r->a_table : r->b_table);
-  a.order_ = so.order;
-  a.skey_ = so.key;
+  a.order_ = order;
+  a.skey_ = key;
   a.xs = xs;
   a.ws = ws;
   a.os = os;
@@ -1470,30 +1484,14 @@ static int launch_tiles(const rld_route* r, const void* w, uint32_t ws, const vo
   a.K = TRANS ? r->n_out : r->k_in;
   a.N = TRANS ? r->k_in : r->n_out;
   a.R = r->max_rank;
-  a.keep = so.keep ? 1u : 0u;
-  const uint32_t big = div_ceil(n, 256) * div_ceil(a.N, 256);
-  if (big >= kBigTiles) {
-    a.tiles_m = div_ceil(n, 256);
-    a.tiles_n = div_ceil(a.N, 256);
-    big_tile_kernel<TRANS><<<xcd_grid(big), 512, 0, st>>>(a);
-  } else if (n > 128) {
-    a.tiles_m = div_ceil(n, 128);
-    a.tiles_n = div_ceil(a.N, 128);
-    tile_kernel<128, 128, 2, 2, 2, TRANS><<<a.tiles_m * a.tiles_n, 256, 0, st>>>(a);
-  } else {
-    a.tiles_m = div_ceil(n, 64);
-    a.tiles_n = div_ceil(a.N, 64);
-    tile_kernel<64, 64, 2, 2, 4, TRANS><<<a.tiles_m * a.tiles_n, 256, 0, st>>>(a);
-  }
+  a.tiles_m = p.tiles_m;
+  a.tiles_n = p.tiles_n;
+  big_tile_kernel<TRANS><<<xcd_grid(a.tiles_m * a.tiles_n), 512, 0, st>>>(a);
   return launch_status();
 }
 
-template <int MI>
-static int launch_rows(const RowsArgs& a, hipStream_t st) {
-  const uint32_t lds = kRowsWaves * MI * kWave * 16 + a.n * 2 * (a.R + 8) * 2;
-  rows_kernel<MI><<<div_ceil(a.N, 16), 64 * kRowsWaves, lds, st>>>(a);
-  return launch_status();
-}
+// Rows that large tiles cannot reach in any order through 32-bit offsets.
+static bool too_far(uint32_t n, uint32_t stride) { return (uint64_t)n * stride * 2 > kGatherSpan; }
 
 static int check_wide(uint32_t stride) { return stride > kMaxStride ? RLD_EUNSUPPORTED : RLD_OK; }
 
@@ -1501,8 +1499,8 @@ static int check_wide(uint32_t stride) { return stride > kMaxStride ? RLD_EUNSUP
 static int check_items(const rld_route* r, uint32_t n) {
   const uint64_t k = r->k_in > r->n_out ? r->k_in : r->n_out;
   const uint64_t tiles = (k + 63) / 64;
-  if (k > (1u << 24) || div_ceil(n, 64) * tiles >= (1u << 23) ||
-      r->max_loras * tiles >= (1u << 22) || (uint64_t)n * (r->max_rank / 4) >= (1u << 30))
+  if (n > (1u << 26) || k > (1u << 24) || div_ceil(n, 64) * tiles >= (1u << 23) ||
+      r->max_loras * tiles >= (1u << 21) || (uint64_t)n * (r->max_rank / 4) >= (1u << 30))
     return RLD_EUNSUPPORTED;
   return RLD_OK;
 }
@@ -1511,11 +1509,11 @@ static int check_items(const rld_route* r, uint32_t n) {
 
 using namespace rld;
 
-extern "C" size_t rld_proj_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t max_rank,
-                                           uint32_t max_loras) {
-  if (n == 0 || k_in == 0 || max_rank == 0 || max_loras == 0) return 0;
+extern "C" size_t rld_proj_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t n_out,
+                                           uint32_t max_rank, uint32_t max_loras) {
+  if (n == 0 || k_in == 0 || n_out == 0 || max_rank == 0 || max_loras == 0) return 0;
   const LowPlan p = low_plan(n, k_in, max_rank);
-  return sort_bytes(n, max_loras) + p.low + p.partial;
+  return sort_bytes(n, max_loras) + p.low + p.partial + tile_plan(n, k_in, n_out).sums;
 }
 
 extern "C" int rld_proj(const rld_route* route, const void* w, uint32_t w_row_stride,
@@ -1534,57 +1532,76 @@ extern "C" int rld_proj(const rld_route* route, const void* w, uint32_t w_row_st
       (e = check_wide(out_row_stride)))
     return e;
   if ((e = check_items(route, n))) return e;
-  if (workspace_bytes < rld_proj_workspace_bytes(n, route->k_in, route->max_rank, route->max_loras))
+  const uint32_t K = route->k_in, N = route->n_out, R = route->max_rank;
+  if (workspace_bytes < rld_proj_workspace_bytes(n, K, N, R, route->max_loras))
     return RLD_ENOSPACE;
-  const LowPlan p = low_plan(n, route->k_in, route->max_rank);
+  const LowPlan p = low_plan(n, K, R);
+  const TilePlan t = tile_plan(n, K, N);
   const uint64_t parts = (uint64_t)workspace + sort_bytes(n, route->max_loras);
   const uint64_t partial = parts + p.low;
+  const uint64_t sums = partial + p.partial;
+  const uint64_t seq = (uint64_t)seq_slot;
   const hipStream_t st = (hipStream_t)stream;
-  if (n <= kRowsMax) {
-    const LowArgs l = low_args(route, false, x, x_row_stride, n, 0, (uint64_t)seq_slot, 0, 0,
-                               partial);
+  const SortArgs sort = sort_args(route, seq_slot, n, (uint64_t)workspace);
+
+  if (t.big) {
+    sort_kernel<<<route->max_loras + 1, 256, 0, st>>>(sort);
+    if ((e = launch_status())) return e;
+    const bool keep = too_far(n, x_row_stride) || too_far(n, out_row_stride);
+    const uint64_t order = keep ? 0 : sort.order_, key = keep ? sort.rkey_ : sort.skey_;
+    const LowArgs l = low_args(route, false, x, x_row_stride, n, order, key, 0, parts,
+                               p.nch == 1 ? 0 : partial);
     low_kernel<<<low_items(l), 256, 0, st>>>(l);
     if ((e = launch_status())) return e;
-    RowsArgs a;
-    a.x_ = (uint64_t)x;
-    a.w_ = (uint64_t)w;
-    a.out_ = (uint64_t)out;
-    a.seq_ = (uint64_t)seq_slot;
-    a.partial_ = partial;
-    a.atab_ = (uint64_t)route->a_table;
-    a.btab_ = (uint64_t)route->b_table;
-    a.stab_ = (uint64_t)route->scale_table;
-    a.xs = x_row_stride;
-    a.ws = w_row_stride;
-    a.os = out_row_stride;
-    a.n = n;
-    a.K = route->k_in;
-    a.N = route->n_out;
-    a.R = route->max_rank;
-    a.nch = p.nch;
-    a.max_loras = route->max_loras;
-    return n <= 16 ? launch_rows<1>(a, st) : n <= 32 ? launch_rows<2>(a, st) : launch_rows<4>(a, st);
+    if (p.nch > 1) {
+      low_reduce_kernel<<<sum_blocks(l), 256, 0, st>>>(l, l, sum_blocks(l));
+      if ((e = launch_status())) return e;
+    }
+    return launch_big<false>(route, t, w, w_row_stride, x, x_row_stride, order, key, n, parts, out,
+                             out_row_stride, st);
   }
-  Sorted so;
-  const uint32_t wide = x_row_stride > out_row_stride ? x_row_stride : out_row_stride;
-  if ((e = launch_sort(route, seq_slot, n, wide, (uint64_t)workspace, &so, st))) return e;
-  const LowArgs l = low_args(route, false, x, x_row_stride, n, so.order, so.key, 0, parts,
-                             p.nch == 1 ? 0 : partial);
-  low_kernel<<<low_items(l), 256, 0, st>>>(l);
-  if ((e = launch_status())) return e;
-  if (p.nch > 1) {
+
+  // up to 64 rows no sort: a block of finish has 16 rows' slots at most
+  const bool sorted = n > 64, first = sorted && sort_first(route, n, K);
+  if (first) {
+    sort_kernel<<<route->max_loras + 1, 256, 0, st>>>(sort);
+    if ((e = launch_status())) return e;
+  }
+  // finish adds up the low rows' chunks itself while its column tiles are few
+  const uint64_t again = (uint64_t)div_ceil(N, 64) * n * R * 4 * p.nch;
+  const bool sum = again > (32ull << 20);
+  const LowArgs l = low_args(route, false, x, x_row_stride, n, first ? sort.order_ : 0,
+                             first ? sort.skey_ : seq, 0, parts, partial);
+  StartArgs s;
+  s.part = part_args<false>(t, w, w_row_stride, x, x_row_stride, n, K, N, sums);
+  s.u = l;
+  s.g = l;
+  s.sort = sort;
+  s.sorts = sorted && !first ? route->max_loras + 1 : 0u;
+  s.parts = t.tiles_m * t.tiles_n * t.splits;
+  s.us = low_items(l);
+  s.gs = 0;
+  if ((e = launch_start<false>(t, s, st))) return e;
+  if (sum) {
     low_reduce_kernel<<<sum_blocks(l), 256, 0, st>>>(l, l, sum_blocks(l));
     if ((e = launch_status())) return e;
   }
-  return launch_tiles<false>(route, w, w_row_stride, x, x_row_stride, so, n, parts, out,
-                             out_row_stride, st);
+  const FinishArgs f =
+      finish_args(route, false, t, sums, sorted ? sort.order_ : 0, sorted ? sort.skey_ : seq,
+                  sum ? parts : 0, partial, p.nch, first, out, out_row_stride, n);
+  const uint32_t grid = f.tiles * div_ceil(n, 16);
+  if (R <= 32) finish_kernel<1><<<grid, 256, 0, st>>>(f);
+  else if (R <= 64) finish_kernel<2><<<grid, 256, 0, st>>>(f);
+  else finish_kernel<4><<<grid, 256, 0, st>>>(f);
+  return launch_status();
 }
 
 extern "C" size_t rld_proj_grad_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t n_out,
                                                 uint32_t max_rank, uint32_t max_loras) {
   if (k_in == 0 || n_out == 0 || max_rank == 0 || max_loras == 0) return 0;
   const LowPlan u = low_plan(n, k_in, max_rank), g = low_plan(n, n_out, max_rank);
-  return sort_bytes(n, max_loras) + u.low + u.partial + 2 * g.low + g.partial;
+  return sort_bytes(n, max_loras) + u.low + u.partial + 2 * g.low + g.partial +
+         (n ? tile_plan(n, n_out, k_in).sums : 0);
 }
 
 extern "C" int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_row_stride,
@@ -1615,43 +1632,64 @@ extern "C" int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_r
     }
   }
   if ((e = check_items(route, n))) return e;
-  if (workspace_bytes < rld_proj_grad_workspace_bytes(n, route->k_in, route->n_out,
-                                                      route->max_rank, route->max_loras))
+  const uint32_t K = route->k_in, N = route->n_out, R = route->max_rank;
+  if (workspace_bytes < rld_proj_grad_workspace_bytes(n, K, N, R, route->max_loras))
     return RLD_ENOSPACE;
   if (n == 0 && !adapters) return RLD_OK;
-  const LowPlan pu = low_plan(n, route->k_in, route->max_rank);
-  const LowPlan pg = low_plan(n, route->n_out, route->max_rank);
+  const LowPlan pu = low_plan(n, K, R), pg = low_plan(n, N, R);
   const uint64_t ul = (uint64_t)workspace + sort_bytes(n, route->max_loras);
   const uint64_t usum = ul + pu.low;
   const uint64_t gl = usum + pu.partial;
   const uint64_t gparts = gl + pg.low;
   const uint64_t gsum = gparts + pg.low;
+  const uint64_t sums = gsum + pg.partial;
   const hipStream_t st = (hipStream_t)stream;
-  Sorted so;
-  uint32_t wide = dy_row_stride;
-  if (dx && dx_row_stride > wide) wide = dx_row_stride;
-  if ((e = launch_sort(route, seq_slot, n, wide, (uint64_t)workspace, &so, st))) return e;
-  if (n != 0) {
-    // u for dB; g for dx (as parts) and dA
-    const LowArgs u = low_args(route, false, x, x_row_stride, n, so.order, so.key, ul, 0,
-                               pu.nch == 1 ? 0 : usum);
-    const LowArgs g = low_args(route, true, dy, dy_row_stride, n, so.order, so.key,
-                               da_table ? gl : 0, dx ? gparts : 0, pg.nch == 1 ? 0 : gsum);
-    const bool want_u = db_table != nullptr, want_g = dx || da_table;
-    const uint32_t iu = want_u ? low_items(u) : 0u, ig = want_g ? low_items(g) : 0u;
+  const SortArgs sort = sort_args(route, seq_slot, n, (uint64_t)workspace);
+  const TilePlan t = n ? tile_plan(n, N, K) : TilePlan{};
+  const bool want_u = n && db_table, want_g = n && (dx || da_table);
+  const bool part = n && dx && !t.big;
+  // the sort first where the low products gain from it, or nothing else starts with it
+  const bool first = !part || sort_first(route, n, K > N ? K : N);
+  // low rows by sorted position, if they are sorted first and the large tiles
+  // can reach the rows so
+  const bool keep =
+      n && dx && t.big && (too_far(n, dy_row_stride) || too_far(n, dx_row_stride));
+  const bool by_pos = first && !keep;
+  const uint64_t order = by_pos ? sort.order_ : 0;
+  const uint64_t key = by_pos ? sort.skey_ : keep ? sort.rkey_ : (uint64_t)seq_slot;
+  // u for dB; g for dx (as parts) and dA
+  const LowArgs u = low_args(route, false, x, x_row_stride, n, order, key, ul, 0, usum);
+  const LowArgs g = low_args(route, true, dy, dy_row_stride, n, order, key, da_table ? gl : 0,
+                             dx ? gparts : 0, gsum);
+  const uint32_t iu = want_u ? low_items(u) : 0u, ig = want_g ? low_items(g) : 0u;
+  if (first) {
+    sort_kernel<<<route->max_loras + 1, 256, 0, st>>>(sort);
+    if ((e = launch_status())) return e;
+  }
+  if (part) {
+    StartArgs s;
+    s.part = part_args<true>(t, w, w_row_stride, dy, dy_row_stride, n, N, K, sums);
+    s.u = u;
+    s.g = g;
+    s.sort = sort;
+    s.sorts = first ? 0u : route->max_loras + 1;
+    s.parts = t.tiles_m * t.tiles_n * t.splits;
+    s.us = iu;
+    s.gs = ig;
+    if ((e = launch_start<true>(t, s, st))) return e;
+  } else if (iu + ig) {
     low_pair_kernel<<<iu + ig, 256, 0, st>>>(u, g, iu);
     if ((e = launch_status())) return e;
-    const uint32_t bu = want_u && pu.nch > 1 ? sum_blocks(u) : 0u;
-    const uint32_t bg = want_g && pg.nch > 1 ? sum_blocks(g) : 0u;
-    if (bu + bg) {
-      low_reduce_kernel<<<bu + bg, 256, 0, st>>>(u, g, bu);
-      if ((e = launch_status())) return e;
-    }
-    if (dx && (e = launch_tiles<true>(route, w, w_row_stride, dy, dy_row_stride, so, n, gparts, dx,
-                                      dx_row_stride, st)))
-      return e;
   }
-  if (!adapters) return RLD_OK;
+  if (iu + ig) {
+    const uint32_t bu = want_u ? sum_blocks(u) : 0u, bg = want_g ? sum_blocks(g) : 0u;
+    low_reduce_kernel<<<bu + bg, 256, 0, st>>>(u, g, bu);
+    if ((e = launch_status())) return e;
+  }
+  if (n && dx && t.big &&
+      (e = launch_big<true>(route, t, w, w_row_stride, dy, dy_row_stride, order, key, n, gparts,
+                            dx, dx_row_stride, st)))
+    return e;
   WgradArgs a, b;
   a.v_ = (uint64_t)x;
   b.v_ = (uint64_t)dy;
@@ -1661,19 +1699,24 @@ extern "C" int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_r
   b.low_ = ul;
   a.dtab_ = (uint64_t)da_table;
   b.dtab_ = (uint64_t)db_table;
-  a.width = route->k_in;
-  b.width = route->n_out;
-  a.order_ = b.order_ = so.order;
-  a.span_ = b.span_ = so.span;
-  a.R = b.R = route->max_rank;
+  a.width = K;
+  b.width = N;
+  a.order_ = b.order_ = sort.order_;
+  a.span_ = b.span_ = sort.span_;
+  a.R = b.R = R;
   a.accumulate = b.accumulate = accumulate ? 1u : 0u;
+  a.low_sorted = b.low_sorted = by_pos ? 1u : 0u;
   a.tiles = div_ceil(a.width, 64);
   b.tiles = div_ceil(b.width, 64);
   const uint32_t ia = da_table ? a.tiles * route->max_loras : 0u;
   const uint32_t ib = db_table ? b.tiles * route->max_loras : 0u;
-  if (a.R <= 16) wgrad_kernel<1><<<ia + ib, 256, 0, st>>>(a, b, ia);
-  else if (a.R <= 32) wgrad_kernel<2><<<ia + ib, 256, 0, st>>>(a, b, ia);
-  else if (a.R <= 64) wgrad_kernel<4><<<ia + ib, 256, 0, st>>>(a, b, ia);
-  else wgrad_kernel<8><<<ia + ib, 256, 0, st>>>(a, b, ia);
+  const FinishArgs f = finish_args(route, true, t, sums, sort.order_, sort.skey_, gparts, 0, 0, by_pos, dx,
+                                   dx_row_stride, n);
+  const uint32_t grid = ia + ib + (part ? f.tiles * div_ceil(n, 16) : 0u);
+  if (grid == 0) return RLD_OK;
+  if (R <= 16) end_kernel<1><<<grid, 256, 0, st>>>(a, b, f, ia, ib);
+  else if (R <= 32) end_kernel<2><<<grid, 256, 0, st>>>(a, b, f, ia, ib);
+  else if (R <= 64) end_kernel<4><<<grid, 256, 0, st>>>(a, b, f, ia, ib);
+  else end_kernel<8><<<grid, 256, 0, st>>>(a, b, f, ia, ib);
   return launch_status();
 }

@@ -156,12 +156,12 @@ class Case:
         return h[1:-1, :width]
 
     def call_proj(self, out, ws, stream=None):
-        need = R.rld_proj_workspace_bytes(self.n, self.k, self.r, self.slots)
+        need = R.rld_proj_workspace_bytes(self.n, self.k, self.m, self.r, self.slots)
         return R.rld_proj(self.route, self.wd, self.ws, self.xd, self.xs, self.slotd, self.n,
                           out.data_ptr() + 2 * self.os, self.os, ws, need, stream)
 
     def proj(self):
-        need = R.rld_proj_workspace_bytes(self.n, self.k, self.r, self.slots)
+        need = R.rld_proj_workspace_bytes(self.n, self.k, self.m, self.r, self.slots)
         ws, out = self.scratch(need), self.out_rows(self.os)
         R.check(self.call_proj(out, ws), "rld_proj")
         torch.cuda.synchronize()
@@ -424,7 +424,7 @@ def test_graph_replays_with_new_routing():
     turn with new routing, with eager calls and host waits between the replays."""
     say("case: proj graphs")
     c = Case(96, 520, 264, 16, 6, seed=11)
-    need = max(R.rld_proj_workspace_bytes(c.n, c.k, c.r, c.slots),
+    need = max(R.rld_proj_workspace_bytes(c.n, c.k, c.m, c.r, c.slots),
                R.rld_proj_grad_workspace_bytes(c.n, c.k, c.m, c.r, c.slots))
     ws, out, dx = c.scratch(need), c.out_rows(c.os), c.out_rows(c.xs)
     c.tables()
@@ -459,7 +459,7 @@ def test_on_another_stream():
     c = Case(200, 264, 136, 16, 4, seed=13)
     want = c.proj()
     s = torch.cuda.Stream()
-    ws, out = c.scratch(R.rld_proj_workspace_bytes(c.n, c.k, c.r, c.slots)), c.out_rows(c.os)
+    ws, out = c.scratch(R.rld_proj_workspace_bytes(c.n, c.k, c.m, c.r, c.slots)), c.out_rows(c.os)
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):
         R.check(c.call_proj(out, ws), "rld_proj")
@@ -480,7 +480,7 @@ def test_far_rows():
     want, grads = c.proj(), c.grad()
     c.xd, c.xs = far, stride
     out = c.out_rows(c.os)
-    ws = c.scratch(R.rld_proj_workspace_bytes(n, k, r, 3))
+    ws = c.scratch(R.rld_proj_workspace_bytes(n, k, m, r, 3))
     R.check(c.call_proj(out, ws), "rld_proj")
     torch.cuda.synchronize()
     assert np.array_equal(c.body(out, m, c.os), want)
@@ -490,3 +490,23 @@ def test_far_rows():
     torch.cuda.synchronize()
     for a, b in zip(c.slot_gradients(), grads[1:]):
         assert np.array_equal(a, b)
+
+
+def test_far_rows_of_large_tiles():
+    """Grids of large tiles over rows that 32-bit offsets do not reach in sorted
+    order (they are then taken in their own order): the projection and dx with
+    wide strides have the bits of the narrow ones' bounds, dA and dB too."""
+    say("case: proj far rows, large tiles")
+    n, k, m, r = 2060, 328, 4616, 16
+    c = Case(n, k, m, r, 5, "mixed", seed=15)
+    wide = 1 << 18
+    assert n * wide * 2 > 1 << 30
+    far = torch.full((n, wide), NAN16, dtype=torch.int16, device=c.dev)
+    far[:, :k] = c.xd[:, :k]
+    c.xd, c.xs = far, wide
+    c.check_proj()
+    c = Case(n, m, k, r, 5, "mixed", seed=16)  # dx [n, 4616] from dy [n, 328]
+    far[:, :k] = c.dyd[:, :k]
+    far[:, k:] = NAN16
+    c.dyd, c.os = far, wide
+    c.check_grads()

@@ -457,7 +457,7 @@ def test_training_step_through_router_and_projection():
     wts, loss = torch.zeros((n, k), device=dev), torch.zeros(1, device=dev)
     dw_h = rng.standard_normal((n, k)).astype(np.float32)
     dw, dl = torch.from_numpy(dw_h).to(dev), torch.full((1,), 2.0, device=dev)
-    wb = max(R.rld_proj_workspace_bytes(n, k_in, rank, slots),
+    wb = max(R.rld_proj_workspace_bytes(n, k_in, E, rank, slots),
              R.rld_proj_grad_workspace_bytes(n, k_in, E, rank, slots),
              R.rld_moe_router_workspace_bytes(n, E, k))
     ws = torch.full((wb,), 0xFF, dtype=torch.uint8, device=dev)

@@ -145,8 +145,9 @@ def test_router_grad_empty_batch_is_a_no_op():
 
 def test_workspace_sizes_grow_with_the_call():
     p = R.rld_proj_workspace_bytes
-    assert p(0, 64, 16, 4) == 0 and p(4, 64, 16, 0) == 0 and p(4, 64, 16, 4) >= 4 * 16 * 4
-    assert p(5, 4096, 16, 4) > p(4, 4096, 16, 4) and p(4, 8192, 16, 4) > p(4, 4096, 16, 4)
+    assert p(0, 64, 64, 16, 4) == 0 and p(4, 64, 64, 16, 0) == 0 and p(4, 64, 0, 16, 4) == 0
+    assert p(4, 64, 64, 16, 4) >= 4 * 16 * 4 + 4 * 64 * 4
+    assert p(5, 4096, 64, 16, 4) > p(4, 4096, 64, 16, 4)
     g = R.rld_proj_grad_workspace_bytes
     assert g(4, 64, 128, 16, 0) == 0 and g(0, 64, 128, 16, 4) > 0
     assert g(5, 4096, 128, 16, 4) > g(4, 4096, 128, 16, 4)

@@ -33,7 +33,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 #define RLD_CONST __attribute__((address_space(4)))
 
 constexpr uint32_t kLowRows = 64;    // rows of a low item
-constexpr uint32_t kLowChunk = 512;  // k elements of a low item
+constexpr uint32_t kLowChunk = 512;  // k elements of a low item, at least
 constexpr uint32_t kMaxStride = 1u << 21;
 constexpr uint32_t kBigTiles = 160;  // 256 x 256 tiles from which a grid of them pays
 
@@ -67,7 +67,7 @@ __device__ __forceinline__ void bf16_parts(const float (&v)[8], uint4 (&out)[NP]
 struct SortArgs {
   uint64_t seq_, atab_, btab_;
   uint64_t order_, skey_;  // [n]: the row at a sorted position; its slot, -1 for base rows
-  uint64_t rkey_;          // [n]: the same slots by row
+  uint64_t rkey_, rpos_;   // [n]: by row, the same slot and the row's position
   uint64_t span_;          // [max_loras][2]: a slot's first position and rows
   uint32_t n, max_loras;
 };
@@ -150,6 +150,7 @@ __device__ __forceinline__ void sort_item(const SortArgs& a, uint32_t item, uint
         gp<int32_t>(a.order_)[at] = (int)(r0 + e);
         gp<int32_t>(a.skey_)[at] = active ? s : -1;
         gp<int32_t>(a.rkey_)[r0 + e] = active ? s : -1;
+        gp<int32_t>(a.rpos_)[r0 + e] = (int)at;
         ++at;
       }
     cnt += tot;
@@ -165,160 +166,7 @@ __global__ void __launch_bounds__(256) sort_kernel(SortArgs a) {
   sort_item(a, blockIdx.x, wsum);
 }
 
-// -------------------------------------------------------------------- low ----
-
-struct LowArgs {
-  uint64_t x_, mtab_, otab_, stab_, partial_;
-  uint64_t order_;  // sorted positions' rows, or 0: positions are rows
-  uint64_t key_;    // slots by position
-  uint64_t low_;    // fp32 [n][R], or 0: not wanted
-  uint64_t parts_;  // bf16 [n][2][R]: the value's two parts, or 0
-  uint32_t xs, n, max_loras, K, R, nch, nz, tiles;
-};
-
-// Four columns of a low row, scaled, to where they are wanted.
-__device__ __forceinline__ void store_low(const LowArgs& a, uint32_t pos, uint32_t col,
-                                          const floatx4& v) {
-  if (a.low_) *gp<floatx4>(a.low_ + ((size_t)pos * a.R + col) * 4) = v;
-  if (a.parts_) {
-    const uint2v hi = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-    const uint2v lo = {
-        pack_bf16x2(v[0] - bf16_to_f32(hi.x & 0xffffu), v[1] - bf16_to_f32(hi.x >> 16)),
-        pack_bf16x2(v[2] - bf16_to_f32(hi.y & 0xffffu), v[3] - bf16_to_f32(hi.y >> 16))};
-    RLD_GLOBAL uint16_t* p = gp<uint16_t>(a.parts_) + (size_t)pos * 2 * a.R + col;
-    *reinterpret_cast<RLD_GLOBAL uint2v*>(p) = hi;
-    *reinterpret_cast<RLD_GLOBAL uint2v*>(p + a.R) = lo;
-  }
-}
-
-typedef floatx4 LowSmem[2][4][4][kWave];
-
-// One item: 64 positions, one k chunk, every nz-th of the distinct slots that
-// they name.  The x fragments stay in registers over the slots; each wave
-// contracts every fourth 32-wide step and the four sums meet in LDS.
-// TRANS: the matrix is [K][R] (B_s) instead of [R][K] (A_s).
-template <bool TRANS>
-__device__ __forceinline__ void low_item(const LowArgs& a, uint32_t item, LowSmem& red) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int g = lane >> 4, c = lane & 15;
-  const uint32_t tile = item % a.tiles, ch = item / a.tiles % a.nch;
-  const uint32_t z = item / (a.tiles * a.nch);
-  const uint32_t pos0 = tile * kLowRows;
-  const uint32_t kb = ch * kLowChunk, ke = min(kb + kLowChunk, a.K);
-
-  const int key = pos0 + lane < a.n ? gp<const int32_t>(a.key_)[pos0 + lane] : -1;
-  uint64_t left = __ballot(key >= 0 && (uint32_t)key < a.max_loras);
-  if (!left) return;
-
-  uint4 xf[4][4];
-#pragma unroll
-  for (int mi = 0; mi < 4; ++mi) {
-    const uint32_t pos = pos0 + mi * 16 + c;
-    const uint32_t at = min(pos, a.n - 1);
-    const uint32_t row = a.order_ ? (uint32_t)gp<const int32_t>(a.order_)[at] : at;
-    const RLD_GLOBAL uint16_t* xr = gp<const uint16_t>(a.x_) + (size_t)row * a.xs;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t k = kb + (wave + 4 * i) * 32 + g * 8;
-      xf[mi][i] = (pos < a.n && k < ke) ? load16(xr + k) : zero16();
-    }
-  }
-
-  int buf = 0;
-  for (uint32_t idx = 0; left; ++idx) {
-    const int s = __builtin_amdgcn_readlane(key, __builtin_ctzll(left));
-    const uint64_t mine = __ballot(key == s);
-    left &= ~mine;
-    if (idx % a.nz != z) continue;
-    const uint64_t mt = gp<const uint64_t>(a.mtab_)[s], ot = gp<const uint64_t>(a.otab_)[s];
-    if (mt == 0ull || ot == 0ull) continue;
-    const RLD_GLOBAL uint16_t* M = gp<const uint16_t>(mt);
-    for (uint32_t j0 = 0; j0 < a.R; j0 += 16) {
-      const uint32_t j = j0 + c;
-      floatx4 acc[4] = {};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t k = kb + (wave + 4 * i) * 32 + g * 8;
-        uint4 m = zero16();
-        if (j < a.R && k < ke) {
-          if constexpr (!TRANS) {
-            m = load16(M + (size_t)j * a.K + k);
-          } else {
-            uint32_t e[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) e[q] = M[(size_t)(k + q) * a.R + j];
-            m = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16,
-                           e[6] | e[7] << 16);
-          }
-        }
-#pragma unroll
-        for (int mi = 0; mi < 4; ++mi) acc[mi] = mfma_bf16_16x16x32(m, xf[mi][i], acc[mi]);
-      }
-#pragma unroll
-      for (int mi = 0; mi < 4; ++mi) red[buf][wave][mi][lane] = acc[mi];
-      __syncthreads();
-      // wave w finishes positions 16w .. 16w+15: lane (g, c) holds columns 4g.. of c
-      floatx4 sum = red[buf][0][wave][lane];
-#pragma unroll
-      for (int v = 1; v < 4; ++v) sum += red[buf][v][wave][lane];
-      buf ^= 1;
-      const int lr = wave * 16 + c;
-      const uint32_t col = j0 + 4 * g;
-      if (((mine >> lr) & 1) && col < a.R) {
-        if (a.nch == 1 && !a.partial_)
-          store_low(a, pos0 + lr, col, sum * gp<const float>(a.stab_)[s]);
-        else
-          *gp<floatx4>(a.partial_ + (((size_t)ch * a.n + pos0 + lr) * a.R + col) * 4) = sum;
-      }
-    }
-  }
-}
-
-__global__ void __launch_bounds__(256) low_kernel(LowArgs a) {
-  __shared__ LowSmem red;
-  low_item<false>(a, blockIdx.x, red);
-}
-
-// u = x A^T and g = dy B in one launch: the first `items` blocks make u.
-__global__ void __launch_bounds__(256) low_pair_kernel(LowArgs u, LowArgs gr, uint32_t items) {
-  __shared__ LowSmem red;
-  if (blockIdx.x < items) low_item<false>(u, blockIdx.x, red);
-  else low_item<true>(gr, blockIdx.x - items, red);
-}
-
-// low[p] = scale_s * (the chunks' sums in chunk order), routed rows only.
-__device__ __forceinline__ void low_sum(const LowArgs& a, uint32_t block) {
-  const uint32_t q = a.R / 4;
-  const uint64_t t = (uint64_t)block * 256 + threadIdx.x;
-  if (t >= (uint64_t)a.n * q) return;
-  const uint32_t pos = (uint32_t)(t / q);
-  const int s = gp<const int32_t>(a.key_)[pos];
-  if (s < 0 || (uint32_t)s >= a.max_loras) return;
-  floatx4 sum = {};
-  for (uint32_t ch = 0; ch < a.nch; ++ch)
-    sum += gp<const floatx4>(a.partial_)[(size_t)ch * a.n * q + t];
-  store_low(a, pos, (uint32_t)(t % q) * 4, sum * gp<const float>(a.stab_)[s]);
-}
-
-__global__ void __launch_bounds__(256) low_reduce_kernel(LowArgs u, LowArgs gr, uint32_t blocks) {
-  if (blockIdx.x < blocks) low_sum(u, blockIdx.x);
-  else low_sum(gr, blockIdx.x - blocks);
-}
-
-// ------------------------------------------------------------------- tile ----
-
-struct TileArgs {
-  uint64_t x_, w_, out_, parts_, etab_;
-  uint64_t order_;  // sorted positions' rows, or 0: rows in their own order, their
-                    // offsets taken from a tile's first row
-  uint64_t skey_;   // slots by position
-  uint32_t xs, ws, os, n, K, N, R, tiles_m, tiles_n;
-};
-
-// The row at position p, less the row that offsets are taken from.
-__device__ __forceinline__ uint32_t tile_row(const TileArgs& a, uint32_t p, uint32_t first) {
-  return (a.order_ ? (uint32_t)gp<const int32_t>(a.order_)[p] : p) - first;
-}
+// ------------------------------------------------------- memory to LDS ----
 
 // Until at most N of this wave's loads and stores are in flight.
 template <int N>
@@ -354,6 +202,17 @@ __device__ __forceinline__ void dma16(const rsrc_t& r, uint32_t to, uint32_t vof
       "buffer_load_dwordx4 %1, %2, %3 offen lds"
       :
       : "s"(to), "v"(voff), "s"(r), "s"(soff)
+      : "memory");
+}
+
+// The same from a 64-bit address of each lane.
+__device__ __forceinline__ void dma16(uint64_t from, uint32_t to) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, off"
+      :
+      : "s"(to), "v"(from)
       : "memory");
 }
 
@@ -403,6 +262,231 @@ __device__ __forceinline__ uint32_t buffer_load2(uint64_t base, uint64_t bytes, 
   return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
 }
 
+// A value that is the same in every lane, in scalar registers.
+__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v) |
+         (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) << 32;
+}
+
+// -------------------------------------------------------------------- low ----
+
+struct LowArgs {
+  uint64_t x_, mtab_, otab_, stab_, partial_;
+  uint64_t order_;  // sorted positions' rows, or 0: positions are rows
+  uint64_t key_;    // slots by position
+  uint64_t low_;    // fp32 [n][R], or 0: not wanted
+  uint64_t parts_;  // bf16 [n][2][R]: the value's two parts, or 0
+  uint64_t low_at_, parts_at_;  // where a position goes in either, or 0: the same
+  uint32_t xs, n, max_loras, K, R, kc, nch, nz, tiles;
+};
+
+// Four columns of a low row, scaled, to where they are wanted.
+__device__ __forceinline__ void store_low(const LowArgs& a, uint32_t from, uint32_t col,
+                                          const floatx4& v) {
+  uint32_t pos = a.low_at_ ? (uint32_t)gp<const int32_t>(a.low_at_)[from] : from;
+  if (a.low_) *gp<floatx4>(a.low_ + ((size_t)pos * a.R + col) * 4) = v;
+  if (a.parts_) {
+    pos = a.parts_at_ ? (uint32_t)gp<const int32_t>(a.parts_at_)[from] : from;
+    const uint2v hi = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    const uint2v lo = {
+        pack_bf16x2(v[0] - bf16_to_f32(hi.x & 0xffffu), v[1] - bf16_to_f32(hi.x >> 16)),
+        pack_bf16x2(v[2] - bf16_to_f32(hi.y & 0xffffu), v[3] - bf16_to_f32(hi.y >> 16))};
+    RLD_GLOBAL uint16_t* p = gp<uint16_t>(a.parts_) + (size_t)pos * 2 * a.R + col;
+    *reinterpret_cast<RLD_GLOBAL uint2v*>(p) = hi;
+    *reinterpret_cast<RLD_GLOBAL uint2v*>(p + a.R) = lo;
+  }
+}
+
+// The r-th set bit of m (r below their number).
+__device__ __forceinline__ uint32_t nth_bit(uint64_t m, uint32_t r) {
+  uint32_t at = 0;
+#pragma unroll
+  for (int w = 32; w; w >>= 1) {
+    const uint32_t c = __popcll(m & ((1ull << w) - 1));
+    const bool up = r >= c;
+    r -= up ? c : 0u;
+    at += up ? w : 0;
+    m = up ? m >> w : m;
+  }
+  return at;
+}
+
+constexpr int kLowStages = 4;
+constexpr int kLowLds = kLowStages * 128 * 128;
+
+// One item: 64 positions, one k chunk, every nz-th of the distinct slots that
+// they name, one after another: that slot's positions, close together (the
+// places behind them hold zeros), times 64 columns of its matrix at a time.
+// x and the matrix go by in 64-wide k steps through LDS, in whole 128-byte
+// pieces; four waves of 32 x 32.
+// TRANS: the matrix is [K][R] (B_s) instead of [R][K] (A_s).
+template <bool TRANS>
+__device__ __forceinline__ void low_item(const LowArgs& a, uint32_t item, unsigned char* lds) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, c = lane & 15;
+  const int wr = wave >> 1, wc = wave & 1;
+  const uint32_t tile = item % a.tiles, ch = item / a.tiles % a.nch;
+  const uint32_t z = item / (a.tiles * a.nch);
+  const uint32_t pos0 = tile * kLowRows;
+  const uint32_t kb = ch * a.kc, ke = min(kb + a.kc, a.K), nk = (ke - kb + 63) / 64;
+  const uint32_t lds0 = lds_addr(lds);
+  const uint64_t zeros = (uint64_t)&g_zero16[0];
+
+  const int key = pos0 + lane < a.n ? gp<const int32_t>(a.key_)[pos0 + lane] : -1;
+  const int row_of = (a.order_ && pos0 + lane < a.n) ? gp<const int32_t>(a.order_)[pos0 + lane]
+                                                     : (int)(pos0 + lane);
+  uint64_t left = __ballot(key >= 0 && (uint32_t)key < a.max_loras);
+  for (uint32_t idx = 0; left; ++idx) {
+    const int s = __builtin_amdgcn_readlane(key, __builtin_ctzll(left));
+    const uint64_t mine = __ballot(key == s);
+    left &= ~mine;
+    if (idx % a.nz != z) continue;
+    const uint64_t mt = uniform64(gp<const uint64_t>(a.mtab_)[s]);
+    const uint64_t ot = uniform64(gp<const uint64_t>(a.otab_)[s]);
+    if (mt == 0ull || ot == 0ull) continue;
+    const uint32_t cnt = __popcll(mine);
+
+    // this wave's loads of a stage: two of eight rows of x, two of the matrix
+    uint64_t px[2];
+    uint32_t kx[2], km[2], vm[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const uint32_t r = (wave + 4 * p) * 8 + (lane >> 3);
+      const uint32_t q = (lane & 7) ^ ((r >> 1) & 7);
+      const uint32_t row = (uint32_t)__shfl(row_of, (int)nth_bit(mine, min(r, cnt - 1)));
+      px[p] = a.x_ + ((uint64_t)row * a.xs + kb + q * 8) * 2;
+      kx[p] = r < cnt ? kb + q * 8 : 0xff000000u;
+    }
+    for (uint32_t j0 = 0; j0 < a.R; j0 += 64) {
+      const uint32_t ranks = min(64u, a.R - j0);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const uint32_t r = (wave + 4 * p) * 8 + (lane >> 3);
+        if constexpr (!TRANS) {
+          const uint32_t q = (lane & 7) ^ ((r >> 1) & 7);
+          vm[p] = r * a.K * 2 + q * 16;
+          km[p] = r < ranks ? kb + q * 8 : 0xff000000u;
+        } else {
+          const uint32_t h = ((r >> 1) & 1) | ((r >> 3) & 1) << 1;
+          const uint32_t col = (((lane & 7) >> 1 ^ h) * 2 + (lane & 1)) * 8;
+          vm[p] = (r * a.R + col) * 2;
+          km[p] = col < ranks ? kb + r : 0xff000000u;
+        }
+      }
+      const rsrc_t rm =
+          TRANS ? buffer(mt + ((uint64_t)kb * a.R + j0) * 2, ((uint64_t)(ke - kb) * a.R - j0) * 2)
+                : buffer(mt + ((uint64_t)j0 * a.K + kb) * 2,
+                         ((uint64_t)(ranks - 1) * a.K + ke - kb) * 2);
+      auto issue = [&](uint32_t t) {
+        const uint32_t st = lds0 + (t % kLowStages) * 16384 + wave * 1024;
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          dma16(kx[p] + t * 64 < ke ? px[p] + t * 128 : zeros, st + p * 4096);
+        const uint32_t at = TRANS ? t * 128 * a.R : t * 128;
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          dma16(rm, st + 8192 + p * 4096, km[p] + t * 64 < ke ? vm[p] + at : kOutside, 0);
+      };
+      floatx4 acc[2][2] = {};
+#pragma unroll
+      for (int t = 0; t < kLowStages - 1; ++t) issue(t);
+      for (uint32_t t = 0; t < nk; ++t) {
+        wait_vm<(kLowStages - 2) * 4>();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        issue(t + kLowStages - 1);
+        const uint32_t st = lds0 + (t % kLowStages) * 16384;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          const uint32_t sw = ((ks * 4 + g) ^ (c >> 1)) * 16;
+          uint4 xf[2], mf[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            xf[i] = lds16(lds_at(st + (wr * 32 + i * 16 + c) * 128 + sw));
+            if constexpr (!TRANS) {
+              mf[i] = lds16(lds_at(st + 8192 + (wc * 32 + i * 16 + c) * 128 + sw));
+            } else {
+              const int h = ((c >> 3) & 1) | (g & 1) << 1;
+              mf[i] = lds_tr16(lds_at(st + 8192 + (ks * 32 + 8 * g + (c >> 2)) * 128 +
+                                      ((wc * 2 + i) ^ h) * 32 + (c & 3) * 8),
+                               4 * 128);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              acc[j][i] = mfma_bf16_16x16x32(mf[j], xf[i], acc[j][i]);
+        }
+      }
+      wait_vm<0>();  // the loads past the end, of zeros
+      __builtin_amdgcn_s_barrier();  // everyone has read: the places may be loaded again
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t r = wr * 32 + i * 16 + c;
+        const uint32_t pos = pos0 + nth_bit(mine, min(r, cnt - 1));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t col = j0 + wc * 32 + j * 16 + 4 * g;
+          if (r >= cnt || col >= a.R) continue;
+          if (a.partial_)
+            *gp<floatx4>(a.partial_ + (((size_t)ch * a.n + pos) * a.R + col) * 4) = acc[j][i];
+          else
+            store_low(a, pos, col, acc[j][i] * gp<const float>(a.stab_)[s]);
+        }
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(256) low_kernel(LowArgs a) {
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[kLowLds];
+  low_item<false>(a, blockIdx.x, lds);
+}
+
+// u = x A^T and g = dy B in one launch: the first `items` blocks make u.
+__global__ void __launch_bounds__(256) low_pair_kernel(LowArgs u, LowArgs gr, uint32_t items) {
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[kLowLds];
+  if (blockIdx.x < items) low_item<false>(u, blockIdx.x, lds);
+  else low_item<true>(gr, blockIdx.x - items, lds);
+}
+
+// low[p] = scale_s * (the chunks' sums in chunk order), routed rows only.
+__device__ __forceinline__ void low_sum(const LowArgs& a, uint32_t block) {
+  const uint32_t q = a.R / 4;
+  const uint64_t t = (uint64_t)block * 256 + threadIdx.x;
+  if (t >= (uint64_t)a.n * q) return;
+  const uint32_t pos = (uint32_t)(t / q);
+  const int s = gp<const int32_t>(a.key_)[pos];
+  if (s < 0 || (uint32_t)s >= a.max_loras) return;
+  floatx4 sum = {};
+  for (uint32_t ch = 0; ch < a.nch; ++ch)
+    sum += gp<const floatx4>(a.partial_)[(size_t)ch * a.n * q + t];
+  store_low(a, pos, (uint32_t)(t % q) * 4, sum * gp<const float>(a.stab_)[s]);
+}
+
+__global__ void __launch_bounds__(256) low_reduce_kernel(LowArgs u, LowArgs gr, uint32_t blocks) {
+  if (blockIdx.x < blocks) low_sum(u, blockIdx.x);
+  else low_sum(gr, blockIdx.x - blocks);
+}
+
+// ------------------------------------------------------------------- tile ----
+
+struct TileArgs {
+  uint64_t x_, w_, out_, parts_, etab_;
+  uint64_t order_;  // sorted positions' rows, or 0: rows in their own order, their
+                    // offsets taken from a tile's first row
+  uint64_t skey_;   // slots by position
+  uint32_t xs, ws, os, n, K, N, R, tiles_m, tiles_n;
+};
+
+// The row at position p, less the row that offsets are taken from.
+__device__ __forceinline__ uint32_t tile_row(const TileArgs& a, uint32_t p, uint32_t first) {
+  return (a.order_ ? (uint32_t)gp<const int32_t>(a.order_)[p] : p) - first;
+}
+
 // The last K - k0 < 64 of the product, from global memory (zeros past K).
 template <int MI, int NI, bool TRANS>
 __device__ __forceinline__ void k_tail(const TileArgs& a, uint32_t k0, floatx4 (&acc)[NI][MI],
@@ -447,12 +531,6 @@ __device__ __forceinline__ void k_tail(const TileArgs& a, uint32_t k0, floatx4 (
       if (mi % 4 == 3) issue_point();
     }
   }
-}
-
-// A value that is the same in every lane, in scalar registers.
-__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
-  return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v) |
-         (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) << 32;
 }
 
 // acc[ni][mi] of a wave holds the 16 x 16 block of positions row0 + rows_at[mi] ..
@@ -645,15 +723,17 @@ struct FinishArgs {
 // order, plus the low rows times their slots' second matrices.  A slot's
 // product is made apart and added to its own rows alone (a NaN or infinity of
 // its matrix would survive zeros in the others).  KS: 32-wide steps of rank.
+// TRANS: the matrices are [R][N]; their 64 columns go through LDS (32 KB) and
+// transposing reads.
 template <int KS, bool TRANS>
-__device__ __forceinline__ void finish_item(const FinishArgs& a, uint32_t item) {
+__device__ __forceinline__ void finish_item(const FinishArgs& a, uint32_t item,
+                                            unsigned char* lds) {
   constexpr int SB = KS == 1 ? 8 : KS == 2 ? 4 : 2;  // slots whose matrices are loaded at once
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, c = lane & 15;
-  const uint32_t col0 = item % a.tiles * 64 + wave * 16;
+  const uint32_t tile0 = item % a.tiles * 64, col0 = tile0 + wave * 16;
   const uint32_t pos0 = item / a.tiles * 16;
-  if (col0 >= a.N) return;
   const uint32_t pos = pos0 + c, at = min(pos, a.n - 1);
   int key = gp<const int32_t>(a.key_)[at];
   const uint32_t row = a.order_ ? (uint32_t)gp<const int32_t>(a.order_)[at] : at;
@@ -680,6 +760,7 @@ __device__ __forceinline__ void finish_item(const FinishArgs& a, uint32_t item) 
     if (e == 0ull || gp<const uint64_t>(a.otab_)[key] == 0ull) key = -1;
   }
   const uint32_t lat = a.low_sorted ? pos : row;
+  [[maybe_unused]] const uint32_t lds0 = lds_addr(lds);
   uint64_t left = __ballot(key >= 0 && lane < 16);
   if (left) {
     uint4 hi[KS], lo[KS];
@@ -729,22 +810,37 @@ __device__ __forceinline__ void finish_item(const FinishArgs& a, uint32_t item) 
         left &= ~__ballot(key == s[b]);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          const uint32_t k = ks * 32 + 8 * g;
-          const bool in = s[b] >= 0 && k < a.R && col0 + c < a.N;
+          [[maybe_unused]] const uint32_t k = ks * 32 + 8 * g;
+          [[maybe_unused]] const bool in = s[b] >= 0 && k < a.R && col0 + c < a.N;
           if constexpr (!TRANS) {
             ef[b][ks] = buffer_load16(eb + (uint64_t)col0 * a.R * 2, s[b] >= 0 ? kBufferEnd : 0u,
                                       in ? (c * a.R + k) * 2 : kBufferEnd);
           } else {
-            uint32_t w[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              w[q] = buffer_load2(eb + ((uint64_t)(ks * 32 + q) * a.N + col0) * 2,
-                                  s[b] >= 0 ? kBufferEnd : 0u,
-                                  in ? 16 * g * a.N + c * 2 : kBufferEnd);
-            ef[b][ks] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16,
-                                   w[6] | w[7] << 16);
+            const uint32_t r = ks * 32 + wave * 8 + (lane >> 3);
+            const uint32_t h = ((r >> 1) & 1) | ((r >> 3) & 1) << 1;
+            const uint32_t cc = (((lane & 7) >> 1 ^ h) * 2 + (lane & 1)) * 8;
+            const rsrc_t re = buffer(eb + (uint64_t)tile0 * 2,
+                                     s[b] >= 0 ? ((uint64_t)a.R * a.N - tile0) * 2 : 0u);
+            dma16(re, lds0 + (b * KS + ks) * 4096 + wave * 1024,
+                  (r < a.R && tile0 + cc < a.N) ? (r * a.N + cc) * 2 : kOutside, 0);
           }
         }
+      }
+      if constexpr (TRANS) {
+        wait_vm<0>();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        const int h = ((c >> 3) & 1) | (g & 1) << 1;
+#pragma unroll
+        for (int b = 0; b < SB; ++b)
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+            ef[b][ks] = lds_tr16(lds_at(lds0 + (b * KS + ks) * 4096 + (8 * g + (c >> 2)) * 128 +
+                                        (wave ^ h) * 32 + (c & 3) * 8),
+                                 4 * 128);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();  // everyone has read: the next slots may come
+        asm volatile("" ::: "memory");
       }
 #pragma unroll
       for (int b = 0; b < SB; ++b) {
@@ -775,14 +871,14 @@ struct StartArgs {
 
 template <int BM, int BN, int WR, int WC, int STAGES, bool TRANS>
 __device__ __forceinline__ void start_body(const StartArgs& a) {
-  constexpr int kTile = STAGES * (BM + BN) * 128, kLow = (int)sizeof(LowSmem);
-  __shared__ __attribute__((aligned(1024))) unsigned char lds[kTile > kLow ? kTile : kLow];
+  constexpr int kTile = STAGES * (BM + BN) * 128;
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[kTile > kLowLds ? kTile : kLowLds];
   uint32_t b = blockIdx.x;
   if (b < a.parts) return part_item<BM, BN, WR, WC, STAGES, TRANS>(a.part, b, lds);
   b -= a.parts;
-  if (b < a.us) return low_item<false>(a.u, b, *reinterpret_cast<LowSmem*>(lds));
+  if (b < a.us) return low_item<false>(a.u, b, lds);
   b -= a.us;
-  if (TRANS && b < a.gs) return low_item<true>(a.g, b, *reinterpret_cast<LowSmem*>(lds));
+  if (TRANS && b < a.gs) return low_item<true>(a.g, b, lds);
   b -= a.gs;
   sort_item(a.sort, b, reinterpret_cast<uint32_t*>(lds));
 }
@@ -1175,13 +1271,13 @@ __global__ void __launch_bounds__(512) big_tile_kernel(TileArgs a) {
 struct WgradArgs {
   uint64_t v_, low_, order_, span_, dtab_;
   uint32_t vs, width, R, tiles, accumulate;
-  uint32_t low_sorted;  // low rows by position (else by row)
 };
 
 struct WgradSmem {
   __attribute__((aligned(1024))) unsigned char stage[4][4096];
   floatx4 red[4][4][kWave];
 };
+static_assert(sizeof(WgradSmem) >= 32768, "finish_item uses as much");
 
 // Slot s, 64 columns of the wide operand (x for dA, dy for dB): the sum over
 // the slot's positions of low[pos][r] * wide[row][col].  Each of four waves
@@ -1202,7 +1298,7 @@ __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, Wg
   const uint32_t begin = gp<const uint32_t>(a.span_)[2 * s];
   const uint32_t cnt = gp<const uint32_t>(a.span_)[2 * s + 1];
   const RLD_GLOBAL int32_t* order = gp<const int32_t>(a.order_) + begin;
-  const RLD_GLOBAL float* low = gp<const float>(a.low_);
+  const RLD_GLOBAL float* low = gp<const float>(a.low_) + (size_t)begin * a.R;
 
   floatx4 acc[RT][4];
 #pragma unroll
@@ -1222,12 +1318,6 @@ __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, Wg
       __builtin_amdgcn_global_load_lds((const void*)(in ? src : (uint64_t)&g_zero16[0]),
                                        (RLD_LDS void*)(&stage[wave][p * 1024]), 16, 0, 0);
     }
-    uint32_t at[8];  // where the low rows of this lane's positions lie
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t i = min(i0 + 8 * g + e, cnt - 1);
-      at[e] = a.low_sorted ? begin + i : (uint32_t)order[i];
-    }
     uint4 lf[RT][3];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -1236,7 +1326,7 @@ __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, Wg
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const uint32_t i = i0 + 8 * g + e;
-        v[e] = (i < cnt && r < a.R) ? low[(size_t)at[e] * a.R + r] : 0.f;
+        v[e] = (i < cnt && r < a.R) ? low[(size_t)i * a.R + r] : 0.f;
       }
       bf16_parts<3>(v, lf[rt]);
     }
@@ -1244,13 +1334,10 @@ __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, Wg
 #pragma unroll
     for (int ni = 0; ni < 4; ++ni) {
       const int h = ((c >> 3) & 1) | (g & 1) << 1;
-      const unsigned char* p =
+      unsigned char* p =
           &stage[wave][(8 * g + (c >> 2)) * 128 + (ni ^ h) * 32 + (c & 3) * 8];
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((RLD_LDS s16x4*)p);
       // rows 4 further on: (k >> 1) & 1 and (k >> 3) & 1 are the same
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((RLD_LDS s16x4*)(p + 4 * 128));
-      const uint2 l2 = __builtin_bit_cast(uint2, lo), h2 = __builtin_bit_cast(uint2, hi);
-      const uint4 vf = make_uint4(l2.x, l2.y, h2.x, h2.y);
+      const uint4 vf = lds_tr16((RLD_LDS unsigned char*)p, 4 * 128);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -1291,12 +1378,12 @@ __global__ void __launch_bounds__(256) end_kernel(WgradArgs da, WgradArgs db, Fi
   constexpr int KS = RT < 2 ? 1 : RT / 2;
   if (blockIdx.x < ia) wgrad_item<RT, false>(da, blockIdx.x, sm);
   else if (blockIdx.x < ia + ib) wgrad_item<RT, true>(db, blockIdx.x - ia, sm);
-  else finish_item<KS, true>(fin, blockIdx.x - ia - ib);
+  else finish_item<KS, true>(fin, blockIdx.x - ia - ib, sm.stage[0]);
 }
 
 template <int KS>
 __global__ void __launch_bounds__(256) finish_kernel(FinishArgs a) {
-  finish_item<KS, false>(a, blockIdx.x);
+  finish_item<KS, false>(a, blockIdx.x, nullptr);
 }
 
 // ------------------------------------------------------------------- host ----
@@ -1304,13 +1391,16 @@ __global__ void __launch_bounds__(256) finish_kernel(FinishArgs a) {
 static inline size_t round16(size_t v) { return (v + 15) & ~(size_t)15; }
 
 struct LowPlan {
-  uint32_t nch;
+  uint32_t kc, nch;
   size_t low, partial;  // bytes
 };
 
 static LowPlan low_plan(uint32_t n, uint32_t K, uint32_t R) {
   LowPlan p;
-  p.nch = div_ceil(K, kLowChunk);
+  // longer chunks once they make some 512 items: fewer sums to write and add
+  const uint64_t items = (uint64_t)div_ceil(n, kLowRows) * div_ceil(K, kLowChunk);
+  p.kc = kLowChunk * (items < 1024 ? 1u : items >= 512 * 16 ? 16u : (uint32_t)(items / 512));
+  p.nch = div_ceil(K, p.kc);
   p.low = round16((size_t)n * R * 4);
   p.partial = round16((size_t)p.nch * n * R * 4);
   return p;
@@ -1350,7 +1440,7 @@ static TilePlan tile_plan(uint32_t n, uint32_t K, uint32_t N) {
 }
 
 static size_t sort_bytes(uint32_t n, uint32_t max_loras) {
-  return 3 * round16((size_t)n * 4) + round16((size_t)max_loras * 8);
+  return 4 * round16((size_t)n * 4) + round16((size_t)max_loras * 8);
 }
 
 static SortArgs sort_args(const rld_route* r, const int32_t* seq, uint32_t n,
@@ -1362,7 +1452,8 @@ static SortArgs sort_args(const rld_route* r, const int32_t* seq, uint32_t n,
   a.order_ = workspace;
   a.skey_ = a.order_ + round16((size_t)n * 4);
   a.rkey_ = a.skey_ + round16((size_t)n * 4);
-  a.span_ = a.rkey_ + round16((size_t)n * 4);
+  a.rpos_ = a.rkey_ + round16((size_t)n * 4);
+  a.span_ = a.rpos_ + round16((size_t)n * 4);
   a.n = n;
   a.max_loras = r->max_loras;
   return a;
@@ -1387,7 +1478,10 @@ static LowArgs low_args(const rld_route* r, bool trans, const void* x, uint32_t 
   a.max_loras = r->max_loras;
   a.K = trans ? r->n_out : r->k_in;
   a.R = r->max_rank;
-  a.nch = div_ceil(a.K, kLowChunk);
+  const LowPlan p = low_plan(n, a.K, a.R);
+  a.kc = p.kc;
+  a.nch = p.nch;
+  a.low_at_ = a.parts_at_ = 0;
   a.tiles = div_ceil(n, kLowRows);
   // few items: the slots of a tile go to several blocks
   const uint32_t items = a.tiles * a.nch;
@@ -1499,7 +1593,7 @@ static int check_wide(uint32_t stride) { return stride > kMaxStride ? RLD_EUNSUP
 static int check_items(const rld_route* r, uint32_t n) {
   const uint64_t k = r->k_in > r->n_out ? r->k_in : r->n_out;
   const uint64_t tiles = (k + 63) / 64;
-  if (n > (1u << 26) || k > (1u << 24) || div_ceil(n, 64) * tiles >= (1u << 23) ||
+  if (n > (1u << 26) || k > kMaxStride || div_ceil(n, 64) * tiles >= (1u << 23) ||
       r->max_loras * tiles >= (1u << 21) || (uint64_t)n * (r->max_rank / 4) >= (1u << 30))
     return RLD_EUNSUPPORTED;
   return RLD_OK;
@@ -1658,9 +1752,12 @@ extern "C" int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_r
   const uint64_t order = by_pos ? sort.order_ : 0;
   const uint64_t key = by_pos ? sort.skey_ : keep ? sort.rkey_ : (uint64_t)seq_slot;
   // u for dB; g for dx (as parts) and dA
-  const LowArgs u = low_args(route, false, x, x_row_stride, n, order, key, ul, 0, usum);
-  const LowArgs g = low_args(route, true, dy, dy_row_stride, n, order, key, da_table ? gl : 0,
-                             dx ? gparts : 0, gsum);
+  LowArgs u = low_args(route, false, x, x_row_stride, n, order, key, ul, 0, usum);
+  LowArgs g = low_args(route, true, dy, dy_row_stride, n, order, key, da_table ? gl : 0,
+                       dx ? gparts : 0, gsum);
+  // dA and dB take them by position; dx too, but for rows in their own order
+  if (!by_pos) u.low_at_ = g.low_at_ = sort.rpos_;
+  if (!by_pos && !keep) g.parts_at_ = sort.rpos_;
   const uint32_t iu = want_u ? low_items(u) : 0u, ig = want_g ? low_items(g) : 0u;
   if (first) {
     sort_kernel<<<route->max_loras + 1, 256, 0, st>>>(sort);
@@ -1705,12 +1802,11 @@ extern "C" int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_r
   a.span_ = b.span_ = sort.span_;
   a.R = b.R = R;
   a.accumulate = b.accumulate = accumulate ? 1u : 0u;
-  a.low_sorted = b.low_sorted = by_pos ? 1u : 0u;
   a.tiles = div_ceil(a.width, 64);
   b.tiles = div_ceil(b.width, 64);
   const uint32_t ia = da_table ? a.tiles * route->max_loras : 0u;
   const uint32_t ib = db_table ? b.tiles * route->max_loras : 0u;
-  const FinishArgs f = finish_args(route, true, t, sums, sort.order_, sort.skey_, gparts, 0, 0, by_pos, dx,
+  const FinishArgs f = finish_args(route, true, t, sums, sort.order_, sort.skey_, gparts, 0, 0, true, dx,
                                    dx_row_stride, n);
   const uint32_t grid = ia + ib + (part ? f.tiles * div_ceil(n, 16) : 0u);
   if (grid == 0) return RLD_OK;

@@ -493,7 +493,7 @@ int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_row_stride, 
                   void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace rld_moe_router needs, under the contract of rld_proj's:
- * a count and a partial sum per expert and block of 64 tokens. */
+ * a count and a partial sum per expert and block of 128 tokens. */
 size_t rld_moe_router_workspace_bytes(uint32_t num_tokens, uint32_t num_experts,
                                       uint32_t top_k);
 

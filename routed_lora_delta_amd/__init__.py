@@ -164,8 +164,19 @@ def ptr(obj) -> int | None:
     raise TypeError(f"cannot pass {type(obj)} as a pointer")
 
 
+# torch's current stream of the current device as a handle: without the Stream
+# object, which takes 3 us to make, where torch offers it so
+try:
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+    from torch.cuda import current_device as _current_device
+except ImportError:
+    _raw_stream = None
+
+
 def stream_handle(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(_current_device())
         import torch
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):

@@ -13,40 +13,154 @@
 // a fixed order (per lane over its tokens, over the lanes and waves of a
 // block, over the blocks), so results do not change from run to run.
 //
-// Three launches: route (choices, and per block of 64 tokens the counts and
-// probability sums of every expert), scan (per expert, over the blocks) and
-// place (each row's place in the expert-sorted order).  A block keeps one
-// 64-bit mask per expert of its tokens that chose it: the set bits below a
-// token's own are its rank there, whatever order the lanes arrive in.
+// One launch for up to 128 tokens, two otherwise: route (choices, and per block
+// of 128 tokens the counts and probability sums of every expert) and place
+// (each row's place in the expert-sorted order, from the counts of all
+// blocks); past 32 blocks a scan in between turns the counts into prefix
+// sums, so that no place block reads them all.  A block keeps 128 bits per
+// expert of its tokens that chose it: the set bits below a token's own are its
+// rank there, whatever order the lanes arrive in.
+#include <type_traits>
+
 #include "rld_device.hpp"
 #include "rld_internal.hpp"
 
 namespace rld {
 
-constexpr uint32_t kRouteTokens = 64;  // tokens of a block (bits of a mask)
+constexpr uint32_t kRouteTokens = 128;  // tokens of a block
+constexpr uint32_t kRouteThreads = 1024;
+constexpr uint32_t kRouteWaves = kRouteThreads / 64;
+constexpr uint32_t kScanBlocks = 32;    // token blocks above which the scan is worth a launch
 constexpr uint32_t kMaxExperts = 1024;
 constexpr uint32_t kMaxTopK = 32;
 
 struct RouterArgs {
   uint64_t logits_, mask_, indices_, weights_;
   uint64_t counts_, offsets_, tokens_, rows_, loss_;
-  uint64_t cnt_, psum_;      // [E + 1][nblk]: counts (then their prefix sums), sums of p
-  uint64_t total_, ptotal_;  // [E + 1], [E]
-  uint32_t ls, T, E, k, nblk, norm;
+  uint64_t cnt_, psum_;      // [nblk][E + 1]: counts (after the scan their prefix sums), [nblk][E]:
+                             // sums of p
+  uint64_t total_, ptotal_;  // [E + 1], [E]: of the scan
+  uint32_t ls, T, E, k, nblk, norm, scanned;
 };
 
-template <int LPT>
-__device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int o = 1; o < LPT; o <<= 1) v = fmaxf(v, __shfl_xor(v, o));
+// A value of another lane of the row of 16, in the vector pipe.
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) {
+  return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, true);
+}
+
+// v combined over the LPT lanes of a group, the same bits in each: exchanges
+// with the lane 1 and 2 away, then mirrored eights and sixteens.
+template <int LPT, class T, class F>
+__device__ __forceinline__ T group_all(T v, F f) {
+  auto at = [](T x, auto ctrl) {
+    constexpr int C = decltype(ctrl)::value;
+    if constexpr (sizeof(T) == 8) {
+      const uint64_t u = __builtin_bit_cast(uint64_t, x);
+      return __builtin_bit_cast(T, (uint64_t)(uint32_t)dpp<C>((int)(uint32_t)u) |
+                                       (uint64_t)(uint32_t)dpp<C>((int)(uint32_t)(u >> 32)) << 32);
+    } else {
+      return __builtin_bit_cast(T, dpp<C>(__builtin_bit_cast(int, x)));
+    }
+  };
+  v = f(v, at(v, std::integral_constant<int, 0xB1>{}));
+  v = f(v, at(v, std::integral_constant<int, 0x4E>{}));
+  v = f(v, at(v, std::integral_constant<int, 0x141>{}));
+  if constexpr (LPT >= 16) v = f(v, at(v, std::integral_constant<int, 0x140>{}));
+  if constexpr (LPT >= 32) v = f(v, __shfl_xor(v, 16));
+  if constexpr (LPT >= 64) v = f(v, __shfl_xor(v, 32));
   return v;
 }
 
 template <int LPT>
+__device__ __forceinline__ float group_max(float v) {
+  return group_all<LPT>(v, [](float x, float y) { return fmaxf(x, y); });
+}
+
+template <int LPT>
 __device__ __forceinline__ float group_sum(float v) {
+  return group_all<LPT>(v, [](float x, float y) { return x + y; });
+}
+
+template <int LPT>
+__device__ __forceinline__ uint32_t group_umax(uint32_t v) {
+  return group_all<LPT>(v, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
+}
+
+// exp(d), d <= 0 (NaN as -150, exp of which is 0): 2^n times 2^f with n the
+// whole part of d log2(e) and f, within a half, from the product's two parts.
+__device__ __forceinline__ float exp_le0(float d) {
+  d = fmaxf(d, -150.f);
+  const float hi = 1.44269502f, lo = 1.92596299e-8f;  // log2(e)
+  const float n = __builtin_rintf(d * hi);
+  const float f = __builtin_fmaf(d, lo, __builtin_fmaf(d, hi, -n));
+  return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
+}
+
+// Keys that order the logits of a token, the lower expert first among equals,
+// all different.  BF16: the ordered bits (negative numbers complemented) and
+// the expert's complement below them.  fp32: the value as a double, whose
+// significand has 29 bits to spare, with the expert (or its complement, where
+// more is larger) in the last ten.  none(): below every key.
+struct KeyBf16 {
+  using T = uint32_t;
+  static __device__ __forceinline__ T none() { return 0u; }
+  static __device__ __forceinline__ T make(float v, uint32_t e) {
+    const uint32_t u = __float_as_uint(v + 0.f);  // -0 as +0
+    return ((u & 0x80000000u ? ~u : u | 0x80000000u) & 0xffff0000u) | (0xffffu - e);
+  }
+  static __device__ __forceinline__ T max(T x, T y) { return x > y ? x : y; }
+  static __device__ __forceinline__ T min(T x, T y) { return x > y ? y : x; }
+  static __device__ __forceinline__ uint32_t expert(T k) { return 0xffffu - (k & 0xffffu); }
+  static __device__ __forceinline__ float value(T k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fff0000u : ~(k | 0xffffu));
+  }
+};
+
+struct KeyF32 {
+  using T = double;
+  static __device__ __forceinline__ T none() { return -__builtin_inf(); }
+  static __device__ __forceinline__ T make(float v, uint32_t e) {
+    const float z = v + 0.f;  // -0 as +0
+    return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, (double)z) |
+                                          (z < 0.f ? e : 1023u - e));
+  }
+  // (written out: no operand is a NaN that would have to be made quiet first)
+  static __device__ __forceinline__ T max(T x, T y) {
+    T r;
+    asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(x), "v"(y));
+    return r;
+  }
+  static __device__ __forceinline__ T min(T x, T y) {
+    T r;
+    asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(x), "v"(y));
+    return r;
+  }
+  static __device__ __forceinline__ uint32_t expert(T k) {
+    const uint32_t e = (uint32_t)__builtin_bit_cast(uint64_t, k) & 1023u;
+    return k < 0.0 ? e : 1023u - e;
+  }
+  static __device__ __forceinline__ float value(T k) {
+    return (float)__builtin_bit_cast(double, __builtin_bit_cast(uint64_t, k) & ~1023ull);
+  }
+};
+
+// Sorts N keys, the largest first (odd-even merge sort: 19 exchanges for 8).
+template <class K, int N>
+__device__ __forceinline__ void sort_keys(typename K::T (&k)[N]) {
 #pragma unroll
-  for (int o = 1; o < LPT; o <<= 1) v += __shfl_xor(v, o);
-  return v;
+  for (int p = 1; p < N; p <<= 1)
+#pragma unroll
+    for (int q = p; q >= 1; q >>= 1)
+#pragma unroll
+      for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const typename K::T x = k[i + j], y = k[i + j + q];
+            k[i + j] = K::max(x, y);
+            k[i + j + q] = K::min(x, y);
+          }
 }
 
 // This lane's logits of a token: experts l, l + LPT, ... ; -Inf past E.
@@ -68,106 +182,196 @@ enum TokenState { kEmpty, kRoutes, kBad };
 
 template <int LPT, int VPT>
 __device__ __forceinline__ TokenState token_state(bool on, const float (&v)[VPT], float& top) {
-  float m = -__builtin_inff(), nan = 0.f;
+  float m = -__builtin_inff();
+  uint32_t nan = 0;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     m = fmaxf(m, v[i]);
-    nan = (v[i] != v[i]) ? 1.f : nan;
+    nan = (v[i] != v[i]) ? 1u : nan;
   }
   top = group_max<LPT>(m);
-  const bool bad = group_max<LPT>(nan) != 0.f || top == __builtin_inff();
+  const bool bad = group_umax<LPT>(nan) != 0 || top == __builtin_inff();
   if (!on) return kEmpty;
   if (bad) return kBad;
   return top == -__builtin_inff() ? kEmpty : kRoutes;
 }
 
+struct PlaceSmem {
+  uint64_t chose[2][kMaxExperts];  // tokens 0-63 and 64-127 of the block
+  int off[kMaxExperts];            // the place of the block's first row of an expert
+  int wsum[kRouteWaves];
+  double dsum[kRouteWaves];
+};
+
+// Sum over the block before this thread, and the block's sum.
+__device__ __forceinline__ int block_prefix(int v, int* wsum, int& total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(inc, o);
+    if (lane >= o) inc += u;
+  }
+  if (lane == 63) wsum[wave] = inc;
+  __syncthreads();
+  int at = inc - v;
+  total = 0;
+#pragma unroll
+  for (uint32_t w = 0; w < kRouteWaves; ++w) {
+    at += w < (uint32_t)wave ? wsum[w] : 0;
+    total += wsum[w];
+  }
+  __syncthreads();
+  return at;
+}
+
+// The block's rows to their places; block 0 also writes the tables and the
+// loss.  total(e), ptotal(e): rows and probability sum of expert e over all
+// tokens (total(E): tokens that route); before(e): its rows in earlier blocks;
+// index(i): the expert of the block's row i.  `chose` is filled.
+template <class Total, class PTotal, class Before, class Index>
+__device__ __forceinline__ void place_rows(const RouterArgs& a, uint32_t blk, PlaceSmem& sm,
+                                           Total total, PTotal ptotal, Before before,
+                                           Index index) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  static_assert(kMaxExperts <= kRouteThreads, "one expert a thread");
+  const uint32_t e1 = threadIdx.x;
+  const int c = e1 < a.E ? total(e1) : 0;
+  int rows;
+  const int at = block_prefix(c, sm.wsum, rows);
+  if (e1 < a.E) sm.off[e1] = at + before(e1);
+  __syncthreads();
+  if (blk == 0) {
+    double d = 0.0;
+    if (e1 < a.E) {
+      if (a.counts_) gp<int32_t>(a.counts_)[e1] = c;
+      if (a.offsets_) gp<int32_t>(a.offsets_)[e1] = at;
+      d = (double)c * (double)ptotal(e1);
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) d += __shfl_xor(d, o);
+    if (lane == 0) sm.dsum[wave] = d;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      const int n = total(a.E);
+      if (a.counts_) gp<int32_t>(a.counts_)[a.E] = n;
+      if (a.offsets_) gp<int32_t>(a.offsets_)[a.E] = rows;
+      if (a.loss_) {
+        double s = 0.0;
+        for (uint32_t w = 0; w < kRouteWaves; ++w) s += sm.dsum[w];
+        gp<float>(a.loss_)[0] =
+            n ? (float)(s * (double)a.E / ((double)a.k * (double)n * (double)n)) : 0.f;
+      }
+    }
+  }
+  if (!a.tokens_ && !a.rows_) return;
+  const uint32_t t0 = blk * kRouteTokens;
+  const uint64_t r0 = (uint64_t)t0 * a.k;
+  const uint32_t nr = min(kRouteTokens, a.T - t0) * a.k;
+  for (uint32_t i = threadIdx.x; i < nr; i += kRouteThreads) {
+    const int e = index(i);
+    if (e >= 0) {
+      const uint32_t q = i / a.k;
+      const uint64_t m0 = sm.chose[0][e], m1 = sm.chose[1][e];
+      const uint32_t rank = q < 64 ? __popcll(m0 & ((1ull << q) - 1))
+                                   : __popcll(m0) + __popcll(m1 & ((1ull << (q - 64)) - 1));
+      const uint32_t dst = (uint32_t)sm.off[e] + rank;
+      if (a.tokens_) gp<int32_t>(a.tokens_)[dst] = (int)(t0 + q);
+      if (a.rows_) gp<int32_t>(a.rows_)[dst] = (int)(r0 + i);
+    }
+    if (r0 + i >= (uint64_t)rows) {  // no row of the order lies here
+      if (a.tokens_) gp<int32_t>(a.tokens_)[r0 + i] = -1;
+      if (a.rows_) gp<int32_t>(a.rows_)[r0 + i] = -1;
+    }
+  }
+}
+
 template <bool F32, int LPT, int VPT>
-__global__ void __launch_bounds__(256) route_kernel(RouterArgs a) {
-  constexpr int kTokensPerWave = 64 / LPT;
-  __shared__ uint64_t chose[kMaxExperts];
-  __shared__ float psum[4][LPT * VPT];
+__global__ void __launch_bounds__(kRouteThreads) route_kernel(RouterArgs a) {
+  constexpr uint32_t kTokensPerWave = 64 / LPT;
+  constexpr int KPL = (kMaxTopK + LPT - 1) / LPT;
+  __shared__ PlaceSmem sm;
+  __shared__ float psum[kRouteWaves][LPT * VPT];
+  __shared__ int16_t index[kRouteTokens * kMaxTopK];  // of a batch of one block
   __shared__ int live_s;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l = lane % LPT, grp = lane / LPT;
   const uint32_t t0 = blockIdx.x * kRouteTokens;
-  for (uint32_t e = threadIdx.x; e < a.E; e += 256) chose[e] = 0ull;
+  for (uint32_t e = threadIdx.x; e < a.E; e += kRouteThreads)
+    sm.chose[0][e] = sm.chose[1][e] = 0ull;
   if (threadIdx.x == 0) live_s = 0;
   __syncthreads();
 
   float sum_p[VPT] = {};
   int live = 0;
-  for (uint32_t q = wave * kTokensPerWave + grp; q < kRouteTokens; q += 4 * kTokensPerWave) {
-    const uint32_t t = t0 + q;
-    const bool on = t < a.T && (a.mask_ == 0 || gp<const int32_t>(a.mask_)[t] != 0);
-    float v[VPT], p[VPT], top;
+  const uint32_t here = min(kRouteTokens, a.T - t0);
+  // (a wave stays together: the exchanges take every lane)
+  for (uint32_t q0 = wave * kTokensPerWave; q0 < here; q0 += kRouteWaves * kTokensPerWave) {
+    const uint32_t q = q0 + grp, t = t0 + q;
+    const bool on = q < here && (a.mask_ == 0 || gp<const int32_t>(a.mask_)[min(t, a.T - 1)] != 0);
+    float v[VPT], top;
     load_logits<F32, LPT, VPT>(a.logits_, (uint64_t)min(t, a.T - 1) * a.ls, a.E, l, v);
     const TokenState state = token_state<LPT, VPT>(on, v, top);
-    float s = 0.f;
+    float s = 0.f, p[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      p[i] = expf(v[i] - top);
+      p[i] = exp_le0(v[i] - top);
       s += p[i];
     }
     s = group_sum<LPT>(s);
-    const float nan = __builtin_nanf("");
+    const float nan = __builtin_nanf(""), inv = 1.f / s;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      p[i] = p[i] / s;
-      sum_p[i] += state == kRoutes ? p[i] : state == kBad ? nan : 0.f;
-    }
+    for (int i = 0; i < VPT; ++i)
+      sum_p[i] += state == kRoutes ? p[i] * inv : state == kBad ? nan : 0.f;
     live += state != kEmpty && l == 0;
 
-    // top_k rounds: the lane's best unused logit, then the group's
-    float chosen_sum = 0.f, mine_w[(kMaxTopK + LPT - 1) / LPT];
-    int mine_e[(kMaxTopK + LPT - 1) / LPT];
-    uint32_t used = 0;
+    // Every lane sorts its keys once; a round takes the largest head of the
+    // group's lists.  Lane j of the group (and j + LPT, ...) keeps choice j.
+    using Key = std::conditional_t<F32, KeyF32, KeyBf16>;
+    typename Key::T key[VPT], mine[KPL];
 #pragma unroll
-    for (int i = 0; i < (int)((kMaxTopK + LPT - 1) / LPT); ++i) {
-      mine_e[i] = -1;
-      mine_w[i] = state == kBad ? nan : 0.f;
-    }
+    for (int i = 0; i < VPT; ++i)
+      key[i] = (state == kRoutes && v[i] > -__builtin_inff()) ? Key::make(v[i], l + LPT * i)
+                                                             : Key::none();
+    sort_keys<Key>(key);
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) mine[i] = Key::none();
     for (uint32_t j = 0; j < a.k; ++j) {
-      float best = -__builtin_inff(), bp = 0.f;
-      uint32_t at = 0x7fffffffu;
+      const typename Key::T best =
+          group_all<LPT>(key[0], [](auto x, auto y) { return Key::max(x, y); });
+      const bool own = key[0] == best;
+      typename Key::T next[VPT];
 #pragma unroll
-      for (int i = 0; i < VPT; ++i)
-        if (!((used >> i) & 1) && v[i] > best) {
-          best = v[i];
-          bp = p[i];
-          at = l + LPT * i;
-        }
+      for (int i = 0; i + 1 < VPT; ++i) next[i] = key[i + 1];
+      next[VPT - 1] = Key::none();
 #pragma unroll
-      for (int o = 1; o < LPT; o <<= 1) {
-        const float ob = __shfl_xor(best, o), op = __shfl_xor(bp, o);
-        const uint32_t oa = __shfl_xor(at, o);
-        if (ob > best || (ob == best && oa < at)) {
-          best = ob;
-          bp = op;
-          at = oa;
-        }
-      }
-      if (at != 0x7fffffffu && at % LPT == (uint32_t)l) used |= 1u << (at / LPT);
-      const bool ok = state == kRoutes && at != 0x7fffffffu;
-      if (ok) {
-        chosen_sum += bp;
-        if (l == 0) atomicOr((unsigned long long*)&chose[at], 1ull << q);
-      }
+      for (int i = 0; i < VPT; ++i) key[i] = own ? next[i] : key[i];
 #pragma unroll
-      for (int i = 0; i < (int)((kMaxTopK + LPT - 1) / LPT); ++i)
-        if (ok && j == (uint32_t)(l + LPT * i)) {
-          mine_e[i] = (int)at;
-          mine_w[i] = bp;
-        }
+      for (int i = 0; i < KPL; ++i) mine[i] = j == (uint32_t)(l + LPT * i) ? best : mine[i];
     }
-    if (t < a.T) {
+    int mine_e[KPL];
+    float w[KPL], chosen = 0.f;
 #pragma unroll
-      for (int i = 0; i < (int)((kMaxTopK + LPT - 1) / LPT); ++i) {
+    for (int i = 0; i < KPL; ++i) {
+      const bool ok = mine[i] != Key::none();
+      mine_e[i] = ok ? (int)Key::expert(mine[i]) : -1;
+      w[i] = ok ? exp_le0(Key::value(mine[i]) - top) * inv : 0.f;
+      chosen += w[i];
+    }
+    chosen = group_sum<LPT>(chosen);
+    if (q < here) {
+#pragma unroll
+      for (int i = 0; i < KPL; ++i) {
         const uint32_t j = l + LPT * i;
-        if (j < a.k) {
-          const float w = (a.norm && mine_e[i] >= 0) ? mine_w[i] / chosen_sum : mine_w[i];
-          gp<int32_t>(a.indices_)[(uint64_t)t * a.k + j] = mine_e[i];
-          gp<float>(a.weights_)[(uint64_t)t * a.k + j] = w;
+        if (j >= a.k) continue;
+        if (mine_e[i] >= 0) {
+          atomicOr((unsigned long long*)&sm.chose[q >> 6][mine_e[i]], 1ull << (q & 63));
+          if (a.norm) w[i] /= chosen;
         }
+        if (state == kBad) w[i] = nan;
+        index[q * a.k + j] = (int16_t)mine_e[i];
+        gp<int32_t>(a.indices_)[(uint64_t)t * a.k + j] = mine_e[i];
+        gp<float>(a.weights_)[(uint64_t)t * a.k + j] = w[i];
       }
     }
   }
@@ -181,144 +385,134 @@ __global__ void __launch_bounds__(256) route_kernel(RouterArgs a) {
   }
   if (live) atomicAdd(&live_s, live);
   __syncthreads();
-  for (uint32_t e = threadIdx.x; e < a.E; e += 256) {
-    gp<int32_t>(a.cnt_)[(uint64_t)e * a.nblk + blockIdx.x] = __popcll(chose[e]);
-    gp<float>(a.psum_)[(uint64_t)e * a.nblk + blockIdx.x] =
-        (psum[0][e] + psum[1][e]) + (psum[2][e] + psum[3][e]);
+  auto block_psum = [&](uint32_t e) {
+    float s = psum[0][e];
+    for (uint32_t w = 1; w < kRouteWaves; ++w) s += psum[w][e];
+    return s;
+  };
+  auto block_count = [&](uint32_t e) {
+    return e == a.E ? live_s : (int)(__popcll(sm.chose[0][e]) + __popcll(sm.chose[1][e]));
+  };
+  if (a.nblk > 1) {
+    for (uint32_t e = threadIdx.x; e <= a.E; e += kRouteThreads) {
+      gp<int32_t>(a.cnt_)[(uint64_t)blockIdx.x * (a.E + 1) + e] = block_count(e);
+      if (e < a.E) gp<float>(a.psum_)[(uint64_t)blockIdx.x * a.E + e] = block_psum(e);
+    }
+    return;
   }
-  if (threadIdx.x == 0) gp<int32_t>(a.cnt_)[(uint64_t)a.E * a.nblk + blockIdx.x] = live_s;
+  place_rows(a, 0, sm, block_count, block_psum, [](uint32_t) { return 0; },
+             [&](uint32_t i) { return (int)index[i]; });
 }
 
-// One block per expert (and one for the routing tokens): its counts become
-// the exclusive prefix sums over the blocks of tokens.
-__global__ void __launch_bounds__(256) router_scan_kernel(RouterArgs a) {
-  __shared__ int wsum[4];
-  __shared__ float fsum[4];
-  const uint32_t e = blockIdx.x;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  RLD_GLOBAL int32_t* cnt = gp<int32_t>(a.cnt_) + (uint64_t)e * a.nblk;
-  int before = 0;
+// 16 experts a block (and the tokens that route): the counts become the
+// exclusive prefix sums over the blocks of tokens, in 64 runs of blocks.
+__global__ void __launch_bounds__(1024) router_scan_kernel(RouterArgs a) {
+  __shared__ int run[64][16];
+  __shared__ float frun[64][16];
+  const int l = threadIdx.x & 15, part = threadIdx.x >> 4;
+  const uint32_t e = blockIdx.x * 16 + l, w = a.E + 1;
+  const uint32_t per = (a.nblk + 63) / 64, b0 = min(part * per, a.nblk), b1 = min(b0 + per, a.nblk);
+  RLD_GLOBAL int32_t* cnt = gp<int32_t>(a.cnt_);
+  int n = 0;
   float ps = 0.f;
-  for (uint32_t b0 = 0; b0 < a.nblk; b0 += 256) {
-    const uint32_t b = b0 + threadIdx.x;
-    const int c = b < a.nblk ? cnt[b] : 0;
-    if (b < a.nblk && e < a.E) ps += gp<const float>(a.psum_)[(uint64_t)e * a.nblk + b];
-    int inc = c;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int u = __shfl_up(inc, o);
-      if (lane >= o) inc += u;
-    }
-    if (lane == 63) wsum[wave] = inc;
-    __syncthreads();
-    int off = before, tot = 0;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      off += w < wave ? wsum[w] : 0;
-      tot += wsum[w];
-    }
-    if (b < a.nblk) cnt[b] = off + inc - c;
-    before += tot;
-    __syncthreads();
+#pragma unroll 8
+  for (uint32_t b = b0; b < b1; ++b) {
+    n += e < w ? cnt[(uint64_t)b * w + e] : 0;
+    ps += e < a.E ? gp<const float>(a.psum_)[(uint64_t)b * a.E + e] : 0.f;
   }
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) ps += __shfl_xor(ps, o);
-  if (lane == 0) fsum[wave] = ps;
+  run[part][l] = n;
+  frun[part][l] = ps;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    gp<int32_t>(a.total_)[e] = before;
-    if (e < a.E) gp<float>(a.ptotal_)[e] = (fsum[0] + fsum[1]) + (fsum[2] + fsum[3]);
+  if (e >= w) return;
+  int at = 0, total = 0;
+  float ptotal = 0.f;
+#pragma unroll 16
+  for (int i = 0; i < 64; ++i) {
+    at += i < part ? run[i][l] : 0;
+    total += run[i][l];
+    ptotal += frun[i][l];
+  }
+  for (uint32_t b = b0; b < b1; b += 8) {
+    int c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = b + i < b1 ? cnt[(uint64_t)(b + i) * w + e] : 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (b + i < b1) {
+        cnt[(uint64_t)(b + i) * w + e] = at;
+        at += c[i];
+      }
+  }
+  if (part == 0) {
+    gp<int32_t>(a.total_)[e] = total;
+    if (e < a.E) gp<float>(a.ptotal_)[e] = ptotal;
   }
 }
 
-// One block per 64 tokens: the rows' places.  Every block adds up the experts'
-// totals itself; block 0 also writes the tables and the loss.
-__global__ void __launch_bounds__(256) router_place_kernel(RouterArgs a) {
-  __shared__ uint64_t chose[kMaxExperts];
-  __shared__ int off[kMaxExperts];
-  __shared__ int wsum[4];
-  __shared__ double dsum[4];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint32_t t0 = blockIdx.x * kRouteTokens;
-  // four consecutive experts a thread
-  int c[4], sum = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t e = threadIdx.x * 4 + i;
-    c[i] = e < a.E ? gp<const int32_t>(a.total_)[e] : 0;
-    sum += c[i];
-    if (e < a.E) chose[e] = 0ull;
-  }
-  int inc = sum;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(inc, o);
-    if (lane >= o) inc += u;
-  }
-  if (lane == 63) wsum[wave] = inc;
-  __syncthreads();
-  int at = inc - sum, total = 0;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    at += w < wave ? wsum[w] : 0;
-    total += wsum[w];
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t e = threadIdx.x * 4 + i;
-    if (e < a.E) off[e] = at;
-    at += c[i];
+// One block per 128 tokens.  Without the scan the block adds up all blocks'
+// counts itself, and block 0 the probability sums (experts over the lanes, every
+// `parts`-th block of tokens a thread; the threads' sums in order).
+__global__ void __launch_bounds__(kRouteThreads) router_place_kernel(RouterArgs a) {
+  __shared__ PlaceSmem sm;
+  __shared__ int all[kMaxExperts + 1], early[kMaxExperts + 1];
+  __shared__ float ps[kRouteThreads];
+  const uint32_t w = a.E + 1, blk = blockIdx.x;
+  for (uint32_t e = threadIdx.x; e < w; e += kRouteThreads) {
+    all[e] = early[e] = 0;
+    if (e < a.E) sm.chose[0][e] = sm.chose[1][e] = 0ull;
   }
   __syncthreads();
-
-  if (blockIdx.x == 0) {
-    double d = 0.0;
-    for (uint32_t e = threadIdx.x; e < a.E; e += 256) {
-      const int n = gp<const int32_t>(a.total_)[e];
-      if (a.counts_) gp<int32_t>(a.counts_)[e] = n;
-      if (a.offsets_) gp<int32_t>(a.offsets_)[e] = off[e];
-      d += (double)n * (double)gp<const float>(a.ptotal_)[e];
+  const RLD_GLOBAL int32_t* cnt = gp<const int32_t>(a.cnt_);
+  const uint32_t parts = kRouteThreads / a.E, part = threadIdx.x / a.E, e1 = threadIdx.x % a.E;
+  if (a.scanned) {
+    for (uint32_t e = threadIdx.x; e < w; e += kRouteThreads) {
+      all[e] = gp<const int32_t>(a.total_)[e];
+      early[e] = cnt[(uint64_t)blk * w + e];
     }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) d += __shfl_xor(d, o);
-    if (lane == 0) dsum[wave] = d;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      const int n = gp<const int32_t>(a.total_)[a.E];
-      if (a.counts_) gp<int32_t>(a.counts_)[a.E] = n;
-      if (a.offsets_) gp<int32_t>(a.offsets_)[a.E] = total;
-      if (a.loss_) {
-        const double s = (dsum[0] + dsum[1]) + (dsum[2] + dsum[3]);
-        gp<float>(a.loss_)[0] =
-            n ? (float)(s * (double)a.E / ((double)a.k * (double)n * (double)n)) : 0.f;
+  } else {
+    if (part < parts) {
+      int n = 0, m = 0;
+      float p = 0.f;
+#pragma unroll 16
+      for (uint32_t b = part; b < a.nblk; b += parts) {
+        const int c = cnt[(uint64_t)b * w + e1];
+        n += c;
+        m += b < blk ? c : 0;
       }
+      if (blk == 0) {
+#pragma unroll 16
+        for (uint32_t b = part; b < a.nblk; b += parts)
+          p += gp<const float>(a.psum_)[(uint64_t)b * a.E + e1];
+      }
+      ps[threadIdx.x] = p;
+      atomicAdd(&all[e1], n);  // whole numbers: any order gives the same sum
+      atomicAdd(&early[e1], m);
+    }
+    if (blk == 0) {
+      int n = 0;
+      for (uint32_t b = threadIdx.x; b < a.nblk; b += kRouteThreads) n += cnt[(uint64_t)b * w + a.E];
+      if (n) atomicAdd(&all[a.E], n);
     }
   }
-  if (!a.tokens_ && !a.rows_) return;
-
-  const uint32_t nt = min(kRouteTokens, a.T - t0);
+  const uint32_t t0 = blk * kRouteTokens;
   const uint64_t r0 = (uint64_t)t0 * a.k;
-  const uint32_t nr = nt * a.k;
-  for (uint32_t i = threadIdx.x; i < nr; i += 256) {
+  const uint32_t nr = min(kRouteTokens, a.T - t0) * a.k;
+  for (uint32_t i = threadIdx.x; i < nr; i += kRouteThreads) {
     const int e = gp<const int32_t>(a.indices_)[r0 + i];
-    if (e >= 0) atomicOr((unsigned long long*)&chose[e], 1ull << (i / a.k));
+    const uint32_t q = i / a.k;
+    if (e >= 0) atomicOr((unsigned long long*)&sm.chose[q >> 6][e], 1ull << (q & 63));
   }
   __syncthreads();
-  for (uint32_t i = threadIdx.x; i < nr; i += 256) {
-    const int e = gp<const int32_t>(a.indices_)[r0 + i];
-    if (e >= 0) {
-      const uint32_t q = i / a.k;
-      const uint64_t dst = (uint64_t)off[e] +
-                           gp<const int32_t>(a.cnt_)[(uint64_t)e * a.nblk + blockIdx.x] +
-                           __popcll(chose[e] & ((1ull << q) - 1));
-      if (a.tokens_) gp<int32_t>(a.tokens_)[dst] = (int)(t0 + q);
-      if (a.rows_) gp<int32_t>(a.rows_)[dst] = (int)(r0 + i);
-    }
-    if (r0 + i >= (uint64_t)total) {  // no row of the order lies here
-      if (a.tokens_) gp<int32_t>(a.tokens_)[r0 + i] = -1;
-      if (a.rows_) gp<int32_t>(a.rows_)[r0 + i] = -1;
-    }
-  }
+  place_rows(
+      a, blk, sm, [&](uint32_t e) { return all[e]; },
+      [&](uint32_t e) {
+        if (a.scanned) return gp<const float>(a.ptotal_)[e];
+        float p = ps[e];
+        for (uint32_t i = 1; i < parts; ++i) p += ps[i * a.E + e];
+        return p;
+      },
+      [&](uint32_t e) { return early[e]; },
+      [&](uint32_t i) { return gp<const int32_t>(a.indices_)[r0 + i]; });
 }
 
 // ------------------------------------------------------------------- grad ----
@@ -336,6 +530,7 @@ template <bool F32, int LPT, int VPT>
 __global__ void __launch_bounds__(256) router_grad_kernel(RouterGradArgs a) {
   constexpr int KPL = (kMaxTopK + LPT - 1) / LPT;
   constexpr uint32_t kTokens = 256 / LPT;
+  __shared__ float spread[kTokens][LPT * VPT];
   const int lane = threadIdx.x & 63;
   const int l = lane % LPT;
   const uint32_t t = blockIdx.x * kTokens + threadIdx.x / LPT;
@@ -347,12 +542,12 @@ __global__ void __launch_bounds__(256) router_grad_kernel(RouterGradArgs a) {
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    v[i] = expf(v[i] - top);
+    v[i] = exp_le0(v[i] - top);
     s += v[i];
   }
-  s = group_sum<LPT>(s);
+  const float inv = 1.f / group_sum<LPT>(s);
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) v[i] = v[i] / s;  // p
+  for (int i = 0; i < VPT; ++i) v[i] *= inv;  // p
 
   float coef = 0.f;
   if (a.dloss_) {
@@ -371,7 +566,11 @@ __global__ void __launch_bounds__(256) router_grad_kernel(RouterGradArgs a) {
   for (int i = 0; i < VPT; ++i) d[i] = v[i] * (d[i] - dot);
 
   if (a.dw_) {
-    // lane j of the group (and j + LPT, ...) takes chosen expert j
+    // lane j of the group (and j + LPT, ...) takes chosen expert j and adds its
+    // gradient at that expert's place in LDS, which the expert's lane reads
+    float* const add = spread[threadIdx.x / LPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) add[l + LPT * i] = 0.f;
     int at[KPL];
     float w[KPL], dw[KPL], wsum = 0.f;
 #pragma unroll
@@ -387,7 +586,7 @@ __global__ void __launch_bounds__(256) router_grad_kernel(RouterGradArgs a) {
           const float lv = F32 ? gp<const float>(a.logits_)[le]
                                : bf16_to_f32(gp<const uint16_t>(a.logits_)[le]);
           at[i] = e;
-          w[i] = expf(lv - top) / s;
+          w[i] = exp_le0(lv - top) * inv;
           dw[i] = gp<const float>(a.dw_)[(uint64_t)tc * a.k + j];
         }
       }
@@ -401,21 +600,15 @@ __global__ void __launch_bounds__(256) router_grad_kernel(RouterGradArgs a) {
       wd += w[i] * dw[i];
     }
     wd = group_sum<LPT>(wd);
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int i = 0; i < KPL; ++i) w[i] *= a.norm ? dw[i] - wd : dw[i];
-    if (!a.norm) {
+    for (int i = 0; i < KPL; ++i)
+      if (at[i] >= 0) atomicAdd(&add[at[i]], w[i] * (a.norm ? dw[i] - wd : dw[i]));
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) d[i] -= v[i] * wd;
-    }
-#pragma unroll
-    for (int i = 0; i < KPL; ++i) {
-      for (uint32_t j = 0; j < (uint32_t)LPT && j + LPT * i < a.k; ++j) {
-        const int e = __shfl(at[i], (int)j, LPT);
-        const float add = __shfl(w[i], (int)j, LPT);
-#pragma unroll
-        for (int q = 0; q < VPT; ++q)
-          if (e == l + LPT * q) d[q] += add;
-      }
+    for (int i = 0; i < VPT; ++i) {
+      if (!a.norm) d[i] -= v[i] * wd;
+      d[i] += add[l + LPT * i];
     }
   }
   if (t >= a.T) return;
@@ -459,7 +652,7 @@ static void by_experts(bool f32, uint32_t E, const A& a, hipStream_t st) {
 template <bool F32, int LPT, int VPT>
 struct Route {
   static void go(const RouterArgs& a, hipStream_t st) {
-    route_kernel<F32, LPT, VPT><<<a.nblk, 256, 0, st>>>(a);
+    route_kernel<F32, LPT, VPT><<<a.nblk, kRouteThreads, 0, st>>>(a);
   }
 };
 
@@ -530,6 +723,7 @@ extern "C" int rld_moe_router(const void* logits, int logits_f32, uint32_t logit
   a.k = top_k;
   a.norm = norm_topk ? 1u : 0u;
   a.nblk = div_ceil(num_tokens, kRouteTokens);
+  a.scanned = a.nblk > kScanBlocks ? 1u : 0u;
   const uint64_t cells = (uint64_t)(num_experts + 1) * a.nblk;
   a.cnt_ = (uint64_t)workspace;
   a.psum_ = a.cnt_ + cells * 4;
@@ -539,9 +733,12 @@ extern "C" int rld_moe_router(const void* logits, int logits_f32, uint32_t logit
   int r = launch_status();
   if (r) return r;
   if (!counts && !expert_offsets && !sorted_token_ids && !sorted_rows && !loss) return RLD_OK;
-  router_scan_kernel<<<num_experts + 1, 256, 0, st>>>(a);
-  if ((r = launch_status())) return r;
-  router_place_kernel<<<a.nblk, 256, 0, st>>>(a);
+  if (a.nblk == 1) return RLD_OK;  // placed in the first launch
+  if (a.scanned) {
+    router_scan_kernel<<<div_ceil(num_experts + 1, 16), 1024, 0, st>>>(a);
+    if ((r = launch_status())) return r;
+  }
+  router_place_kernel<<<a.nblk, kRouteThreads, 0, st>>>(a);
   return launch_status();
 }
 

@@ -225,7 +225,7 @@ def logits_of(rng, T, E, odd=True):
     return l
 
 
-SIZES = [(1, 1, 1), (1, 128, 8), (3, 5, 5), (8, 2, 1), (32, 128, 8), (63, 60, 4), (64, 64, 6),
+SIZES = [(128, 128, 8), (129, 40, 3), (66000, 8, 2), (1, 1, 1), (1, 128, 8), (3, 5, 5), (8, 2, 1), (32, 128, 8), (63, 60, 4), (64, 64, 6),
          (65, 65, 3), (130, 8, 8), (200, 129, 32), (257, 256, 8), (70, 257, 10), (90, 512, 8),
          (77, 513, 2), (66, 1024, 32), (1000, 160, 6)]
 

@@ -152,4 +152,4 @@ def test_workspace_sizes_grow_with_the_call():
     assert g(4, 64, 128, 16, 0) == 0 and g(0, 64, 128, 16, 4) > 0
     assert g(5, 4096, 128, 16, 4) > g(4, 4096, 128, 16, 4)
     r = R.rld_moe_router_workspace_bytes
-    assert r(0, 128, 8) == 0 and r(65, 128, 8) > r(64, 128, 8) > 0
+    assert r(0, 128, 8) == 0 and r(129, 128, 8) > r(128, 128, 8) > 0

@@ -32,6 +32,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 #define RLD_LDS __attribute__((address_space(3)))
 #define RLD_CONST __attribute__((address_space(4)))
 
+constexpr uint32_t kFinishRows = 64;  // positions of a finish block of a large call
 constexpr uint32_t kLowRows = 64;    // rows of a low item
 constexpr uint32_t kLowChunk = 512;  // k elements of a low item, at least
 constexpr uint32_t kMaxStride = 1u << 21;
@@ -297,6 +298,40 @@ __device__ __forceinline__ void store_low(const LowArgs& a, uint32_t from, uint3
   }
 }
 
+// A slot's two table entries, of which `mine` is the matrix of the product at
+// hand.  Up to 64 slots the wave loads the whole tables, one slot a lane, while
+// the rows' slot ids are still on their way.
+struct SlotTables {
+  uint64_t mine, other;  // this lane's slot
+  uint64_t mtab, otab;
+  bool held;
+  __device__ __forceinline__ SlotTables(uint64_t m, uint64_t o, uint32_t max_loras)
+      : mtab(m), otab(o), held(max_loras <= 64) {
+    const uint32_t lane = threadIdx.x & 63;
+    mine = other = 0;
+    if (held && lane < max_loras) {
+      mine = gp<const uint64_t>(m)[lane];
+      other = gp<const uint64_t>(o)[lane];
+    }
+  }
+  // of a slot that is the same in the whole wave; 0: not adapted
+  __device__ __forceinline__ uint64_t at(int s) const {
+    uint64_t a, b;
+    if (held) {
+      a = lane64(mine, s);
+      b = lane64(other, s);
+    } else {
+      a = uniform64(gp<const uint64_t>(mtab)[s]);
+      b = uniform64(gp<const uint64_t>(otab)[s]);
+    }
+    return a != 0ull && b != 0ull ? a : 0ull;
+  }
+  static __device__ __forceinline__ uint64_t lane64(uint64_t v, int l) {
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, l) |
+           (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), l) << 32;
+  }
+};
+
 // The r-th set bit of m (r below their number).
 __device__ __forceinline__ uint32_t nth_bit(uint64_t m, uint32_t r) {
   uint32_t at = 0;
@@ -333,6 +368,7 @@ __device__ __forceinline__ void low_item(const LowArgs& a, uint32_t item, unsign
   const uint32_t lds0 = lds_addr(lds);
   const uint64_t zeros = (uint64_t)&g_zero16[0];
 
+  const SlotTables tables(a.mtab_, a.otab_, a.max_loras);
   const int key = pos0 + lane < a.n ? gp<const int32_t>(a.key_)[pos0 + lane] : -1;
   const int row_of = (a.order_ && pos0 + lane < a.n) ? gp<const int32_t>(a.order_)[pos0 + lane]
                                                      : (int)(pos0 + lane);
@@ -342,9 +378,8 @@ __device__ __forceinline__ void low_item(const LowArgs& a, uint32_t item, unsign
     const uint64_t mine = __ballot(key == s);
     left &= ~mine;
     if (idx % a.nz != z) continue;
-    const uint64_t mt = uniform64(gp<const uint64_t>(a.mtab_)[s]);
-    const uint64_t ot = uniform64(gp<const uint64_t>(a.otab_)[s]);
-    if (mt == 0ull || ot == 0ull) continue;
+    const uint64_t mt = tables.at(s);
+    if (mt == 0ull) continue;
     const uint32_t cnt = __popcll(mine);
 
     // this wave's loads of a stage: two of eight rows of x, two of the matrix
@@ -462,6 +497,7 @@ __device__ __forceinline__ void low_sum(const LowArgs& a, uint32_t block) {
   const int s = gp<const int32_t>(a.key_)[pos];
   if (s < 0 || (uint32_t)s >= a.max_loras) return;
   floatx4 sum = {};
+#pragma unroll 8
   for (uint32_t ch = 0; ch < a.nch; ++ch)
     sum += gp<const floatx4>(a.partial_)[(size_t)ch * a.n * q + t];
   store_low(a, pos, (uint32_t)(t % q) * 4, sum * gp<const float>(a.stab_)[s]);
@@ -719,13 +755,13 @@ struct FinishArgs {
   uint32_t low_sorted;
 };
 
-// 16 positions x 64 columns, 16 columns a wave: the splits of the product, in
-// order, plus the low rows times their slots' second matrices.  A slot's
+// 16 * MI positions x 64 columns, 16 columns a wave: the splits of the product,
+// in order, plus the low rows times their slots' second matrices.  A slot's
 // product is made apart and added to its own rows alone (a NaN or infinity of
 // its matrix would survive zeros in the others).  KS: 32-wide steps of rank.
 // TRANS: the matrices are [R][N]; their 64 columns go through LDS (32 KB) and
 // transposing reads.
-template <int KS, bool TRANS>
+template <int KS, int MI, bool TRANS>
 __device__ __forceinline__ void finish_item(const FinishArgs& a, uint32_t item,
                                             unsigned char* lds) {
   constexpr int SB = KS == 1 ? 8 : KS == 2 ? 4 : 2;  // slots whose matrices are loaded at once
@@ -733,96 +769,119 @@ __device__ __forceinline__ void finish_item(const FinishArgs& a, uint32_t item,
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, c = lane & 15;
   const uint32_t tile0 = item % a.tiles * 64, col0 = tile0 + wave * 16;
-  const uint32_t pos0 = item / a.tiles * 16;
-  const uint32_t pos = pos0 + c, at = min(pos, a.n - 1);
-  int key = gp<const int32_t>(a.key_)[at];
-  const uint32_t row = a.order_ ? (uint32_t)gp<const int32_t>(a.order_)[at] : at;
-  if (pos >= a.n || key < 0 || (uint32_t)key >= a.max_loras) key = -1;
+  const uint32_t pos0 = item / a.tiles * (16 * MI);
+  const SlotTables tables(a.etab_, a.otab_, a.max_loras);
   const uint32_t col = col0 + 4 * g;
   const bool in_col = col < a.N;
-
-  floatx4 acc = floatx4{0.f, 0.f, 0.f, 0.f};
-  for (uint32_t sp = 0; sp < a.splits; sp += 4) {
-    floatx4 v[4];
+  int key[MI], left[MI];
+  uint32_t row[MI];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w = min(sp + i, a.splits - 1);
-      v[i] = gp<const floatx4>(
-          a.sum_ + (((uint64_t)w * a.n + row) * a.N + (in_col ? col : 0u)) * 4)[0];
+  for (int mi = 0; mi < MI; ++mi) {
+    const uint32_t pos = pos0 + mi * 16 + c, at = min(pos, a.n - 1);
+    key[mi] = gp<const int32_t>(a.key_)[at];
+    row[mi] = a.order_ ? (uint32_t)gp<const int32_t>(a.order_)[at] : at;
+    if (pos >= a.n || key[mi] < 0 || (uint32_t)key[mi] >= a.max_loras) key[mi] = -1;
+    left[mi] = key[mi];
+  }
+
+  floatx4 acc[MI];
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) acc[mi] = floatx4{0.f, 0.f, 0.f, 0.f};
+  constexpr int SP = MI == 1 ? 4 : 2;  // splits loaded at once
+  for (uint32_t sp = 0; sp < a.splits; sp += SP) {
+    floatx4 v[SP][MI];
+#pragma unroll
+    for (int i = 0; i < SP; ++i) {
+      const uint64_t at =
+          a.sum_ + ((uint64_t)min(sp + i, a.splits - 1) * a.n * a.N + (in_col ? col : 0u)) * 4;
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+        v[i][mi] = *gp<const floatx4>(at + (uint64_t)row[mi] * a.N * 4);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (sp + i < a.splits) acc += v[i];
+    for (int i = 0; i < SP; ++i)
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+        if (sp + i < a.splits) acc[mi] += v[i][mi];
   }
-  uint64_t e = 0;
-  if (key >= 0) {
-    e = gp<const uint64_t>(a.etab_)[key];
-    if (e == 0ull || gp<const uint64_t>(a.otab_)[key] == 0ull) key = -1;
-  }
-  const uint32_t lat = a.low_sorted ? pos : row;
+
+  auto next_slot = [&]() {
+    int first = -1;
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) first = first < 0 ? left[mi] : first;
+    const uint64_t m = __ballot(first >= 0);
+    if (!m) return -1;
+    const int s = __builtin_amdgcn_readlane(first, __builtin_ctzll(m));
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) left[mi] = left[mi] == s ? -1 : left[mi];
+    return s;
+  };
+  int s = next_slot();
   [[maybe_unused]] const uint32_t lds0 = lds_addr(lds);
-  uint64_t left = __ballot(key >= 0 && lane < 16);
-  if (left) {
-    uint4 hi[KS], lo[KS];
+  if (s >= 0) {
+    uint4 hi[MI][KS], lo[MI][KS];
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const uint32_t k = ks * 32 + 8 * g;
-      hi[ks] = lo[ks] = zero16();
-      if (key >= 0 && k < a.R) {
-        if (a.parts_) {
-          const RLD_GLOBAL uint16_t* p = gp<const uint16_t>(a.parts_) + (size_t)lat * 2 * a.R + k;
-          hi[ks] = load16(p);
-          lo[ks] = load16(p + a.R);
-        } else {
-          floatx4 u = {}, v = {};
-          for (uint32_t ch = 0; ch < a.nch; ++ch) {
-            const RLD_GLOBAL floatx4* p =
-                gp<const floatx4>(a.partial_ + (((size_t)ch * a.n + lat) * a.R + k) * 4);
-            u += p[0];
-            v += p[1];
-          }
-          const float sc = gp<const float>(a.stab_)[key];
-          float f[8];
+    for (int mi = 0; mi < MI; ++mi) {
+      const uint32_t at = a.low_sorted ? pos0 + mi * 16 + c : row[mi];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            f[i] = u[i] * sc;
-            f[4 + i] = v[i] * sc;
+      for (int ks = 0; ks < KS; ++ks) {
+        const uint32_t k = ks * 32 + 8 * g;
+        hi[mi][ks] = lo[mi][ks] = zero16();
+        if (key[mi] >= 0 && k < a.R) {
+          if (a.parts_) {
+            const RLD_GLOBAL uint16_t* p = gp<const uint16_t>(a.parts_) + (size_t)at * 2 * a.R + k;
+            hi[mi][ks] = load16(p);
+            lo[mi][ks] = load16(p + a.R);
+          } else {
+            floatx4 u = {}, v = {};
+#pragma unroll 8
+            for (uint32_t ch = 0; ch < a.nch; ++ch) {
+              const RLD_GLOBAL floatx4* p =
+                  gp<const floatx4>(a.partial_ + (((size_t)ch * a.n + at) * a.R + k) * 4);
+              u += p[0];
+              v += p[1];
+            }
+            const float sc = gp<const float>(a.stab_)[key[mi]];
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              f[i] = u[i] * sc;
+              f[4 + i] = v[i] * sc;
+            }
+            uint4 two[2];
+            bf16_parts<2>(f, two);
+            hi[mi][ks] = two[0];
+            lo[mi][ks] = two[1];
           }
-          uint4 two[2];
-          bf16_parts<2>(f, two);
-          hi[ks] = two[0];
-          lo[ks] = two[1];
         }
       }
     }
-    while (left) {
-      int s[SB];
+    while (s >= 0) {
+      int of[SB];  // the slots of this turn; -1: none, or not adapted
       uint4 ef[SB][KS];
 #pragma unroll
       for (int b = 0; b < SB; ++b) {
-        // none left: the last slot again, its product not added
-        const int from = left ? __builtin_ctzll(left) : 0;
-        s[b] = left ? __builtin_amdgcn_readlane(key, from) : -2;
-        const uint64_t eb = left ? (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)e, from) |
-                                       (uint64_t)(uint32_t)__builtin_amdgcn_readlane(
-                                           (int)(uint32_t)(e >> 32), from) << 32
-                                 : 0ull;
-        left &= ~__ballot(key == s[b]);
+        of[b] = s;
+        if (s >= 0) {
+          const uint64_t eb = tables.at(s);
+          if (eb == 0ull) of[b] = -1;
+          s = next_slot();
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          [[maybe_unused]] const uint32_t k = ks * 32 + 8 * g;
-          [[maybe_unused]] const bool in = s[b] >= 0 && k < a.R && col0 + c < a.N;
-          if constexpr (!TRANS) {
-            ef[b][ks] = buffer_load16(eb + (uint64_t)col0 * a.R * 2, s[b] >= 0 ? kBufferEnd : 0u,
-                                      in ? (c * a.R + k) * 2 : kBufferEnd);
-          } else {
-            const uint32_t r = ks * 32 + wave * 8 + (lane >> 3);
-            const uint32_t h = ((r >> 1) & 1) | ((r >> 3) & 1) << 1;
-            const uint32_t cc = (((lane & 7) >> 1 ^ h) * 2 + (lane & 1)) * 8;
-            const rsrc_t re = buffer(eb + (uint64_t)tile0 * 2,
-                                     s[b] >= 0 ? ((uint64_t)a.R * a.N - tile0) * 2 : 0u);
-            dma16(re, lds0 + (b * KS + ks) * 4096 + wave * 1024,
-                  (r < a.R && tile0 + cc < a.N) ? (r * a.N + cc) * 2 : kOutside, 0);
+          for (int ks = 0; ks < KS; ++ks) {
+            if constexpr (!TRANS) {
+              const uint32_t k = ks * 32 + 8 * g;
+              ef[b][ks] = buffer_load16(
+                  eb + (uint64_t)col0 * a.R * 2, eb != 0ull ? kBufferEnd : 0u,
+                  (k < a.R && col0 + c < a.N) ? (c * a.R + k) * 2 : kBufferEnd);
+            } else {
+              const uint32_t r = ks * 32 + wave * 8 + (lane >> 3);
+              const uint32_t h = ((r >> 1) & 1) | ((r >> 3) & 1) << 1;
+              const uint32_t cc = (((lane & 7) >> 1 ^ h) * 2 + (lane & 1)) * 8;
+              const rsrc_t re = buffer(eb + (uint64_t)tile0 * 2,
+                                       eb != 0ull ? ((uint64_t)a.R * a.N - tile0) * 2 : 0u);
+              dma16(re, lds0 + (b * KS + ks) * 4096 + wave * 1024,
+                    (r < a.R && tile0 + cc < a.N) ? (r * a.N + cc) * 2 : kOutside, 0);
+            }
           }
         }
       }
@@ -830,34 +889,41 @@ __device__ __forceinline__ void finish_item(const FinishArgs& a, uint32_t item,
         wait_vm<0>();
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        const int h = ((c >> 3) & 1) | (g & 1) << 1;
+      }
 #pragma unroll
-        for (int b = 0; b < SB; ++b)
+      for (int b = 0; b < SB; ++b) {
+        if (of[b] < 0) continue;
+        if constexpr (TRANS) {
+          const int h = ((c >> 3) & 1) | (g & 1) << 1;
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks)
             ef[b][ks] = lds_tr16(lds_at(lds0 + (b * KS + ks) * 4096 + (8 * g + (c >> 2)) * 128 +
                                         (wave ^ h) * 32 + (c & 3) * 8),
                                  4 * 128);
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi) {
+          floatx4 t = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            t = mfma_bf16_16x16x32(ef[b][ks], lo[mi][ks], t);
+            t = mfma_bf16_16x16x32(ef[b][ks], hi[mi][ks], t);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[mi][i] += key[mi] == of[b] ? t[i] : 0.f;
+        }
+      }
+      if constexpr (TRANS) {
         __builtin_amdgcn_s_barrier();  // everyone has read: the next slots may come
         asm volatile("" ::: "memory");
       }
-#pragma unroll
-      for (int b = 0; b < SB; ++b) {
-        floatx4 t = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          t = mfma_bf16_16x16x32(ef[b][ks], lo[ks], t);
-          t = mfma_bf16_16x16x32(ef[b][ks], hi[ks], t);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] += key == s[b] ? t[i] : 0.f;
-      }
     }
   }
-  if (pos < a.n && in_col)
-    *gp<uint2v>(a.out_ + ((size_t)row * a.os + col) * 2) =
-        uint2v{pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3])};
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi)
+    if (pos0 + mi * 16 + c < a.n && in_col)
+      *gp<uint2v>(a.out_ + ((size_t)row[mi] * a.os + col) * 2) =
+          uint2v{pack_bf16x2(acc[mi][0], acc[mi][1]), pack_bf16x2(acc[mi][2], acc[mi][3])};
 }
 
 // Work on a product that no other work of the call waits for goes out together:
@@ -1378,12 +1444,12 @@ __global__ void __launch_bounds__(256) end_kernel(WgradArgs da, WgradArgs db, Fi
   constexpr int KS = RT < 2 ? 1 : RT / 2;
   if (blockIdx.x < ia) wgrad_item<RT, false>(da, blockIdx.x, sm);
   else if (blockIdx.x < ia + ib) wgrad_item<RT, true>(db, blockIdx.x - ia, sm);
-  else finish_item<KS, true>(fin, blockIdx.x - ia - ib, sm.stage[0]);
+  else finish_item<KS, kFinishRows / 16, true>(fin, blockIdx.x - ia - ib, sm.stage[0]);
 }
 
-template <int KS>
+template <int KS, int MI>
 __global__ void __launch_bounds__(256) finish_kernel(FinishArgs a) {
-  finish_item<KS, false>(a, blockIdx.x, nullptr);
+  finish_item<KS, MI, false>(a, blockIdx.x, nullptr);
 }
 
 // ------------------------------------------------------------------- host ----
@@ -1399,7 +1465,9 @@ static LowPlan low_plan(uint32_t n, uint32_t K, uint32_t R) {
   LowPlan p;
   // longer chunks once they make some 512 items: fewer sums to write and add
   const uint64_t items = (uint64_t)div_ceil(n, kLowRows) * div_ceil(K, kLowChunk);
-  p.kc = kLowChunk * (items < 1024 ? 1u : items >= 512 * 16 ? 16u : (uint32_t)(items / 512));
+  // (and half as long for one tile of rows, whose call waits for little else)
+  p.kc = n <= kLowRows ? kLowChunk / 2
+         : kLowChunk * (items < 1024 ? 1u : items >= 512 * 16 ? 16u : (uint32_t)(items / 512));
   p.nch = div_ceil(K, p.kc);
   p.low = round16((size_t)n * R * 4);
   p.partial = round16((size_t)p.nch * n * R * 4);
@@ -1427,9 +1495,11 @@ static TilePlan tile_plan(uint32_t n, uint32_t K, uint32_t N) {
   p.bn = n <= 128 ? 64 : 128;
   p.tiles_m = div_ceil(n, p.bm);
   p.tiles_n = div_ceil(N, p.bn);
-  // two blocks a CU, of at least four steps each
+  // One block a CU, or two where one would leave CUs idle; of at least four
+  // steps each.  (us, splits for 256 blocks against 512: 64 rows 16.1 against
+  // 20.5, 1237 ragged rows 35.8 against 44.3; 192 tiles whole 91, halved 80.)
   const uint32_t tiles = p.tiles_m * p.tiles_n, steps = div_ceil(K, 64);
-  uint32_t s = tiles >= 512 ? 1 : 512 / tiles;
+  uint32_t s = tiles <= 128 ? 256 / tiles : tiles <= 256 ? 2 : 1;
   if (s > steps / 4) s = steps / 4;
   if (s > 16) s = 16;
   if (s < 1) s = 1;
@@ -1489,6 +1559,7 @@ static LowArgs low_args(const rld_route* r, bool trans, const void* x, uint32_t 
   if (a.nz > r->max_loras) a.nz = r->max_loras;
   if (a.nz > n) a.nz = n;
   if (a.nz > kLowRows) a.nz = kLowRows;
+  if (order && a.nz > 2) a.nz = 2;  // sorted rows: few slots a tile
   return a;
 }
 
@@ -1557,6 +1628,15 @@ static FinishArgs finish_args(const rld_route* r, bool trans, const TilePlan& p,
   a.tiles = div_ceil(a.N, 64);
   a.low_sorted = low_sorted ? 1u : 0u;
   return a;
+}
+
+template <int MI>
+static int launch_finish(const FinishArgs& f, uint32_t rows, hipStream_t st) {
+  const uint32_t grid = f.tiles * div_ceil(f.n, rows);
+  if (f.R <= 32) finish_kernel<1, MI><<<grid, 256, 0, st>>>(f);
+  else if (f.R <= 64) finish_kernel<2, MI><<<grid, 256, 0, st>>>(f);
+  else finish_kernel<4, MI><<<grid, 256, 0, st>>>(f);
+  return launch_status();
 }
 
 template <bool TRANS>
@@ -1683,11 +1763,9 @@ extern "C" int rld_proj(const rld_route* route, const void* w, uint32_t w_row_st
   const FinishArgs f =
       finish_args(route, false, t, sums, sorted ? sort.order_ : 0, sorted ? sort.skey_ : seq,
                   sum ? parts : 0, partial, p.nch, first, out, out_row_stride, n);
-  const uint32_t grid = f.tiles * div_ceil(n, 16);
-  if (R <= 32) finish_kernel<1><<<grid, 256, 0, st>>>(f);
-  else if (R <= 64) finish_kernel<2><<<grid, 256, 0, st>>>(f);
-  else finish_kernel<4><<<grid, 256, 0, st>>>(f);
-  return launch_status();
+  // 64 positions a block where the low rows are summed already (adding up their
+  // chunks takes longer for more rows a wave: 17 us against 10 for 1237 rows)
+  return sum ? launch_finish<4>(f, 64, st) : launch_finish<1>(f, 16, st);
 }
 
 extern "C" size_t rld_proj_grad_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t n_out,
@@ -1808,7 +1886,7 @@ extern "C" int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_r
   const uint32_t ib = db_table ? b.tiles * route->max_loras : 0u;
   const FinishArgs f = finish_args(route, true, t, sums, sort.order_, sort.skey_, gparts, 0, 0, true, dx,
                                    dx_row_stride, n);
-  const uint32_t grid = ia + ib + (part ? f.tiles * div_ceil(n, 16) : 0u);
+  const uint32_t grid = ia + ib + (part ? f.tiles * div_ceil(n, kFinishRows) : 0u);
   if (grid == 0) return RLD_OK;
   if (R <= 16) end_kernel<1><<<grid, 256, 0, st>>>(a, b, f, ia, ib);
   else if (R <= 32) end_kernel<2><<<grid, 256, 0, st>>>(a, b, f, ia, ib);

@@ -130,21 +130,32 @@ __device__ __forceinline__ void sort_item(const SortArgs& a, uint32_t item, uint
   const bool active =
       !base && gp<const uint64_t>(a.atab_)[s] != 0ull && gp<const uint64_t>(a.btab_)[s] != 0ull;
   int key[16];
-  uint32_t below = 0, first;
+  uint32_t below = 0, own = 0, first, cnt = 0;
   for (uint32_t b0 = 0; b0 < a.n; b0 += kSortBatch) {
     sort_keys(a, b0 + threadIdx.x * 16, key);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) below += key[e] < s;
+    for (int e = 0; e < 16; ++e) {
+      below += key[e] < s;
+      own += key[e] == s;
+    }
   }
-  block_prefix(below, wsum, first);
-  uint32_t cnt = 0;
+  // one batch: both sums, of at most 2^12, in one pass of a word
+  const bool one = a.n <= kSortBatch;
+  uint32_t before = block_prefix(one ? below << 16 | own : below, wsum, first);
+  const uint32_t both = first;
+  if (one) first >>= 16;
   for (uint32_t b0 = 0; b0 < a.n; b0 += kSortBatch) {
     const uint32_t r0 = b0 + threadIdx.x * 16;
-    if (a.n > kSortBatch) sort_keys(a, r0, key);
-    uint32_t own = 0, tot;
+    uint32_t tot = both & 0xffffu;
+    before &= 0xffffu;
+    if (!one) {
+      sort_keys(a, r0, key);
+      own = 0;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) own += key[e] == s;
-    uint32_t at = first + cnt + block_prefix(own, wsum, tot);
+      for (int e = 0; e < 16; ++e) own += key[e] == s;
+      before = block_prefix(own, wsum, tot);
+    }
+    uint32_t at = first + cnt + before;
 #pragma unroll
     for (int e = 0; e < 16; ++e)
       if (key[e] == s) {
@@ -275,26 +286,30 @@ struct LowArgs {
   uint64_t x_, mtab_, otab_, stab_, partial_;
   uint64_t order_;  // sorted positions' rows, or 0: positions are rows
   uint64_t key_;    // slots by position
-  uint64_t low_;    // fp32 [n][R], or 0: not wanted
-  uint64_t parts_;  // bf16 [n][2][R]: the value's two parts, or 0
-  uint64_t low_at_, parts_at_;  // where a position goes in either, or 0: the same
-  uint32_t xs, n, max_loras, K, R, kc, nch, nz, tiles;
+  // the values' bf16 parts, [n][np][R]: up to two copies (0: not wanted), and
+  // where a position goes in either (0: the same place)
+  uint64_t parts_[2], at_[2];
+  uint32_t xs, n, max_loras, K, R, np, kc, nch, nz, tiles;
 };
 
 // Four columns of a low row, scaled, to where they are wanted.
 __device__ __forceinline__ void store_low(const LowArgs& a, uint32_t from, uint32_t col,
-                                          const floatx4& v) {
-  uint32_t pos = a.low_at_ ? (uint32_t)gp<const int32_t>(a.low_at_)[from] : from;
-  if (a.low_) *gp<floatx4>(a.low_ + ((size_t)pos * a.R + col) * 4) = v;
-  if (a.parts_) {
-    pos = a.parts_at_ ? (uint32_t)gp<const int32_t>(a.parts_at_)[from] : from;
-    const uint2v hi = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-    const uint2v lo = {
-        pack_bf16x2(v[0] - bf16_to_f32(hi.x & 0xffffu), v[1] - bf16_to_f32(hi.x >> 16)),
-        pack_bf16x2(v[2] - bf16_to_f32(hi.y & 0xffffu), v[3] - bf16_to_f32(hi.y >> 16))};
-    RLD_GLOBAL uint16_t* p = gp<uint16_t>(a.parts_) + (size_t)pos * 2 * a.R + col;
-    *reinterpret_cast<RLD_GLOBAL uint2v*>(p) = hi;
-    *reinterpret_cast<RLD_GLOBAL uint2v*>(p + a.R) = lo;
+                                          floatx4 v) {
+  uint2v part[3];
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    part[p] = uint2v{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    v -= floatx4{bf16_to_f32(part[p].x & 0xffffu), bf16_to_f32(part[p].x >> 16),
+                 bf16_to_f32(part[p].y & 0xffffu), bf16_to_f32(part[p].y >> 16)};
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (!a.parts_[i]) continue;
+    const uint32_t pos = a.at_[i] ? (uint32_t)gp<const int32_t>(a.at_[i])[from] : from;
+    RLD_GLOBAL uint16_t* q = gp<uint16_t>(a.parts_[i]) + (size_t)pos * a.np * a.R + col;
+    *reinterpret_cast<RLD_GLOBAL uint2v*>(q) = part[0];
+    *reinterpret_cast<RLD_GLOBAL uint2v*>(q + a.R) = part[1];
+    if (a.np > 2) *reinterpret_cast<RLD_GLOBAL uint2v*>(q + 2 * a.R) = part[2];
   }
 }
 
@@ -515,7 +530,7 @@ struct TileArgs {
   uint64_t order_;  // sorted positions' rows, or 0: rows in their own order, their
                     // offsets taken from a tile's first row
   uint64_t skey_;   // slots by position
-  uint32_t xs, ws, os, n, K, N, R, tiles_m, tiles_n;
+  uint32_t xs, ws, os, n, K, N, R, np, tiles_m, tiles_n;
 };
 
 // The row at position p, less the row that offsets are taken from.
@@ -749,10 +764,10 @@ struct FinishArgs {
   uint64_t order_;         // sorted positions' rows, or 0: positions are rows
   uint64_t key_;           // slots by position (raw ids if order_ is 0)
   uint64_t etab_, otab_, stab_;
-  uint64_t parts_;         // bf16 [n][2][R], or 0: from
+  uint64_t parts_;         // bf16 [n][np][R], or 0: from
   uint64_t partial_;       // fp32 [nch][n][R]; by row, or by position with low_sorted
   uint32_t os, n, N, R, splits, nch, max_loras, tiles;  // tiles: of 64 columns
-  uint32_t low_sorted;
+  uint32_t low_sorted, np;
 };
 
 // 16 * MI positions x 64 columns, 16 columns a wave: the splits of the product,
@@ -829,7 +844,7 @@ __device__ __forceinline__ void finish_item(const FinishArgs& a, uint32_t item,
         hi[mi][ks] = lo[mi][ks] = zero16();
         if (key[mi] >= 0 && k < a.R) {
           if (a.parts_) {
-            const RLD_GLOBAL uint16_t* p = gp<const uint16_t>(a.parts_) + (size_t)at * 2 * a.R + k;
+            const RLD_GLOBAL uint16_t* p = gp<const uint16_t>(a.parts_) + (size_t)at * a.np * a.R + k;
             hi[mi][ks] = load16(p);
             lo[mi][ks] = load16(p + a.R);
           } else {
@@ -1054,14 +1069,15 @@ __device__ __forceinline__ void big_tile_body(const TileArgs& a) {
   };
   // Low operands, 64 of rank from k0: half h of the rows' part `lo` (0 or 1) into
   // the X places, half h of a slot's second matrix into the W places.
-  const rsrc_t rlow = buffer(a.parts_ + (uint64_t)row0 * a.R * 4, (uint64_t)rows * a.R * 4);
+  const uint32_t lrow = a.np * a.R * 2;  // bytes of a row's parts
+  const rsrc_t rlow = buffer(a.parts_ + (uint64_t)row0 * lrow, (uint64_t)rows * lrow);
   auto load_low = [&](int h, int lo, uint32_t k0, int buf) {
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       const uint32_t r = (wave * 2 + p) * 8 + (lane >> 3);
       const uint32_t k = k0 + ((lane & 7) ^ ((r >> 1) & 7)) * 8;
       dma16(rlow, put + buf * 65536 + h * 16384 + p * 1024,
-            k < a.R ? ((h * 128 + r) * 2 + lo) * a.R * 2 + k * 2 : kOutside, 0);
+            k < a.R ? (h * 128 + r) * lrow + (lo * a.R + k) * 2 : kOutside, 0);
     }
   };
   auto load_e = [&](int h, uint64_t e, uint32_t k0, int buf) {
@@ -1335,104 +1351,147 @@ __global__ void __launch_bounds__(512) big_tile_kernel(TileArgs a) {
 // ------------------------------------------------------------------ wgrad ----
 
 struct WgradArgs {
-  uint64_t v_, low_, order_, span_, dtab_;
+  uint64_t v_, parts_, order_, span_, dtab_;  // parts_: bf16 [n][3][R] by position
   uint32_t vs, width, R, tiles, accumulate;
 };
 
-struct WgradSmem {
-  __attribute__((aligned(1024))) unsigned char stage[4][4096];
-  floatx4 red[4][4][kWave];
+// The shape of a block for ranks up to 16 * RT: 128 columns of the wide operand,
+// its waves over the ranks (WR) and the columns.  A stage holds 64 positions of
+// both operands.
+template <int RT>
+struct WgradShape {
+  static constexpr int RP = 16 * RT;              // ranks of a row in LDS
+  static constexpr int WR = RT >= 4 ? 2 : 1, WC = 4 / WR;
+  static constexpr int MT = RT / WR, NT = 8 / WC;  // 16 x 16 blocks of a wave
+  static constexpr int kWide = 64 * 256, kLow = 64 * RP * 2;
+  static constexpr int kStage = kWide + 3 * kLow;
+  static constexpr int kLds = 2 * kStage;          // 80 KB at rank 64: two blocks a CU
 };
-static_assert(sizeof(WgradSmem) >= 32768, "finish_item uses as much");
 
-// Slot s, 64 columns of the wide operand (x for dA, dy for dB): the sum over
-// the slot's positions of low[pos][r] * wide[row][col].  Each of four waves
-// takes every fourth 32-position group, staged in LDS of its own (no barrier
-// in the loop) and read transposed; the waves' sums meet in LDS at the end.
-// DB: the result is [col][R] instead of [R][col].
+// Slot s, 128 columns of the wide operand (x for dA, dy for dB): the sum over
+// the slot's positions of low[pos][r] * wide[row][col], 64 positions a step,
+// two steps in LDS.  Both operands lie by position, as their rows do in memory,
+// and are read transposed.  The low values come in three bf16 parts, which
+// hold all 24 bits.  DB: the result is [col][R] instead of [R][col].
 template <int RT, bool DB>
-__device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, WgradSmem& sm) {
-  auto& stage = sm.stage;
-  auto& red = sm.red;
+__device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, unsigned char* lds) {
+  using S = WgradShape<RT>;
+  constexpr int kPairs = S::RP / 16;
+  constexpr int LL = S::kLow / 1024, LP = (3 * LL + 3) / 4;  // 1 KB loads of a part; a wave's
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, c = lane & 15;
+  const int wr = wave / S::WC, wc = wave % S::WC;
   const int s = item / a.tiles;
-  const uint32_t col0 = item % a.tiles * 64;
+  const uint32_t col0 = item % a.tiles * 128;
   const uint64_t dst = gp<const uint64_t>(a.dtab_)[s];
   if (dst == 0ull) return;
   const uint32_t begin = gp<const uint32_t>(a.span_)[2 * s];
   const uint32_t cnt = gp<const uint32_t>(a.span_)[2 * s + 1];
   const RLD_GLOBAL int32_t* order = gp<const int32_t>(a.order_) + begin;
-  const RLD_GLOBAL float* low = gp<const float>(a.low_) + (size_t)begin * a.R;
+  const uint64_t zeros = (uint64_t)&g_zero16[0];
+  const uint32_t lds0 = lds_addr(lds);
+  const uint32_t lrow = 3 * a.R * 2;
+  const uint64_t parts = uniform64(a.parts_ + (uint64_t)begin * lrow);
 
-  floatx4 acc[RT][4];
+  // this lane's rows (four of a step) and column of the wide operand
+  uint32_t rw[4];
+  uint64_t vcol[4];
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
+  for (int p = 0; p < 4; ++p) {
+    rw[p] = (wave * 4 + p) * 4 + (lane >> 4);
+    const uint32_t h = ((rw[p] & 3) | ((rw[p] >> 3) & 3) << 2) & 7;
+    const uint32_t slot = lane & 15;
+    const uint32_t col = col0 + (((slot >> 1) ^ h) * 2 + (slot & 1)) * 8;
+    vcol[p] = col < a.width ? a.v_ + (uint64_t)col * 2 : 0ull;
+  }
+  // and of the low parts: load j is load wave + 4 j of the 3 * LL
+  uint32_t vl[LP];
 #pragma unroll
-    for (int ni = 0; ni < 4; ++ni) acc[rt][ni] = floatx4{0.f, 0.f, 0.f, 0.f};
-
-  for (uint32_t i0 = wave * 32; i0 < cnt; i0 += 128) {
+  for (int j = 0; j < LP; ++j) {
+    const int i = min(wave + 4 * j, 3 * LL - 1);
+    constexpr int CPR = S::RP / 8;  // chunks of a row
+    const uint32_t k = (i % LL) * (64 / CPR) + lane / CPR;
+    const uint32_t slot = lane % CPR;
+    const uint32_t h = ((k & 3) | ((k >> 3) & 3) << 2) & (kPairs - 1);
+    const uint32_t r = (((slot >> 1) ^ h) * 2 + (slot & 1)) * 8;
+    vl[j] = r < a.R ? k * lrow + ((i / LL) * a.R + r) * 2 : kOutside;
+  }
+  uint32_t row[4];
+  auto rows_of = [&](uint32_t i0) {
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      const uint32_t k = p * 8 + (lane >> 3);
-      const uint32_t h = ((k >> 1) & 1) | ((k >> 3) & 1) << 1;
-      const uint32_t col = col0 + ((((lane & 7) >> 1) ^ h) * 2 + (lane & 1)) * 8;
-      const bool in = i0 + k < cnt && col < a.width;
-      const uint64_t src =
-          a.v_ + ((uint64_t)(in ? order[i0 + k] : 0) * a.vs + (in ? col : 0)) * 2;
-      __builtin_amdgcn_global_load_lds((const void*)(in ? src : (uint64_t)&g_zero16[0]),
-                                       (RLD_LDS void*)(&stage[wave][p * 1024]), 16, 0, 0);
+      const uint32_t i = i0 + rw[p];
+      row[p] = i < cnt ? (uint32_t)order[i] : 0xffffffffu;
     }
-    uint4 lf[RT][3];
+  };
+  auto issue = [&](uint32_t i0) {  // row: of these positions
+    const uint32_t st = lds0 + (i0 / 64 & 1) * S::kStage;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const uint32_t r = rt * 16 + c;
-      float v[8];
+    for (int p = 0; p < 4; ++p)
+      dma16((row[p] != 0xffffffffu && vcol[p]) ? vcol[p] + (uint64_t)row[p] * a.vs * 2 : zeros,
+            st + (wave * 4 + p) * 1024);
+    const rsrc_t rl = buffer(parts + (uint64_t)i0 * lrow,
+                             i0 < cnt ? (uint64_t)min(cnt - i0, 64u) * lrow : 0);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t i = i0 + 8 * g + e;
-        v[e] = (i < cnt && r < a.R) ? low[(size_t)i * a.R + r] : 0.f;
-      }
-      bf16_parts<3>(v, lf[rt]);
-    }
+    for (int j = 0; j < LP; ++j)
+      dma16(rl, st + S::kWide + min(wave + 4 * j, 3 * LL - 1) * 1024, vl[j], 0);
+  };
+
+  floatx4 acc[S::MT][S::NT];
+#pragma unroll
+  for (int mt = 0; mt < S::MT; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < S::NT; ++nt) acc[mt][nt] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+  rows_of(0);
+  issue(0);
+  rows_of(64);
+  for (uint32_t i0 = 0; i0 < cnt; i0 += 64) {
     wait_vm<0>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    issue(i0 + 64);
+    rows_of(i0 + 128);
+    const uint32_t st = lds0 + (i0 / 64 & 1) * S::kStage;
 #pragma unroll
-    for (int ni = 0; ni < 4; ++ni) {
-      const int h = ((c >> 3) & 1) | (g & 1) << 1;
-      unsigned char* p =
-          &stage[wave][(8 * g + (c >> 2)) * 128 + (ni ^ h) * 32 + (c & 3) * 8];
-      // rows 4 further on: (k >> 1) & 1 and (k >> 3) & 1 are the same
-      const uint4 vf = lds_tr16((RLD_LDS unsigned char*)p, 4 * 128);
+    for (int ks = 0; ks < 2; ++ks) {
+      const uint32_t k = ks * 32 + 8 * g + (c >> 2);
+      const int h = (c >> 2) | g << 2;
+      uint4 vf[S::NT];
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
+      for (int nt = 0; nt < S::NT; ++nt)
+        vf[nt] = lds_tr16(
+            lds_at(st + k * 256 + ((wc * S::NT + nt) ^ (h & 7)) * 32 + (c & 3) * 8), 4 * 256);
 #pragma unroll
-        for (int p3 = 2; p3 >= 0; --p3)
-          acc[rt][ni] = DB ? mfma_bf16_16x16x32(lf[rt][p3], vf, acc[rt][ni])
-                           : mfma_bf16_16x16x32(vf, lf[rt][p3], acc[rt][ni]);
+      for (int p = 2; p >= 0; --p)
+#pragma unroll
+        for (int mt = 0; mt < S::MT; ++mt) {
+          const uint4 lf = lds_tr16(
+              lds_at(st + S::kWide + p * S::kLow + k * (S::RP * 2) +
+                     ((wr * S::MT + mt) ^ (h & (kPairs - 1))) * 32 + (c & 3) * 8),
+              4 * S::RP * 2);
+#pragma unroll
+          for (int nt = 0; nt < S::NT; ++nt)
+            acc[mt][nt] = DB ? mfma_bf16_16x16x32(lf, vf[nt], acc[mt][nt])
+                             : mfma_bf16_16x16x32(vf[nt], lf, acc[mt][nt]);
+        }
     }
-    // the next group's loads overwrite what the reads above still fetch
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
+  wait_vm<0>();  // the loads past the end, of zeros
 
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    __syncthreads();
+  for (int mt = 0; mt < S::MT; ++mt)
 #pragma unroll
-    for (int ni = 0; ni < 4; ++ni) red[wave][ni][lane] = acc[rt][ni];
-    __syncthreads();
-    floatx4 sum = red[0][wave][lane];
-#pragma unroll
-    for (int v = 1; v < 4; ++v) sum += red[v][wave][lane];
-    // first operand: index 4g + i, four consecutive per lane; second: index c
-    const uint32_t col = col0 + wave * 16 + (DB ? c : 4 * g);
-    const uint32_t r = rt * 16 + (DB ? 4 * g : c);
-    if (col < a.width && r < a.R) {
-      const uint64_t at = DB ? (uint64_t)col * a.R + r : (uint64_t)r * a.width + col;
-      RLD_GLOBAL floatx4* p = gp<floatx4>(dst + at * 4);
-      *p = a.accumulate ? *p + sum : sum;
+    for (int nt = 0; nt < S::NT; ++nt) {
+      // first operand: index 4g + i, four consecutive per lane; second: index c
+      const uint32_t col = col0 + (wc * S::NT + nt) * 16 + (DB ? c : 4 * g);
+      const uint32_t rank = (wr * S::MT + mt) * 16 + (DB ? 4 * g : c);
+      if (col >= a.width || rank >= a.R) continue;
+      const uint64_t at = DB ? (uint64_t)col * a.R + rank : (uint64_t)rank * a.width + col;
+      RLD_GLOBAL floatx4* o = gp<floatx4>(dst + at * 4);
+      *o = a.accumulate ? *o + acc[mt][nt] : acc[mt][nt];
     }
-  }
 }
 
 // dA, dB and, behind them, the last part of dx in one launch: the first `ia`
@@ -1440,11 +1499,12 @@ __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, Wg
 template <int RT>
 __global__ void __launch_bounds__(256) end_kernel(WgradArgs da, WgradArgs db, FinishArgs fin,
                                                   uint32_t ia, uint32_t ib) {
-  __shared__ WgradSmem sm;
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[WgradShape<RT>::kLds];
+  static_assert(sizeof(lds) >= 32768, "finish_item uses as much");
   constexpr int KS = RT < 2 ? 1 : RT / 2;
-  if (blockIdx.x < ia) wgrad_item<RT, false>(da, blockIdx.x, sm);
-  else if (blockIdx.x < ia + ib) wgrad_item<RT, true>(db, blockIdx.x - ia, sm);
-  else finish_item<KS, kFinishRows / 16, true>(fin, blockIdx.x - ia - ib, sm.stage[0]);
+  if (blockIdx.x < ia) wgrad_item<RT, false>(da, blockIdx.x, lds);
+  else if (blockIdx.x < ia + ib) wgrad_item<RT, true>(db, blockIdx.x - ia, lds);
+  else finish_item<KS, kFinishRows / 16, true>(fin, blockIdx.x - ia - ib, lds);
 }
 
 template <int KS, int MI>
@@ -1461,15 +1521,16 @@ struct LowPlan {
   size_t low, partial;  // bytes
 };
 
-static LowPlan low_plan(uint32_t n, uint32_t K, uint32_t R) {
+static LowPlan low_plan(uint32_t n, uint32_t K, uint32_t R, uint32_t np) {
   LowPlan p;
-  // longer chunks once they make some 512 items: fewer sums to write and add
+  // Longer chunks once they make some 256 items: each loads its slots' tables and
+  // starts its pipeline anew (4096 rows, K 4096: 13.6 us against 17.8 with 512
+  // items).  Half as long for one tile of rows, whose call waits for little else.
   const uint64_t items = (uint64_t)div_ceil(n, kLowRows) * div_ceil(K, kLowChunk);
-  // (and half as long for one tile of rows, whose call waits for little else)
   p.kc = n <= kLowRows ? kLowChunk / 2
-         : kLowChunk * (items < 1024 ? 1u : items >= 512 * 16 ? 16u : (uint32_t)(items / 512));
+         : kLowChunk * (items < 512 ? 1u : items >= 256 * 16 ? 16u : (uint32_t)(items / 256));
   p.nch = div_ceil(K, p.kc);
-  p.low = round16((size_t)n * R * 4);
+  p.low = round16((size_t)n * R * np * 2);
   p.partial = round16((size_t)p.nch * n * R * 4);
   return p;
 }
@@ -1531,7 +1592,7 @@ static SortArgs sort_args(const rld_route* r, const int32_t* seq, uint32_t n,
 
 // order 0: low rows by row, key slots by row.
 static LowArgs low_args(const rld_route* r, bool trans, const void* x, uint32_t xs, uint32_t n,
-                        uint64_t order, uint64_t key, uint64_t low, uint64_t parts,
+                        uint64_t order, uint64_t key, uint32_t np, uint64_t parts,
                         uint64_t partial) {
   LowArgs a;
   a.x_ = (uint64_t)x;
@@ -1541,17 +1602,17 @@ static LowArgs low_args(const rld_route* r, bool trans, const void* x, uint32_t 
   a.partial_ = partial;
   a.order_ = order;
   a.key_ = key;
-  a.low_ = low;
-  a.parts_ = parts;
+  a.np = np;
+  a.parts_[0] = parts;
+  a.parts_[1] = a.at_[0] = a.at_[1] = 0;
   a.xs = xs;
   a.n = n;
   a.max_loras = r->max_loras;
   a.K = trans ? r->n_out : r->k_in;
   a.R = r->max_rank;
-  const LowPlan p = low_plan(n, a.K, a.R);
+  const LowPlan p = low_plan(n, a.K, a.R, np);
   a.kc = p.kc;
   a.nch = p.nch;
-  a.low_at_ = a.parts_at_ = 0;
   a.tiles = div_ceil(n, kLowRows);
   // few items: the slots of a tile go to several blocks
   const uint32_t items = a.tiles * a.nch;
@@ -1627,6 +1688,7 @@ static FinishArgs finish_args(const rld_route* r, bool trans, const TilePlan& p,
   a.max_loras = r->max_loras;
   a.tiles = div_ceil(a.N, 64);
   a.low_sorted = low_sorted ? 1u : 0u;
+  a.np = trans ? 3 : 2;
   return a;
 }
 
@@ -1658,6 +1720,7 @@ static int launch_big(const rld_route* r, const TilePlan& p, const void* w, uint
   a.K = TRANS ? r->n_out : r->k_in;
   a.N = TRANS ? r->k_in : r->n_out;
   a.R = r->max_rank;
+  a.np = TRANS ? 3 : 2;
   a.tiles_m = p.tiles_m;
   a.tiles_n = p.tiles_n;
   big_tile_kernel<TRANS><<<xcd_grid(a.tiles_m * a.tiles_n), 512, 0, st>>>(a);
@@ -1686,7 +1749,7 @@ using namespace rld;
 extern "C" size_t rld_proj_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t n_out,
                                            uint32_t max_rank, uint32_t max_loras) {
   if (n == 0 || k_in == 0 || n_out == 0 || max_rank == 0 || max_loras == 0) return 0;
-  const LowPlan p = low_plan(n, k_in, max_rank);
+  const LowPlan p = low_plan(n, k_in, max_rank, 2);
   return sort_bytes(n, max_loras) + p.low + p.partial + tile_plan(n, k_in, n_out).sums;
 }
 
@@ -1709,7 +1772,7 @@ extern "C" int rld_proj(const rld_route* route, const void* w, uint32_t w_row_st
   const uint32_t K = route->k_in, N = route->n_out, R = route->max_rank;
   if (workspace_bytes < rld_proj_workspace_bytes(n, K, N, R, route->max_loras))
     return RLD_ENOSPACE;
-  const LowPlan p = low_plan(n, K, R);
+  const LowPlan p = low_plan(n, K, R, 2);
   const TilePlan t = tile_plan(n, K, N);
   const uint64_t parts = (uint64_t)workspace + sort_bytes(n, route->max_loras);
   const uint64_t partial = parts + p.low;
@@ -1723,7 +1786,7 @@ extern "C" int rld_proj(const rld_route* route, const void* w, uint32_t w_row_st
     if ((e = launch_status())) return e;
     const bool keep = too_far(n, x_row_stride) || too_far(n, out_row_stride);
     const uint64_t order = keep ? 0 : sort.order_, key = keep ? sort.rkey_ : sort.skey_;
-    const LowArgs l = low_args(route, false, x, x_row_stride, n, order, key, 0, parts,
+    const LowArgs l = low_args(route, false, x, x_row_stride, n, order, key, 2, parts,
                                p.nch == 1 ? 0 : partial);
     low_kernel<<<low_items(l), 256, 0, st>>>(l);
     if ((e = launch_status())) return e;
@@ -1745,7 +1808,7 @@ extern "C" int rld_proj(const rld_route* route, const void* w, uint32_t w_row_st
   const uint64_t again = (uint64_t)div_ceil(N, 64) * n * R * 4 * p.nch;
   const bool sum = again > (32ull << 20);
   const LowArgs l = low_args(route, false, x, x_row_stride, n, first ? sort.order_ : 0,
-                             first ? sort.skey_ : seq, 0, parts, partial);
+                             first ? sort.skey_ : seq, 2, parts, partial);
   StartArgs s;
   s.part = part_args<false>(t, w, w_row_stride, x, x_row_stride, n, K, N, sums);
   s.u = l;
@@ -1771,7 +1834,7 @@ extern "C" int rld_proj(const rld_route* route, const void* w, uint32_t w_row_st
 extern "C" size_t rld_proj_grad_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t n_out,
                                                 uint32_t max_rank, uint32_t max_loras) {
   if (k_in == 0 || n_out == 0 || max_rank == 0 || max_loras == 0) return 0;
-  const LowPlan u = low_plan(n, k_in, max_rank), g = low_plan(n, n_out, max_rank);
+  const LowPlan u = low_plan(n, k_in, max_rank, 3), g = low_plan(n, n_out, max_rank, 3);
   return sort_bytes(n, max_loras) + u.low + u.partial + 2 * g.low + g.partial +
          (n ? tile_plan(n, n_out, k_in).sums : 0);
 }
@@ -1808,12 +1871,12 @@ extern "C" int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_r
   if (workspace_bytes < rld_proj_grad_workspace_bytes(n, K, N, R, route->max_loras))
     return RLD_ENOSPACE;
   if (n == 0 && !adapters) return RLD_OK;
-  const LowPlan pu = low_plan(n, K, R), pg = low_plan(n, N, R);
-  const uint64_t ul = (uint64_t)workspace + sort_bytes(n, route->max_loras);
-  const uint64_t usum = ul + pu.low;
-  const uint64_t gl = usum + pu.partial;
-  const uint64_t gparts = gl + pg.low;
-  const uint64_t gsum = gparts + pg.low;
+  const LowPlan pu = low_plan(n, K, R, 3), pg = low_plan(n, N, R, 3);
+  const uint64_t uparts = (uint64_t)workspace + sort_bytes(n, route->max_loras);
+  const uint64_t usum = uparts + pu.low;
+  const uint64_t gparts = usum + pu.partial;  // by position
+  const uint64_t grows = gparts + pg.low;     // by row, for rows in their own order
+  const uint64_t gsum = grows + pg.low;
   const uint64_t sums = gsum + pg.partial;
   const hipStream_t st = (hipStream_t)stream;
   const SortArgs sort = sort_args(route, seq_slot, n, (uint64_t)workspace);
@@ -1829,13 +1892,11 @@ extern "C" int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_r
   const bool by_pos = first && !keep;
   const uint64_t order = by_pos ? sort.order_ : 0;
   const uint64_t key = by_pos ? sort.skey_ : keep ? sort.rkey_ : (uint64_t)seq_slot;
-  // u for dB; g for dx (as parts) and dA
-  LowArgs u = low_args(route, false, x, x_row_stride, n, order, key, ul, 0, usum);
-  LowArgs g = low_args(route, true, dy, dy_row_stride, n, order, key, da_table ? gl : 0,
-                       dx ? gparts : 0, gsum);
-  // dA and dB take them by position; dx too, but for rows in their own order
-  if (!by_pos) u.low_at_ = g.low_at_ = sort.rpos_;
-  if (!by_pos && !keep) g.parts_at_ = sort.rpos_;
+  // u for dB; g for dx and dA: by position, and by row too where dx takes it so
+  LowArgs u = low_args(route, false, x, x_row_stride, n, order, key, 3, uparts, usum);
+  LowArgs g = low_args(route, true, dy, dy_row_stride, n, order, key, 3, gparts, gsum);
+  if (!by_pos) u.at_[0] = g.at_[0] = sort.rpos_;
+  if (keep) g.parts_[1] = grows;
   const uint32_t iu = want_u ? low_items(u) : 0u, ig = want_g ? low_items(g) : 0u;
   if (first) {
     sort_kernel<<<route->max_loras + 1, 256, 0, st>>>(sort);
@@ -1862,16 +1923,16 @@ extern "C" int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_r
     if ((e = launch_status())) return e;
   }
   if (n && dx && t.big &&
-      (e = launch_big<true>(route, t, w, w_row_stride, dy, dy_row_stride, order, key, n, gparts,
-                            dx, dx_row_stride, st)))
+      (e = launch_big<true>(route, t, w, w_row_stride, dy, dy_row_stride, order, key, n,
+                            keep ? grows : gparts, dx, dx_row_stride, st)))
     return e;
   WgradArgs a, b;
   a.v_ = (uint64_t)x;
   b.v_ = (uint64_t)dy;
   a.vs = x_row_stride;
   b.vs = dy_row_stride;
-  a.low_ = gl;
-  b.low_ = ul;
+  a.parts_ = gparts;
+  b.parts_ = uparts;
   a.dtab_ = (uint64_t)da_table;
   b.dtab_ = (uint64_t)db_table;
   a.width = K;
@@ -1880,8 +1941,8 @@ extern "C" int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_r
   a.span_ = b.span_ = sort.span_;
   a.R = b.R = R;
   a.accumulate = b.accumulate = accumulate ? 1u : 0u;
-  a.tiles = div_ceil(a.width, 64);
-  b.tiles = div_ceil(b.width, 64);
+  a.tiles = div_ceil(a.width, 128);
+  b.tiles = div_ceil(b.width, 128);
   const uint32_t ia = da_table ? a.tiles * route->max_loras : 0u;
   const uint32_t ib = db_table ? b.tiles * route->max_loras : 0u;
   const FinishArgs f = finish_args(route, true, t, sums, sort.order_, sort.skey_, gparts, 0, 0, true, dx,

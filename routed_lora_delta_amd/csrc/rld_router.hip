@@ -13,13 +13,14 @@
 // a fixed order (per lane over its tokens, over the lanes and waves of a
 // block, over the blocks), so results do not change from run to run.
 //
-// One launch for up to 128 tokens, two otherwise: route (choices, and per block
-// of 128 tokens the counts and probability sums of every expert) and place
-// (each row's place in the expert-sorted order, from the counts of all
+// One launch for up to 64 tokens, two otherwise: route (choices, and per block
+// of 32 to 128 tokens the counts and probability sums of every expert) and
+// place (each row's place in the expert-sorted order, from the counts of all
 // blocks); past 32 blocks a scan in between turns the counts into prefix
-// sums, so that no place block reads them all.  A block keeps 128 bits per
-// expert of its tokens that chose it: the set bits below a token's own are its
-// rank there, whatever order the lanes arrive in.
+// sums, so that no place block reads them all (8192 tokens in 64 blocks: 23.6 us
+// with the scan, 24.7 without; 32768 in 256: 27.2 and 39.6).  A block keeps 128
+// bits per expert of its tokens that chose it: the set bits below a token's
+// own are its rank there, whatever order the lanes arrive in.
 #include <type_traits>
 
 #include "rld_device.hpp"
@@ -27,9 +28,10 @@
 
 namespace rld {
 
-constexpr uint32_t kRouteTokens = 128;  // tokens of a block
-constexpr uint32_t kRouteThreads = 1024;
-constexpr uint32_t kRouteWaves = kRouteThreads / 64;
+constexpr uint32_t kOneBlock = 64;       // tokens up to which one block does everything
+constexpr uint32_t kRouteTokens = 128;   // tokens of a block, at most
+constexpr uint32_t kPlaceThreads = 1024;
+constexpr uint32_t kPlaceWaves = kPlaceThreads / 64;
 constexpr uint32_t kScanBlocks = 32;    // token blocks above which the scan is worth a launch
 constexpr uint32_t kMaxExperts = 1024;
 constexpr uint32_t kMaxTopK = 32;
@@ -40,7 +42,7 @@ struct RouterArgs {
   uint64_t cnt_, psum_;      // [nblk][E + 1]: counts (after the scan their prefix sums), [nblk][E]:
                              // sums of p
   uint64_t total_, ptotal_;  // [E + 1], [E]: of the scan
-  uint32_t ls, T, E, k, nblk, norm, scanned;
+  uint32_t ls, T, E, k, nblk, tokens, norm, scanned;  // tokens: of a block
 };
 
 // A value of another lane of the row of 16, in the vector pipe.
@@ -49,12 +51,14 @@ __device__ __forceinline__ int dpp(int v) {
   return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, true);
 }
 
-// v combined over the LPT lanes of a group, the same bits in each: exchanges
-// with the lane 1 and 2 away, then mirrored eights and sixteens.
-template <int LPT, class T, class F>
-__device__ __forceinline__ T group_all(T v, F f) {
-  auto at = [](T x, auto ctrl) {
-    constexpr int C = decltype(ctrl)::value;
+// x of the lane that a group's exchange STEP pairs with this one: the lanes 1 and
+// 2 away, the mirrored eight and sixteen, the lanes 16 and 32 away.
+template <int STEP, class T>
+__device__ __forceinline__ T exchange(T x) {
+  if constexpr (STEP >= 4) {
+    return __shfl_xor(x, 1 << STEP);
+  } else {
+    constexpr int C = STEP == 0 ? 0xB1 : STEP == 1 ? 0x4E : STEP == 2 ? 0x141 : 0x140;
     if constexpr (sizeof(T) == 8) {
       const uint64_t u = __builtin_bit_cast(uint64_t, x);
       return __builtin_bit_cast(T, (uint64_t)(uint32_t)dpp<C>((int)(uint32_t)u) |
@@ -62,14 +66,14 @@ __device__ __forceinline__ T group_all(T v, F f) {
     } else {
       return __builtin_bit_cast(T, dpp<C>(__builtin_bit_cast(int, x)));
     }
-  };
-  v = f(v, at(v, std::integral_constant<int, 0xB1>{}));
-  v = f(v, at(v, std::integral_constant<int, 0x4E>{}));
-  v = f(v, at(v, std::integral_constant<int, 0x141>{}));
-  if constexpr (LPT >= 16) v = f(v, at(v, std::integral_constant<int, 0x140>{}));
-  if constexpr (LPT >= 32) v = f(v, __shfl_xor(v, 16));
-  if constexpr (LPT >= 64) v = f(v, __shfl_xor(v, 32));
-  return v;
+  }
+}
+
+// v combined over the LPT lanes of a group, the same bits in each.
+template <int LPT, int STEP = 0, class T, class F>
+__device__ __forceinline__ T group_all(T v, F f) {
+  if constexpr (1 << STEP < LPT) return group_all<LPT, STEP + 1>(f(v, exchange<STEP>(v)), f);
+  else return v;
 }
 
 template <int LPT>
@@ -101,14 +105,17 @@ __device__ __forceinline__ float exp_le0(float d) {
 // all different.  BF16: the ordered bits (negative numbers complemented) and
 // the expert's complement below them.  fp32: the value as a double, whose
 // significand has 29 bits to spare, with the expert (or its complement, where
-// more is larger) in the last ten.  none(): below every key.
+// more is larger) in the last ten.  -Inf has keys as well, below those of all
+// finite values; none() lies below every key.
 struct KeyBf16 {
   using T = uint32_t;
   static __device__ __forceinline__ T none() { return 0u; }
   static __device__ __forceinline__ T make(float v, uint32_t e) {
     const uint32_t u = __float_as_uint(v + 0.f);  // -0 as +0
-    return ((u & 0x80000000u ? ~u : u | 0x80000000u) & 0xffff0000u) | (0xffffu - e);
+    const uint32_t flip = (uint32_t)((int)u >> 31) | 0x80000000u;
+    return ((u ^ flip) & 0xffff0000u) | (0xffffu - e);
   }
+  static __device__ __forceinline__ bool finite(T k) { return k > 0x007fffffu; }
   static __device__ __forceinline__ T max(T x, T y) { return x > y ? x : y; }
   static __device__ __forceinline__ T min(T x, T y) { return x > y ? y : x; }
   static __device__ __forceinline__ uint32_t expert(T k) { return 0xffffu - (k & 0xffffu); }
@@ -122,9 +129,12 @@ struct KeyF32 {
   static __device__ __forceinline__ T none() { return -__builtin_inf(); }
   static __device__ __forceinline__ T make(float v, uint32_t e) {
     const float z = v + 0.f;  // -0 as +0
-    return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, (double)z) |
-                                          (z < 0.f ? e : 1023u - e));
+    // -Inf as a number below fp32's: its bits with an expert in them are a NaN's
+    const uint64_t u = __builtin_bit_cast(uint64_t, max((double)z, -0x1p130));
+    const uint32_t flip = (uint32_t)((int)(uint32_t)(u >> 32) >> 31);
+    return __builtin_bit_cast(double, u | ((flip ^ (1023u - e)) & 1023u));
   }
+  static __device__ __forceinline__ bool finite(T k) { return k > -0x1p129; }
   // (written out: no operand is a NaN that would have to be made quiet first)
   static __device__ __forceinline__ T max(T x, T y) {
     T r;
@@ -163,16 +173,57 @@ __device__ __forceinline__ void sort_keys(typename K::T (&k)[N]) {
           }
 }
 
+// The N largest keys of a group, sorted, in every lane, from each lane's sorted
+// keys: at each exchange the larger of one list's and the other's reversed are
+// the N largest of both, rising and then falling, which log2(N) rounds sort.
+template <class K, int LPT, int N, int STEP = 0>
+__device__ __forceinline__ void merge_keys(typename K::T (&k)[N]) {
+  if constexpr (1 << STEP < LPT) {
+    typename K::T o[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = exchange<STEP>(k[i]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) k[i] = K::max(k[i], o[N - 1 - i]);
+#pragma unroll
+    for (int q = N / 2; q >= 1; q >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (!(i & q)) {
+          const typename K::T x = k[i], y = k[i + q];
+          k[i] = K::max(x, y);
+          k[i + q] = K::min(x, y);
+        }
+    merge_keys<K, LPT, N, STEP + 1>(k);
+  }
+}
+
+// mine[i]: the group's choice l + LPT i, of the k <= N largest.
+template <class K, int LPT, int N, int VPT, int KPL>
+__device__ __forceinline__ void choose(const typename K::T (&key)[VPT], int l, uint32_t k,
+                                       typename K::T (&mine)[KPL]) {
+  typename K::T top[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) top[i] = key[i];
+  merge_keys<K, LPT, N>(top);
+#pragma unroll
+  for (int i = 0; i < N; ++i) mine[0] = ((uint32_t)i < k && i == l) ? top[i] : mine[0];
+}
+
 // This lane's logits of a token: experts l, l + LPT, ... ; -Inf past E.
 template <bool F32, int LPT, int VPT>
 __device__ __forceinline__ void load_logits(uint64_t base, uint64_t at, uint32_t E, int l,
                                             float (&v)[VPT]) {
+  auto load = [&](uint32_t e) {
+    return F32 ? gp<const float>(base)[at + e] : bf16_to_f32(gp<const uint16_t>(base)[at + e]);
+  };
+  if (E == LPT * VPT) {  // one address, no lane left out
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const uint32_t e = l + LPT * i;
-    v[i] = -__builtin_inff();
-    if (e < E)
-      v[i] = F32 ? gp<const float>(base)[at + e] : bf16_to_f32(gp<const uint16_t>(base)[at + e]);
+    for (int i = 0; i < VPT; ++i) v[i] = load(l + LPT * i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) v[i] = load(min((uint32_t)(l + LPT * i), E - 1));
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) v[i] = l + LPT * i < E ? v[i] : -__builtin_inff();
   }
 }
 
@@ -199,8 +250,8 @@ __device__ __forceinline__ TokenState token_state(bool on, const float (&v)[VPT]
 struct PlaceSmem {
   uint64_t chose[2][kMaxExperts];  // tokens 0-63 and 64-127 of the block
   int off[kMaxExperts];            // the place of the block's first row of an expert
-  int wsum[kRouteWaves];
-  double dsum[kRouteWaves];
+  int wsum[kPlaceWaves];
+  double dsum[kPlaceWaves];
 };
 
 // Sum over the block before this thread, and the block's sum.
@@ -217,7 +268,7 @@ __device__ __forceinline__ int block_prefix(int v, int* wsum, int& total) {
   int at = inc - v;
   total = 0;
 #pragma unroll
-  for (uint32_t w = 0; w < kRouteWaves; ++w) {
+  for (uint32_t w = 0; w < kPlaceWaves; ++w) {
     at += w < (uint32_t)wave ? wsum[w] : 0;
     total += wsum[w];
   }
@@ -234,7 +285,7 @@ __device__ __forceinline__ void place_rows(const RouterArgs& a, uint32_t blk, Pl
                                            Total total, PTotal ptotal, Before before,
                                            Index index) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  static_assert(kMaxExperts <= kRouteThreads, "one expert a thread");
+  static_assert(kMaxExperts <= kPlaceThreads, "one expert a thread");
   const uint32_t e1 = threadIdx.x;
   const int c = e1 < a.E ? total(e1) : 0;
   int rows;
@@ -258,17 +309,17 @@ __device__ __forceinline__ void place_rows(const RouterArgs& a, uint32_t blk, Pl
       if (a.offsets_) gp<int32_t>(a.offsets_)[a.E] = rows;
       if (a.loss_) {
         double s = 0.0;
-        for (uint32_t w = 0; w < kRouteWaves; ++w) s += sm.dsum[w];
+        for (uint32_t w = 0; w < kPlaceWaves; ++w) s += sm.dsum[w];
         gp<float>(a.loss_)[0] =
             n ? (float)(s * (double)a.E / ((double)a.k * (double)n * (double)n)) : 0.f;
       }
     }
   }
   if (!a.tokens_ && !a.rows_) return;
-  const uint32_t t0 = blk * kRouteTokens;
+  const uint32_t t0 = blk * a.tokens;
   const uint64_t r0 = (uint64_t)t0 * a.k;
-  const uint32_t nr = min(kRouteTokens, a.T - t0) * a.k;
-  for (uint32_t i = threadIdx.x; i < nr; i += kRouteThreads) {
+  const uint32_t nr = min(a.tokens, a.T - t0) * a.k;
+  for (uint32_t i = threadIdx.x; i < nr; i += kPlaceThreads) {
     const int e = index(i);
     if (e >= 0) {
       const uint32_t q = i / a.k;
@@ -286,27 +337,30 @@ __device__ __forceinline__ void place_rows(const RouterArgs& a, uint32_t blk, Pl
   }
 }
 
-template <bool F32, int LPT, int VPT>
-__global__ void __launch_bounds__(kRouteThreads) route_kernel(RouterArgs a) {
+// Of 512 threads, so that two blocks fit a CU (32771 tokens in 257 blocks of 128:
+// 26.9 us against 28.1 of 1024 threads); one block alone takes the 1024 of place.
+template <bool F32, int LPT, int VPT, uint32_t THREADS>
+__global__ void __launch_bounds__(THREADS) route_kernel(RouterArgs a) {
+  constexpr uint32_t kWaves = THREADS / 64;
   constexpr uint32_t kTokensPerWave = 64 / LPT;
   constexpr int KPL = (kMaxTopK + LPT - 1) / LPT;
   __shared__ PlaceSmem sm;
-  __shared__ float psum[kRouteWaves][LPT * VPT];
-  __shared__ int16_t index[kRouteTokens * kMaxTopK];  // of a batch of one block
+  __shared__ float psum[kWaves][LPT * VPT];
+  __shared__ int16_t index[kOneBlock * kMaxTopK];  // of a batch of one block
   __shared__ int live_s;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l = lane % LPT, grp = lane / LPT;
-  const uint32_t t0 = blockIdx.x * kRouteTokens;
-  for (uint32_t e = threadIdx.x; e < a.E; e += kRouteThreads)
+  const uint32_t t0 = blockIdx.x * a.tokens;
+  for (uint32_t e = threadIdx.x; e < a.E; e += THREADS)
     sm.chose[0][e] = sm.chose[1][e] = 0ull;
   if (threadIdx.x == 0) live_s = 0;
   __syncthreads();
 
   float sum_p[VPT] = {};
   int live = 0;
-  const uint32_t here = min(kRouteTokens, a.T - t0);
+  const uint32_t here = min(a.tokens, a.T - t0);
   // (a wave stays together: the exchanges take every lane)
-  for (uint32_t q0 = wave * kTokensPerWave; q0 < here; q0 += kRouteWaves * kTokensPerWave) {
+  for (uint32_t q0 = wave * kTokensPerWave; q0 < here; q0 += kWaves * kTokensPerWave) {
     const uint32_t q = q0 + grp, t = t0 + q;
     const bool on = q < here && (a.mask_ == 0 || gp<const int32_t>(a.mask_)[min(t, a.T - 1)] != 0);
     float v[VPT], top;
@@ -320,40 +374,44 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouterArgs a) {
     }
     s = group_sum<LPT>(s);
     const float nan = __builtin_nanf(""), inv = 1.f / s;
+    // (every p is finite, also of a token that does not route)
+    const float share = state == kRoutes ? inv : state == kBad ? nan : 0.f;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      sum_p[i] += state == kRoutes ? p[i] * inv : state == kBad ? nan : 0.f;
+    for (int i = 0; i < VPT; ++i) sum_p[i] = __builtin_fmaf(p[i], share, sum_p[i]);
     live += state != kEmpty && l == 0;
 
-    // Every lane sorts its keys once; a round takes the largest head of the
-    // group's lists.  Lane j of the group (and j + LPT, ...) keeps choice j.
+    // Every lane sorts its keys once.  Up to eight choices the group's lists are
+    // merged; for more, a round for each choice takes the largest of their heads.
+    // Lane j of the group (and j + LPT, ...) keeps choice j.
     using Key = std::conditional_t<F32, KeyF32, KeyBf16>;
     typename Key::T key[VPT], mine[KPL];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      key[i] = (state == kRoutes && v[i] > -__builtin_inff()) ? Key::make(v[i], l + LPT * i)
-                                                             : Key::none();
+    for (int i = 0; i < VPT; ++i) key[i] = Key::make(v[i], l + LPT * i);
     sort_keys<Key>(key);
 #pragma unroll
     for (int i = 0; i < KPL; ++i) mine[i] = Key::none();
-    for (uint32_t j = 0; j < a.k; ++j) {
-      const typename Key::T best =
-          group_all<LPT>(key[0], [](auto x, auto y) { return Key::max(x, y); });
-      const bool own = key[0] == best;
-      typename Key::T next[VPT];
+    if (a.k <= 2) choose<Key, LPT, 2>(key, l, a.k, mine);
+    else if (a.k <= 4) choose<Key, LPT, 4>(key, l, a.k, mine);
+    else if (a.k <= 8) choose<Key, LPT, 8>(key, l, a.k, mine);
+    else
+      for (uint32_t j = 0; j < a.k; ++j) {
+        const typename Key::T best =
+            group_all<LPT>(key[0], [](auto x, auto y) { return Key::max(x, y); });
+        const bool own = key[0] == best;
+        typename Key::T next[VPT];
 #pragma unroll
-      for (int i = 0; i + 1 < VPT; ++i) next[i] = key[i + 1];
-      next[VPT - 1] = Key::none();
+        for (int i = 0; i + 1 < VPT; ++i) next[i] = key[i + 1];
+        next[VPT - 1] = Key::none();
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) key[i] = own ? next[i] : key[i];
+        for (int i = 0; i < VPT; ++i) key[i] = own ? next[i] : key[i];
 #pragma unroll
-      for (int i = 0; i < KPL; ++i) mine[i] = j == (uint32_t)(l + LPT * i) ? best : mine[i];
-    }
+        for (int i = 0; i < KPL; ++i) mine[i] = j == (uint32_t)(l + LPT * i) ? best : mine[i];
+      }
     int mine_e[KPL];
     float w[KPL], chosen = 0.f;
 #pragma unroll
     for (int i = 0; i < KPL; ++i) {
-      const bool ok = mine[i] != Key::none();
+      const bool ok = state == kRoutes && Key::finite(mine[i]);
       mine_e[i] = ok ? (int)Key::expert(mine[i]) : -1;
       w[i] = ok ? exp_le0(Key::value(mine[i]) - top) * inv : 0.f;
       chosen += w[i];
@@ -369,7 +427,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouterArgs a) {
           if (a.norm) w[i] /= chosen;
         }
         if (state == kBad) w[i] = nan;
-        index[q * a.k + j] = (int16_t)mine_e[i];
+        if (THREADS == kPlaceThreads) index[q * a.k + j] = (int16_t)mine_e[i];
         gp<int32_t>(a.indices_)[(uint64_t)t * a.k + j] = mine_e[i];
         gp<float>(a.weights_)[(uint64_t)t * a.k + j] = w[i];
       }
@@ -387,21 +445,21 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouterArgs a) {
   __syncthreads();
   auto block_psum = [&](uint32_t e) {
     float s = psum[0][e];
-    for (uint32_t w = 1; w < kRouteWaves; ++w) s += psum[w][e];
+    for (uint32_t w = 1; w < kWaves; ++w) s += psum[w][e];
     return s;
   };
   auto block_count = [&](uint32_t e) {
     return e == a.E ? live_s : (int)(__popcll(sm.chose[0][e]) + __popcll(sm.chose[1][e]));
   };
-  if (a.nblk > 1) {
-    for (uint32_t e = threadIdx.x; e <= a.E; e += kRouteThreads) {
+  if constexpr (THREADS < kPlaceThreads) {
+    for (uint32_t e = threadIdx.x; e <= a.E; e += THREADS) {
       gp<int32_t>(a.cnt_)[(uint64_t)blockIdx.x * (a.E + 1) + e] = block_count(e);
       if (e < a.E) gp<float>(a.psum_)[(uint64_t)blockIdx.x * a.E + e] = block_psum(e);
     }
-    return;
+  } else {
+    place_rows(a, 0, sm, block_count, block_psum, [](uint32_t) { return 0; },
+               [&](uint32_t i) { return (int)index[i]; });
   }
-  place_rows(a, 0, sm, block_count, block_psum, [](uint32_t) { return 0; },
-             [&](uint32_t i) { return (int)index[i]; });
 }
 
 // 16 experts a block (and the tokens that route): the counts become the
@@ -452,20 +510,20 @@ __global__ void __launch_bounds__(1024) router_scan_kernel(RouterArgs a) {
 // One block per 128 tokens.  Without the scan the block adds up all blocks'
 // counts itself, and block 0 the probability sums (experts over the lanes, every
 // `parts`-th block of tokens a thread; the threads' sums in order).
-__global__ void __launch_bounds__(kRouteThreads) router_place_kernel(RouterArgs a) {
+__global__ void __launch_bounds__(kPlaceThreads) router_place_kernel(RouterArgs a) {
   __shared__ PlaceSmem sm;
   __shared__ int all[kMaxExperts + 1], early[kMaxExperts + 1];
-  __shared__ float ps[kRouteThreads];
+  __shared__ float ps[kPlaceThreads];
   const uint32_t w = a.E + 1, blk = blockIdx.x;
-  for (uint32_t e = threadIdx.x; e < w; e += kRouteThreads) {
+  for (uint32_t e = threadIdx.x; e < w; e += kPlaceThreads) {
     all[e] = early[e] = 0;
     if (e < a.E) sm.chose[0][e] = sm.chose[1][e] = 0ull;
   }
   __syncthreads();
   const RLD_GLOBAL int32_t* cnt = gp<const int32_t>(a.cnt_);
-  const uint32_t parts = kRouteThreads / a.E, part = threadIdx.x / a.E, e1 = threadIdx.x % a.E;
+  const uint32_t parts = kPlaceThreads / a.E, part = threadIdx.x / a.E, e1 = threadIdx.x % a.E;
   if (a.scanned) {
-    for (uint32_t e = threadIdx.x; e < w; e += kRouteThreads) {
+    for (uint32_t e = threadIdx.x; e < w; e += kPlaceThreads) {
       all[e] = gp<const int32_t>(a.total_)[e];
       early[e] = cnt[(uint64_t)blk * w + e];
     }
@@ -490,14 +548,14 @@ __global__ void __launch_bounds__(kRouteThreads) router_place_kernel(RouterArgs 
     }
     if (blk == 0) {
       int n = 0;
-      for (uint32_t b = threadIdx.x; b < a.nblk; b += kRouteThreads) n += cnt[(uint64_t)b * w + a.E];
+      for (uint32_t b = threadIdx.x; b < a.nblk; b += kPlaceThreads) n += cnt[(uint64_t)b * w + a.E];
       if (n) atomicAdd(&all[a.E], n);
     }
   }
-  const uint32_t t0 = blk * kRouteTokens;
+  const uint32_t t0 = blk * a.tokens;
   const uint64_t r0 = (uint64_t)t0 * a.k;
-  const uint32_t nr = min(kRouteTokens, a.T - t0) * a.k;
-  for (uint32_t i = threadIdx.x; i < nr; i += kRouteThreads) {
+  const uint32_t nr = min(a.tokens, a.T - t0) * a.k;
+  for (uint32_t i = threadIdx.x; i < nr; i += kPlaceThreads) {
     const int e = gp<const int32_t>(a.indices_)[r0 + i];
     const uint32_t q = i / a.k;
     if (e >= 0) atomicOr((unsigned long long*)&sm.chose[q >> 6][e], 1ull << (q & 63));
@@ -637,6 +695,16 @@ static int check_router(const void* logits, int f32, uint32_t ls, uint32_t T, ui
   return RLD_OK;
 }
 
+// Tokens of a block: as few as keep the blocks within one for each CU, since a
+// CU takes 2 to 3 us for 32 of them (k = 8 of 128 experts, us with blocks of 128
+// against these: 256 tokens 16.4 and 11.1, 4096 19.3 and 15.9, 16384 22.0 and 19.5).
+static uint32_t block_tokens(uint32_t T) {
+  if (T <= kOneBlock) return kOneBlock;
+  uint32_t n = kRouteTokens;
+  while (n > 32 && div_ceil(T, n / 2) <= 256) n /= 2;
+  return n;
+}
+
 static bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 // Lanes of a token by the number of experts: eight logits a lane (16 above 512).
@@ -652,7 +720,8 @@ static void by_experts(bool f32, uint32_t E, const A& a, hipStream_t st) {
 template <bool F32, int LPT, int VPT>
 struct Route {
   static void go(const RouterArgs& a, hipStream_t st) {
-    route_kernel<F32, LPT, VPT><<<a.nblk, kRouteThreads, 0, st>>>(a);
+    if (a.nblk > 1) route_kernel<F32, LPT, VPT, 512><<<a.nblk, 512, 0, st>>>(a);
+    else route_kernel<F32, LPT, VPT, kPlaceThreads><<<1, kPlaceThreads, 0, st>>>(a);
   }
 };
 
@@ -679,7 +748,7 @@ using namespace rld;
 extern "C" size_t rld_moe_router_workspace_bytes(uint32_t num_tokens, uint32_t num_experts,
                                                  uint32_t top_k) {
   if (num_tokens == 0 || num_experts == 0 || top_k == 0) return 0;
-  const size_t nblk = div_ceil(num_tokens, kRouteTokens);
+  const size_t nblk = div_ceil(num_tokens, block_tokens(num_tokens));
   return ((size_t)(num_experts + 1) * nblk * 8 + (size_t)(num_experts + 1) * 8 + 15) & ~(size_t)15;
 }
 
@@ -722,7 +791,8 @@ extern "C" int rld_moe_router(const void* logits, int logits_f32, uint32_t logit
   a.ls = logits_row_stride;
   a.k = top_k;
   a.norm = norm_topk ? 1u : 0u;
-  a.nblk = div_ceil(num_tokens, kRouteTokens);
+  a.tokens = block_tokens(num_tokens);
+  a.nblk = div_ceil(num_tokens, a.tokens);
   a.scanned = a.nblk > kScanBlocks ? 1u : 0u;
   const uint64_t cells = (uint64_t)(num_experts + 1) * a.nblk;
   a.cnt_ = (uint64_t)workspace;
@@ -738,7 +808,7 @@ extern "C" int rld_moe_router(const void* logits, int logits_f32, uint32_t logit
     router_scan_kernel<<<div_ceil(num_experts + 1, 16), 1024, 0, st>>>(a);
     if ((r = launch_status())) return r;
   }
-  router_place_kernel<<<a.nblk, kRouteThreads, 0, st>>>(a);
+  router_place_kernel<<<a.nblk, kPlaceThreads, 0, st>>>(a);
   return launch_status();
 }
 

@@ -241,6 +241,30 @@ def test_router_and_gradient(T, E, k, f32, norm):
 
 
 @pytest.mark.parametrize("f32", [False, True], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("k", [1, 2, 3, 4, 5, 7, 8, 9, 17])
+@pytest.mark.parametrize("E", [64, 129, 512, 1000])
+def test_every_width_of_the_choice(E, k, f32):
+    """Choices of each count, among many equal logits and rows with few finite ones."""
+    rng = np.random.default_rng(E + k)
+    l = np.round(logits_of(rng, 67, E, odd=False))  # few values: ties
+    l[5] = -INF
+    l[5, E // 2: E // 2 + 3] = 1.0
+    l[6] = 0.0
+    l[7] = -0.0
+    l[7, ::2] = 0.0
+    Router(l, f32).check(k, True)
+
+
+@pytest.mark.parametrize("T", [64, 65, 128, 1025, 8192, 8193, 16385])
+def test_batches_around_the_blocks_of_tokens(T):
+    """Where the blocks become larger, or one more: the tables are those of the
+    plain form, of a masked batch too."""
+    rng = np.random.default_rng(T)
+    mask = (rng.random(T) < 0.9).astype(np.int32)
+    Router(logits_of(rng, T, 16), False, mask).check(2, False)
+
+
+@pytest.mark.parametrize("f32", [False, True], ids=["bf16", "fp32"])
 def test_lowest_values_and_large_ones(f32):
     """Masks of the type's lowest value are finite: such experts come last, with
     probability zero beside others and an even one among themselves."""

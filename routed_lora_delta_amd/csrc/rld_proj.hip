@@ -21,6 +21,7 @@
 // term).  The matrix cores take bf16, so a low value enters as the sum of two
 // bf16 parts where the result is rounded to bf16 (16 significand bits, an
 // error of 2^-17) and of three where it is fp32 (24 bits: all of it).
+#include <algorithm>
 #include <type_traits>
 
 #include "rld_device.hpp"
@@ -1360,6 +1361,8 @@ __global__ void __launch_bounds__(512) big_tile_kernel(TileArgs a) {
 struct WgradArgs {
   uint64_t v_, parts_, order_, span_, dtab_;  // parts_: bf16 [n][3][R] by position
   uint32_t vs, width, R, tiles, accumulate;
+  uint64_t sum_;  // fp32 [splits][slots] results of a split, added up afterwards
+  uint32_t splits, slots;
 };
 
 // The shape of a block for ranks up to 16 * RT: 128 columns of the wide operand,
@@ -1379,7 +1382,8 @@ struct WgradShape {
 // the slot's positions of low[pos][r] * wide[row][col], 64 positions a step,
 // two steps in LDS.  Both operands lie by position, as their rows do in memory,
 // and are read transposed.  The low values come in three bf16 parts, which
-// hold all 24 bits.  DB: the result is [col][R] instead of [R][col].
+// hold all 24 bits.  DB: the result is [col][R] instead of [R][col].  With few
+// slots and columns the positions are split as well (wgrad_splits).
 template <int RT, bool DB>
 __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, unsigned char* lds) {
   using S = WgradShape<RT>;
@@ -1389,12 +1393,15 @@ __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, un
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, c = lane & 15;
   const int wr = wave / S::WC, wc = wave % S::WC;
-  const int s = item / a.tiles;
+  const uint32_t part = item / a.tiles, split = part / a.slots, s = part % a.slots;
   const uint32_t col0 = item % a.tiles * 128;
-  const uint64_t dst = gp<const uint64_t>(a.dtab_)[s];
-  if (dst == 0ull) return;
-  const uint32_t begin = gp<const uint32_t>(a.span_)[2 * s];
-  const uint32_t cnt = gp<const uint32_t>(a.span_)[2 * s + 1];
+  const uint64_t table = gp<const uint64_t>(a.dtab_)[s];
+  if (table == 0ull) return;
+  const bool whole = a.splits == 1;
+  const uint64_t dst = whole ? table : a.sum_ + (uint64_t)part * a.width * a.R * 4;
+  const uint32_t all = gp<const uint32_t>(a.span_)[2 * s + 1];
+  const uint32_t per = ((all + 63) / 64 + a.splits - 1) / a.splits * 64, skip = min(split * per, all);
+  const uint32_t begin = gp<const uint32_t>(a.span_)[2 * s] + skip, cnt = min(per, all - skip);
   const RLD_GLOBAL int32_t* order = gp<const int32_t>(a.order_) + begin;
   const uint64_t zeros = (uint64_t)&g_zero16[0];
   const uint32_t lds0 = lds_addr(lds);
@@ -1497,7 +1504,7 @@ __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, un
       if (col >= a.width || rank >= a.R) continue;
       const uint64_t at = DB ? (uint64_t)col * a.R + rank : (uint64_t)rank * a.width + col;
       RLD_GLOBAL floatx4* o = gp<floatx4>(dst + at * 4);
-      *o = a.accumulate ? *o + acc[mt][nt] : acc[mt][nt];
+      *o = whole && a.accumulate ? *o + acc[mt][nt] : acc[mt][nt];
     }
 }
 
@@ -1517,6 +1524,22 @@ __global__ void __launch_bounds__(256) end_kernel(WgradArgs da, WgradArgs db, Fi
 template <int KS, int MI>
 __global__ void __launch_bounds__(256) finish_kernel(FinishArgs a) {
   finish_item<KS, MI, false>(a, blockIdx.x, nullptr);
+}
+
+// The splits of dA and dB added up in their order, four values a thread.
+__global__ void __launch_bounds__(256) wgrad_sum_kernel(WgradArgs da, WgradArgs db, uint32_t blocks) {
+  const bool second = blockIdx.x >= blocks;
+  const WgradArgs& a = second ? db : da;
+  const uint32_t quads = a.width * (a.R / 4);
+  const uint32_t i = (blockIdx.x - (second ? blocks : 0u)) * 256 + threadIdx.x;
+  if (i >= a.slots * quads) return;
+  const uint64_t table = gp<const uint64_t>(a.dtab_)[i / quads];
+  if (table == 0ull) return;
+  floatx4 v = floatx4{0.f, 0.f, 0.f, 0.f};
+  for (uint32_t sp = 0; sp < a.splits; ++sp)
+    v += *gp<const floatx4>(a.sum_ + ((uint64_t)sp * a.slots * quads + i) * 16);
+  RLD_GLOBAL floatx4* o = gp<floatx4>(table + (uint64_t)(i % quads) * 16);
+  *o = a.accumulate ? *o + v : v;
 }
 
 // ------------------------------------------------------------------- host ----
@@ -1575,6 +1598,21 @@ static TilePlan tile_plan(uint32_t n, uint32_t K, uint32_t N) {
   p.splits = div_ceil(steps, p.steps);
   p.sums = round16((size_t)p.splits * n * N * 4);
   return p;
+}
+
+// How often dA's and dB's positions are split: until some 512 blocks are busy, of
+// at least 256 positions each if the slots have equally many.  (us of dA and dB
+// whole against split, one slot of rank 16, 4096 -> 4096: 4096 rows 69 and 48,
+// 16384 rows 251 and 138, where x and dy are read twice in 113.)
+static uint32_t wgrad_splits(uint32_t n, uint32_t K, uint32_t N, uint32_t slots) {
+  const uint64_t items = (uint64_t)slots * (div_ceil(K, 128) + div_ceil(N, 128));
+  const uint64_t s = std::min<uint64_t>(512 / items, n / ((uint64_t)slots * 256));
+  return s < 1 ? 1u : s > 16 ? 16u : (uint32_t)s;
+}
+
+static size_t wgrad_bytes(uint32_t n, uint32_t K, uint32_t N, uint32_t R, uint32_t slots) {
+  const uint32_t s = wgrad_splits(n, K, N, slots);
+  return s == 1 ? 0 : (size_t)s * slots * R * ((size_t)K + N) * 4;
 }
 
 static size_t sort_bytes(uint32_t n, uint32_t max_loras) {
@@ -1843,7 +1881,7 @@ extern "C" size_t rld_proj_grad_workspace_bytes(uint32_t n, uint32_t k_in, uint3
   if (k_in == 0 || n_out == 0 || max_rank == 0 || max_loras == 0) return 0;
   const LowPlan u = low_plan(n, k_in, max_rank, 3), g = low_plan(n, n_out, max_rank, 3);
   return sort_bytes(n, max_loras) + u.low + u.partial + 2 * g.low + g.partial +
-         (n ? tile_plan(n, n_out, k_in).sums : 0);
+         (n ? tile_plan(n, n_out, k_in).sums : 0) + wgrad_bytes(n, k_in, n_out, max_rank, max_loras);
 }
 
 extern "C" int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_row_stride,
@@ -1950,8 +1988,12 @@ extern "C" int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_r
   a.accumulate = b.accumulate = accumulate ? 1u : 0u;
   a.tiles = div_ceil(a.width, 128);
   b.tiles = div_ceil(b.width, 128);
-  const uint32_t ia = da_table ? a.tiles * route->max_loras : 0u;
-  const uint32_t ib = db_table ? b.tiles * route->max_loras : 0u;
+  a.slots = b.slots = route->max_loras;
+  a.splits = b.splits = wgrad_splits(n, K, N, route->max_loras);
+  a.sum_ = sums + t.sums;
+  b.sum_ = a.sum_ + (uint64_t)a.splits * a.slots * R * K * 4;
+  const uint32_t ia = da_table ? a.tiles * a.slots * a.splits : 0u;
+  const uint32_t ib = db_table ? b.tiles * b.slots * b.splits : 0u;
   const FinishArgs f = finish_args(route, true, t, sums, sort.order_, sort.skey_, gparts, 0, 0, true, dx,
                                    dx_row_stride, n);
   const uint32_t grid = ia + ib + (part ? f.tiles * div_ceil(n, kFinishRows) : 0u);
@@ -1960,5 +2002,11 @@ extern "C" int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_r
   else if (R <= 32) end_kernel<2><<<grid, 256, 0, st>>>(a, b, f, ia, ib);
   else if (R <= 64) end_kernel<4><<<grid, 256, 0, st>>>(a, b, f, ia, ib);
   else end_kernel<8><<<grid, 256, 0, st>>>(a, b, f, ia, ib);
+  if (a.splits > 1 && adapters) {
+    if ((e = launch_status())) return e;
+    const uint32_t ba = da_table ? div_ceil(a.slots * K * (R / 4), 256u) : 0u;
+    const uint32_t bb = db_table ? div_ceil(b.slots * N * (R / 4), 256u) : 0u;
+    wgrad_sum_kernel<<<ba + bb, 256, 0, st>>>(a, b, ba);
+  }
   return launch_status();
 }

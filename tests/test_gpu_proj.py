@@ -368,6 +368,33 @@ def test_grad_accumulates():
     assert np.array_equal(db, (start_b + db0.astype(np.float32)).astype(np.float64))
 
 
+@pytest.mark.parametrize("n,k,m,r,slots,adapted", [
+    (1300, 264, 136, 16, 1, None),
+    (2100, 136, 520, 64, 2, [False, True]),   # one slot left out, rows of no slot between
+    (1100, 72, 40, 128, 1, None),
+])
+def test_grad_of_few_slots(n, k, m, r, slots, adapted):
+    """Many rows a slot, so that their sums are made in pieces: the values, and the
+    one addition where they accumulate; the same bits in both."""
+    say(f"case: proj_grad few slots {n} {k} {m} {r}")
+    c = Case(n, k, m, r, slots, "mixed", 8, 0, 8, seed=31, adapted=adapted)
+    c.check_grads()
+    _, da0, db0 = c.grad()
+    need = R.rld_proj_grad_workspace_bytes(c.n, c.k, c.m, c.r, c.slots)
+    c.tables()
+    start_a = c.rng.standard_normal((c.slots, c.r, c.k)).astype(np.float32)
+    start_b = c.rng.standard_normal((c.slots, c.m, c.r)).astype(np.float32)
+    c.dad[:, :c.r] = torch.from_numpy(start_a).to(c.dev)
+    c.dbd[:, :c.m] = torch.from_numpy(start_b).to(c.dev)
+    scratch = c.scratch(need)
+    R.check(c.call_grad(None, scratch, accumulate=1), "rld_proj_grad")
+    torch.cuda.synchronize()
+    assert (scratch[need:] == 0xFF).all()
+    da, db = c.slot_gradients()
+    assert np.array_equal(da, (start_a + da0.astype(np.float32)).astype(np.float64))
+    assert np.array_equal(db, (start_b + db0.astype(np.float32)).astype(np.float64))
+
+
 @pytest.mark.parametrize("accumulate", [0, 1])
 def test_grad_of_no_rows(accumulate):
     c = Case(1, 72, 40, 8, 3, seed=8)

@@ -37,7 +37,10 @@ constexpr uint32_t kFinishRows = 64;  // positions of a finish block of a large 
 constexpr uint32_t kLowRows = 64;    // rows of a low item
 constexpr uint32_t kLowChunk = 512;  // k elements of a low item, at least
 constexpr uint32_t kMaxStride = 1u << 21;
-constexpr uint32_t kBigTiles = 160;  // 256 x 256 tiles from which a grid of them pays
+// 256 x 256 tiles from which a grid of them pays (us against smaller split ones,
+// 96 tiles, 4096 -> 4096: 99.1 and 95.2; 128: 99 and 99; 144: 100 and 133; 144,
+// 12288 -> 4096: 261 and 358).
+constexpr uint32_t kBigTiles = 128;
 
 // 16 bytes of zeros per device: where a lane's source is outside the operand.
 __device__ uint4 g_zero16[1];
@@ -1674,12 +1677,15 @@ static uint32_t sum_blocks(const LowArgs& a) {
   return (uint32_t)(((uint64_t)a.n * (a.R / 4) + 255) / 256);
 }
 
-// Whether the low products are worth waiting for the sort.  Unsorted, every 64
-// rows may name every slot and read its matrix again (from cache); the sort
-// takes 5 us by itself, in which some 50 MB are read so.
-static bool sort_first(const rld_route* r, uint32_t n, uint32_t K) {
+// Whether the low products (of K columns in all) are worth waiting for the sort.
+// Unsorted, every 64 rows may name every slot and take its matrix by itself; the
+// sort takes 5 us, in which some 1000 pieces of 512 columns are multiplied so.  (us
+// unsorted against sorted, 16 slots of rank 16, 4096 -> 4096, slots shuffled: 512
+// rows 43.8 and 42.0, 768 rows 55.9 and 51.3, 1024 rows 73.0 and 60.4; 1237 rows
+// 4096 -> 1024 in runs of one slot, the other way: 33.4 and 35.7.)
+static bool sort_first(const rld_route* r, uint32_t n, uint64_t K) {
   const uint64_t slots = r->max_loras < kLowRows ? r->max_loras : kLowRows;
-  return (uint64_t)(div_ceil(n, kLowRows) - 1) * slots * r->max_rank * K * 2 > (50ull << 20);
+  return div_ceil(n, kLowRows) * slots * ((K + kLowChunk - 1) / kLowChunk) > 1024;
 }
 
 template <bool TRANS>
@@ -1849,9 +1855,11 @@ extern "C" int rld_proj(const rld_route* route, const void* w, uint32_t w_row_st
     sort_kernel<<<route->max_loras + 1, 256, 0, st>>>(sort);
     if ((e = launch_status())) return e;
   }
-  // finish adds up the low rows' chunks itself while its column tiles are few
+  // finish adds up the low rows' chunks itself while they are few: each of its
+  // tiles of 64 columns reads them (4096 -> 1024 at rank 16, itself against summed
+  // first: 1237 rows, 10 MB read so, 35.7 us and 37.6; 2048 rows, 17 MB, 48.2 and 44.5)
   const uint64_t again = (uint64_t)div_ceil(N, 64) * n * R * 4 * p.nch;
-  const bool sum = again > (32ull << 20);
+  const bool sum = again > (12ull << 20);
   const LowArgs l = low_args(route, false, x, x_row_stride, n, first ? sort.order_ : 0,
                              first ? sort.skey_ : seq, 2, parts, partial);
   StartArgs s;
@@ -1929,7 +1937,7 @@ extern "C" int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_r
   const bool want_u = n && db_table, want_g = n && (dx || da_table);
   const bool part = n && dx && !t.big;
   // the sort first where the low products gain from it, or nothing else starts with it
-  const bool first = !part || sort_first(route, n, K > N ? K : N);
+  const bool first = !part || sort_first(route, n, (uint64_t)K + N);
   // low rows by sorted position, if they are sorted first and the large tiles
   // can reach the rows so
   const bool keep =

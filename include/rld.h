@@ -434,10 +434,10 @@ int rld_moe_grouped_pair(const rld_moe_route* route_a, const rld_moe_route* rout
                          void* stream);
 
 /* Bytes of workspace rld_proj needs: the rows' order by slot, the fp32 low-rank
- * rows [n][max_rank], their partial sums [ceil(k_in / 512)][n][max_rank] and,
- * for calls too small to fill the chip with large tiles, up to 16 partial sums
- * of the product [n][n_out].  It does not grow steadily with n: ask for the
- * largest call of each kind.  16-byte aligned device memory; nothing in it must start at any value or is carried
+ * rows [n][max_rank], their partial sums over k chunks and, for calls too small
+ * to fill the chip with large tiles, up to 16 partial sums of the product
+ * [n][n_out].  What is returned for n does for every smaller n as well.  16-byte
+ * aligned device memory; nothing in it must start at any value or is carried
  * between calls; calls that share it must be ordered (captured graphs that
  * share one included). */
 size_t rld_proj_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t n_out, uint32_t max_rank,
@@ -456,15 +456,18 @@ size_t rld_proj_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t n_out, uint3
  *            out + i*out_row_stride; the rest of the row is left alone.  out
  *            must not overlap w or x
  * n == 0 is a no-op.  RLD_EUNSUPPORTED for row strides above 2^21,
- * n above 2^26, k_in or n_out above 2^21, and from 2^23 tiles of 64 x 64 outputs, 2^21
- * pairs of a slot and 64 columns, or n * max_rank of 2^32 on.
+ * n above 2^26, k_in or n_out above 2^21, and from 2^23 tiles of 64 rows by 64
+ * columns (of k_in or n_out, the wider), 2^21 pairs of a slot and 64 columns, or
+ * n * max_rank of 2^32 on.
  * Results do not change from run to run; a row's summation order may depend on
  * n (the tile shape does). */
 int rld_proj(const rld_route* route, const void* w, uint32_t w_row_stride, const void* x,
              uint32_t x_row_stride, const int32_t* seq_slot, uint32_t n, void* out,
              uint32_t out_row_stride, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace rld_proj_grad needs, under the contract of rld_proj's. */
+/* Bytes of workspace rld_proj_grad needs, under the contract of rld_proj's: the
+ * same for both low-rank products and dx, and where slots are few and rows many
+ * up to 16 partial sums of every slot's gradients. */
 size_t rld_proj_grad_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t n_out,
                                      uint32_t max_rank, uint32_t max_loras);
 
@@ -482,10 +485,10 @@ size_t rld_proj_grad_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t n_out,
  *            overlap
  *   accumulate  0: da and db are overwritten (with zeros for a slot without
  *            rows); nonzero: the gradient is added to what they hold
- * Every routed row of a slot adds to the slot's gradient in ascending row order
- * of fixed groups: results do not change from run to run.  n == 0: zeros, or
- * nothing with accumulate.  Errors as rld_proj (the stride of x is not limited); RLD_EINVAL if nothing is
- * wanted. */
+ * A slot's rows are added in ascending order, in fixed groups: results do not
+ * change from run to run.  dx must not overlap w, x or dy.  n == 0: zeros, or
+ * nothing with accumulate.  Errors as rld_proj (the stride of x is not limited);
+ * RLD_EINVAL if nothing is wanted. */
 int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_row_stride, const void* x,
                   uint32_t x_row_stride, const void* dy, uint32_t dy_row_stride,
                   const int32_t* seq_slot, uint32_t n, void* dx, uint32_t dx_row_stride,
@@ -493,7 +496,7 @@ int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_row_stride, 
                   void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace rld_moe_router needs, under the contract of rld_proj's:
- * a count and a partial sum per expert and block of 128 tokens. */
+ * a count and a partial sum per expert and block of 32 to 128 tokens. */
 size_t rld_moe_router_workspace_bytes(uint32_t num_tokens, uint32_t num_experts,
                                       uint32_t top_k);
 
@@ -540,7 +543,7 @@ int rld_moe_router(const void* logits, int logits_f32, uint32_t logits_row_strid
  *            may then be NULL).  The counts themselves have no gradient
  *   dlogits  of the logits' type, row t at dlogits + t*dlogits_row_stride,
  *            num_experts written; zeros for empty tokens, NaN for a token with a
- *            NaN or +Inf logit.  May be the logits themselves
+ *            NaN or +Inf logit.  May be the logits themselves, at their stride
  * RLD_EINVAL if both gradients are NULL; otherwise errors as rld_moe_router. */
 int rld_moe_router_grad(const void* logits, int logits_f32, uint32_t logits_row_stride,
                         const int32_t* token_mask, uint32_t num_tokens, uint32_t num_experts,

@@ -10,12 +10,15 @@
 //            sorted positions and reach x, dy and the outputs through the order.
 //   low      the low-rank products u and g of every routed row, as fp32 partial
 //            sums of k chunks; low_reduce adds the chunks and applies the scale.
-//   tile     one output tile of x W^T (or dy W) on the matrix cores, with the
-//            low rows times the slots' second matrices added into the same
-//            accumulators, so the output is rounded once and written once.
-//   rows     the same for up to 64 rows, where reading W is all the time: blocks
-//            of 16 columns, K dealt to the waves, no sort and no reduce launch.
-//   wgrad    dA and dB: the products over a slot's rows.
+//   big_tile one 256 x 256 output tile of x W^T (or dy W) with the low rows times
+//            the slots' second matrices added into the same accumulators, so the
+//            output is rounded once and written once.
+//   part     for calls with too few such tiles: smaller tiles over a split of K, as
+//            fp32 sums.  The low products and, where they do not need it, the sort
+//            are other blocks of the same launch (start).
+//   finish   adds the splits and the low rows times the second matrices, and rounds.
+//   wgrad    dA and dB: the products over a slot's rows, in one launch with the
+//            finish of dx (end); wgrad_sum where the positions are split.
 //
 // u and g stay in fp32 (bf16 copies would add a rounding of 2^-9 to every
 // term).  The matrix cores take bf16, so a low value enters as the sum of two
@@ -47,15 +50,14 @@ __device__ uint4 g_zero16[1];
 
 // ------------------------------------------------------------- bf16 parts ----
 
-// v as the sum of NP bf16 values, the largest first.  Rounding to nearest
-// makes each remainder exact in fp32 (it fits the 24 - 8 bits left).
-template <int NP>
-__device__ __forceinline__ void bf16_parts(const float (&v)[8], uint4 (&out)[NP]) {
+// v as the sum of two bf16 values, the larger first, to 2^-17.  Rounding to nearest
+// makes the remainder exact in fp32 (it fits the 24 - 8 bits left).
+__device__ __forceinline__ void bf16_parts(const float (&v)[8], uint4 (&out)[2]) {
   float r[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) r[e] = v[e];
 #pragma unroll
-  for (int p = 0; p < NP; ++p) {
+  for (int p = 0; p < 2; ++p) {
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -127,7 +129,8 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* wsum, uin
 
 // One block per slot, and one for the base rows: its rows in ascending order,
 // behind those of the slots below it, which the block counts itself (no block
-// waits for another).
+// waits for another).  Bound by the latency of two passes over the ids: 4.7 us for
+// 1237 rows and 16 slots, 7 us for 4096 rows.
 __device__ __forceinline__ void sort_item(const SortArgs& a, uint32_t item, uint32_t* wsum) {
   const int s = (int)item;
   const bool base = (uint32_t)s == a.max_loras;
@@ -256,6 +259,18 @@ __device__ __forceinline__ uint4 lds_tr16(RLD_LDS unsigned char* p, int skip) {
   return make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
 
+// What the 32-byte column pairs of row k are swapped by, where a row of such a tile
+// has PAIRS of them: half a wave reads rows 0 .. 3 of two neighbouring eights at a
+// time, whose eight places should lie on all of the 256 bytes of banks.  (Rows of
+// 128 bytes take turns in its halves by themselves, rows of 64 in its quarters.)
+template <int PAIRS>
+__device__ __forceinline__ uint32_t tr_swap(uint32_t k) {
+  const uint32_t eight = (k >> 3) & 1;
+  return PAIRS >= 8 ? (k & 3) | eight << 2
+         : PAIRS == 4 ? ((k >> 1) & 1) | eight << 1
+         : PAIRS == 2 ? eight : 0;
+}
+
 // Buffer accesses that need no branch: lanes past the end read zeros and store
 // nothing.
 __device__ __forceinline__ uint4 buffer_load16(uint64_t base, uint64_t bytes, uint32_t off) {
@@ -374,6 +389,8 @@ constexpr int kLowLds = kLowStages * 128 * 128;
 // x and the matrix go by in 64-wide k steps through LDS, in whole 128-byte
 // pieces; four waves of 32 x 32.
 // TRANS: the matrix is [K][R] (B_s) instead of [R][K] (A_s).
+// Bound by reading x: u of 4096 rows of 12288 and g of 4096 in 34.5 us, 134 MB at
+// 3.9 TB/s (a large copy reaches 4.7).
 template <bool TRANS>
 __device__ __forceinline__ void low_item(const LowArgs& a, uint32_t item, unsigned char* lds) {
   const int lane = threadIdx.x & 63;
@@ -422,7 +439,7 @@ __device__ __forceinline__ void low_item(const LowArgs& a, uint32_t item, unsign
           vm[p] = r * a.K * 2 + q * 16;
           km[p] = r < ranks ? kb + q * 8 : 0xff000000u;
         } else {
-          const uint32_t h = ((r >> 1) & 1) | ((r >> 3) & 1) << 1;
+          const uint32_t h = tr_swap<4>(r);
           const uint32_t col = (((lane & 7) >> 1 ^ h) * 2 + (lane & 1)) * 8;
           vm[p] = (r * a.R + col) * 2;
           km[p] = col < ranks ? kb + r : 0xff000000u;
@@ -461,7 +478,7 @@ __device__ __forceinline__ void low_item(const LowArgs& a, uint32_t item, unsign
             if constexpr (!TRANS) {
               mf[i] = lds16(lds_at(st + 8192 + (wc * 32 + i * 16 + c) * 128 + sw));
             } else {
-              const int h = ((c >> 3) & 1) | (g & 1) << 1;
+              const int h = tr_swap<4>(8 * g + (c >> 2));
               mf[i] = lds_tr16(lds_at(st + 8192 + (ks * 32 + 8 * g + (c >> 2)) * 128 +
                                       ((wc * 2 + i) ^ h) * 32 + (c & 3) * 8),
                                4 * 128);
@@ -643,6 +660,11 @@ struct PartArgs {
 // swizzled by the row, and transposing LDS reads make the fragments.
 // The product is computed transposed (W as the first operand), so a lane
 // holds four consecutive output columns of one row.
+// Bound by reading W where rows are few (64 rows 4096 -> 4096 with their low rows in
+// 9.5 us, 36 MB at 3.8 TB/s; 256 rows 4096 -> 12288 in 43 us, 143 MB at 3.3), else by
+// the latency of a step's loads, which one step of 128 x 128 x 64 does not cover
+// (1237 rows 4096 -> 1024 in 23 us, 450 TFLOP/s).  128 KB of stages in one block
+// instead of two blocks of 64 KB takes 25 to 40% longer, tiles of 64 columns 5 to 10%.
 template <int BM, int BN, int WR, int WC, int STAGES, bool TRANS>
 __device__ __forceinline__ void part_item(const PartArgs& a, uint32_t item, unsigned char* lds) {
   constexpr int MI = BM / (16 * WR), NI = BN / (16 * WC);
@@ -690,7 +712,7 @@ __device__ __forceinline__ void part_item(const PartArgs& a, uint32_t item, unsi
       constexpr int CPR = BN / 8;  // chunks of a row
       const uint32_t k = (i - LA) * (64 / CPR) + lane / CPR;
       const uint32_t slot = lane % CPR;
-      const uint32_t h = ((k & 3) | ((k >> 3) & 3) << 2) & (kPairs - 1);
+      const uint32_t h = tr_swap<kPairs>(k);
       off[j] = k * a.ws * 2 + (((slot >> 1) ^ h) * 2 + (slot & 1)) * 16;
       kq[j] = 0;
     }
@@ -740,7 +762,7 @@ __device__ __forceinline__ void part_item(const PartArgs& a, uint32_t item, unsi
         if constexpr (!TRANS) {
           wf[ni] = lds16(lds_at(st + BM * 128 + (wc * NI * 16 + c) * 128 + sw) + ni * 2048);
         } else {
-          const int h = ((c >> 2) | g << 2) & (kPairs - 1);
+          const int h = tr_swap<kPairs>(8 * g + (c >> 2));
           wf[ni] = lds_tr16(lds_at(st + BM * 128 + (ks * 32 + 8 * g + (c >> 2)) * (BN * 2) +
                                    ((wc * NI + ni) ^ h) * 32 + (c & 3) * 8),
                             4 * BN * 2);
@@ -787,6 +809,8 @@ struct FinishArgs {
 // its matrix would survive zeros in the others).  KS: 32-wide steps of rank.
 // TRANS: the matrices are [R][N]; their 64 columns go through LDS (32 KB) and
 // transposing reads.
+// Bound by reading the sums and the slots' matrices: 256 rows of 31 slots of rank
+// 64, 12288 columns in 22 us, 80 MB at 3.7 TB/s; 5 us of a single row are latency.
 template <int KS, int MI, bool TRANS>
 __device__ __forceinline__ void finish_item(const FinishArgs& a, uint32_t item,
                                             unsigned char* lds) {
@@ -875,7 +899,7 @@ __device__ __forceinline__ void finish_item(const FinishArgs& a, uint32_t item,
               f[4 + i] = v[i] * sc;
             }
             uint4 two[2];
-            bf16_parts<2>(f, two);
+            bf16_parts(f, two);
             hi[mi][ks] = two[0];
             lo[mi][ks] = two[1];
           }
@@ -901,7 +925,7 @@ __device__ __forceinline__ void finish_item(const FinishArgs& a, uint32_t item,
                   (k < a.R && col0 + c < a.N) ? (c * a.R + k) * 2 : kBufferEnd);
             } else {
               const uint32_t r = ks * 32 + wave * 8 + (lane >> 3);
-              const uint32_t h = ((r >> 1) & 1) | ((r >> 3) & 1) << 1;
+              const uint32_t h = tr_swap<4>(r);
               const uint32_t cc = (((lane & 7) >> 1 ^ h) * 2 + (lane & 1)) * 8;
               const rsrc_t re = buffer(eb + (uint64_t)tile0 * 2,
                                        eb != 0ull ? ((uint64_t)a.R * a.N - tile0) * 2 : 0u);
@@ -920,7 +944,7 @@ __device__ __forceinline__ void finish_item(const FinishArgs& a, uint32_t item,
       for (int b = 0; b < SB; ++b) {
         if (of[b] < 0) continue;
         if constexpr (TRANS) {
-          const int h = ((c >> 3) & 1) | (g & 1) << 1;
+          const int h = tr_swap<4>(8 * g + (c >> 2));
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks)
             ef[b][ks] = lds_tr16(lds_at(lds0 + (b * KS + ks) * 4096 + (8 * g + (c >> 2)) * 128 +
@@ -995,6 +1019,10 @@ __global__ void __launch_bounds__(256, 2) start_kernel(StartArgs a) {
 // so that twelve loads of each wave stay in flight all the time, one and a half
 // steps ahead.  Waves 4-7 run one barrier behind waves 0-3 (each SIMD has one
 // of either): while one half multiplies, the other reads.
+//
+// Bound by the matrix cores' rate under these loads: 4096 x 12288 x 4096 with 64
+// ranks of low rows 330-340 us, 1.23 PFLOP/s (a library's product alone: 318-322);
+// dy W 325-345.  The whole call took 495 us with 128 x 128 tiles of four waves, now 347.
 //
 // What makes it safe.  Every phase is
 //   reads, loads, wait (reads done; all but 12 loads landed), barrier,
@@ -1387,6 +1415,10 @@ struct WgradShape {
 // and are read transposed.  The low values come in three bf16 parts, which
 // hold all 24 bits.  DB: the result is [col][R] instead of [R][col].  With few
 // slots and columns the positions are split as well (wgrad_splits).
+// Bound by the latency of a step's loads beside three times the matrix work: 4096
+// rows in four slots, 12288 and 4096 columns, rank 64, 56 us, 134 MB at 2.4 TB/s and
+// 460 TFLOP/s of bf16 parts.  (Rows' numbers in scalar registers, which spares waits,
+// or a third stage in one block a CU: 15% longer.)
 template <int RT, bool DB>
 __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, unsigned char* lds) {
   using S = WgradShape<RT>;
@@ -1417,7 +1449,7 @@ __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, un
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     rw[p] = (wave * 4 + p) * 4 + (lane >> 4);
-    const uint32_t h = ((rw[p] & 3) | ((rw[p] >> 3) & 3) << 2) & 7;
+    const uint32_t h = tr_swap<8>(rw[p]);
     const uint32_t slot = lane & 15;
     const uint32_t col = col0 + (((slot >> 1) ^ h) * 2 + (slot & 1)) * 8;
     vcol[p] = col < a.width ? a.v_ + (uint64_t)col * 2 : 0ull;
@@ -1430,7 +1462,7 @@ __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, un
     constexpr int CPR = S::RP / 8;  // chunks of a row
     const uint32_t k = (i % LL) * (64 / CPR) + lane / CPR;
     const uint32_t slot = lane % CPR;
-    const uint32_t h = ((k & 3) | ((k >> 3) & 3) << 2) & (kPairs - 1);
+    const uint32_t h = tr_swap<kPairs>(k);
     const uint32_t r = (((slot >> 1) ^ h) * 2 + (slot & 1)) * 8;
     vl[j] = r < a.R ? k * lrow + ((i / LL) * a.R + r) * 2 : kOutside;
   }
@@ -1474,19 +1506,19 @@ __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, un
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       const uint32_t k = ks * 32 + 8 * g + (c >> 2);
-      const int h = (c >> 2) | g << 2;
+      const int hw = tr_swap<8>(8 * g + (c >> 2)), hl = tr_swap<kPairs>(8 * g + (c >> 2));
       uint4 vf[S::NT];
 #pragma unroll
       for (int nt = 0; nt < S::NT; ++nt)
         vf[nt] = lds_tr16(
-            lds_at(st + k * 256 + ((wc * S::NT + nt) ^ (h & 7)) * 32 + (c & 3) * 8), 4 * 256);
+            lds_at(st + k * 256 + ((wc * S::NT + nt) ^ hw) * 32 + (c & 3) * 8), 4 * 256);
 #pragma unroll
       for (int p = 2; p >= 0; --p)
 #pragma unroll
         for (int mt = 0; mt < S::MT; ++mt) {
           const uint4 lf = lds_tr16(
               lds_at(st + S::kWide + p * S::kLow + k * (S::RP * 2) +
-                     ((wr * S::MT + mt) ^ (h & (kPairs - 1))) * 32 + (c & 3) * 8),
+                     ((wr * S::MT + mt) ^ hl) * 32 + (c & 3) * 8),
               4 * S::RP * 2);
 #pragma unroll
           for (int nt = 0; nt < S::NT; ++nt)
@@ -1620,6 +1652,27 @@ static size_t wgrad_bytes(uint32_t n, uint32_t K, uint32_t N, uint32_t R, uint32
 
 static size_t sort_bytes(uint32_t n, uint32_t max_loras) {
   return 4 * round16((size_t)n * 4) + round16((size_t)max_loras * 8);
+}
+
+static size_t proj_bytes(uint32_t n, uint32_t K, uint32_t N, uint32_t R, uint32_t slots) {
+  const LowPlan p = low_plan(n, K, R, 2);
+  return sort_bytes(n, slots) + p.low + p.partial + tile_plan(n, K, N).sums;
+}
+
+static size_t grad_bytes(uint32_t n, uint32_t K, uint32_t N, uint32_t R, uint32_t slots) {
+  const LowPlan u = low_plan(n, K, R, 3), g = low_plan(n, N, R, 3);
+  return sort_bytes(n, slots) + u.low + u.partial + 2 * g.low + g.partial +
+         (n ? tile_plan(n, N, K).sums : 0) + wgrad_bytes(n, K, N, R, slots);
+}
+
+// The most that a call of up to n rows takes.  The plans are fixed between 16, 32
+// and multiples of 64 rows, and from 2^18 rows on, so the bytes grow there.
+template <class F>
+static size_t most_bytes(uint32_t n, F bytes) {
+  size_t most = bytes(n);
+  for (uint32_t rows = 16; rows < n && rows <= 1u << 18; rows += rows < 64 ? rows : 64)
+    most = std::max(most, bytes(rows));
+  return most;
 }
 
 static SortArgs sort_args(const rld_route* r, const int32_t* seq, uint32_t n,
@@ -1800,8 +1853,9 @@ using namespace rld;
 extern "C" size_t rld_proj_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t n_out,
                                            uint32_t max_rank, uint32_t max_loras) {
   if (n == 0 || k_in == 0 || n_out == 0 || max_rank == 0 || max_loras == 0) return 0;
-  const LowPlan p = low_plan(n, k_in, max_rank, 2);
-  return sort_bytes(n, max_loras) + p.low + p.partial + tile_plan(n, k_in, n_out).sums;
+  return most_bytes(n, [=](uint32_t rows) {
+    return proj_bytes(rows, k_in, n_out, max_rank, max_loras);
+  });
 }
 
 extern "C" int rld_proj(const rld_route* route, const void* w, uint32_t w_row_stride,
@@ -1821,7 +1875,7 @@ extern "C" int rld_proj(const rld_route* route, const void* w, uint32_t w_row_st
     return e;
   if ((e = check_items(route, n))) return e;
   const uint32_t K = route->k_in, N = route->n_out, R = route->max_rank;
-  if (workspace_bytes < rld_proj_workspace_bytes(n, K, N, R, route->max_loras))
+  if (workspace_bytes < proj_bytes(n, K, N, R, route->max_loras))
     return RLD_ENOSPACE;
   const LowPlan p = low_plan(n, K, R, 2);
   const TilePlan t = tile_plan(n, K, N);
@@ -1887,9 +1941,9 @@ extern "C" int rld_proj(const rld_route* route, const void* w, uint32_t w_row_st
 extern "C" size_t rld_proj_grad_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t n_out,
                                                 uint32_t max_rank, uint32_t max_loras) {
   if (k_in == 0 || n_out == 0 || max_rank == 0 || max_loras == 0) return 0;
-  const LowPlan u = low_plan(n, k_in, max_rank, 3), g = low_plan(n, n_out, max_rank, 3);
-  return sort_bytes(n, max_loras) + u.low + u.partial + 2 * g.low + g.partial +
-         (n ? tile_plan(n, n_out, k_in).sums : 0) + wgrad_bytes(n, k_in, n_out, max_rank, max_loras);
+  return most_bytes(n, [=](uint32_t rows) {
+    return grad_bytes(rows, k_in, n_out, max_rank, max_loras);
+  });
 }
 
 extern "C" int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_row_stride,
@@ -1921,7 +1975,7 @@ extern "C" int rld_proj_grad(const rld_route* route, const void* w, uint32_t w_r
   }
   if ((e = check_items(route, n))) return e;
   const uint32_t K = route->k_in, N = route->n_out, R = route->max_rank;
-  if (workspace_bytes < rld_proj_grad_workspace_bytes(n, K, N, R, route->max_loras))
+  if (workspace_bytes < grad_bytes(n, K, N, R, route->max_loras))
     return RLD_ENOSPACE;
   if (n == 0 && !adapters) return RLD_OK;
   const LowPlan pu = low_plan(n, K, R, 3), pg = low_plan(n, N, R, 3);

@@ -153,3 +153,19 @@ def test_workspace_sizes_grow_with_the_call():
     assert g(5, 4096, 128, 16, 4) > g(4, 4096, 128, 16, 4)
     r = R.rld_moe_router_workspace_bytes
     assert r(0, 128, 8) == 0 and r(129, 128, 8) > r(128, 128, 8) > 0
+
+
+def test_workspace_for_the_largest_call_does_for_every_smaller_one():
+    for k, m, rank, slots in [(4096, 1024, 16, 16), (768, 2048, 64, 2), (64, 12288, 8, 1)]:
+        for size in (R.rld_proj_workspace_bytes, R.rld_proj_grad_workspace_bytes):
+            last = 0
+            for n in [1, 2, 15, 16, 17, 32, 33, 63, 64, 65, 100, 128, 129, 256, 500, 512, 513, 1000,
+                      1024, 1025, 2000, 2047, 2304, 2305, 4096, 8192, 20000, 1 << 17, 1 << 20]:
+                now = size(n, k, m, rank, slots)
+                assert now >= last, (size, n, k, m)
+                last = now
+    last = 0
+    for t in [1, 64, 65, 128, 129, 8191, 8192, 8193, 16384, 16385, 32768, 32769, 65536]:
+        now = R.rld_moe_router_workspace_bytes(t, 128, 8)
+        assert now >= last, t
+        last = now

@@ -662,9 +662,10 @@ struct PartArgs {
 // holds four consecutive output columns of one row.
 // Bound by reading W where rows are few (64 rows 4096 -> 4096 with their low rows in
 // 9.5 us, 36 MB at 3.8 TB/s; 256 rows 4096 -> 12288 in 43 us, 143 MB at 3.3), else by
-// the latency of a step's loads, which one step of 128 x 128 x 64 does not cover
-// (1237 rows 4096 -> 1024 in 23 us, 450 TFLOP/s).  128 KB of stages in one block
-// instead of two blocks of 64 KB takes 25 to 40% longer, tiles of 64 columns 5 to 10%.
+// how far the two blocks of a CU overlap their LDS and matrix work: 1792 rows 4096 ->
+// 4096 in 67 us, 900 TFLOP/s, and no faster where all loads hit the cache; 450 with
+// one block a CU (1237 rows 4096 -> 1024 in 23 us).  Three stages, so one block a CU,
+// take 25 to 40% longer, tiles of 64 columns 5 to 10%.
 template <int BM, int BN, int WR, int WC, int STAGES, bool TRANS>
 __device__ __forceinline__ void part_item(const PartArgs& a, uint32_t item, unsigned char* lds) {
   constexpr int MI = BM / (16 * WR), NI = BN / (16 * WC);
@@ -768,11 +769,16 @@ __device__ __forceinline__ void part_item(const PartArgs& a, uint32_t item, unsi
                             4 * BN * 2);
         }
       }
+      // matrix work before the other block's reads, where both compute much (dy W of
+      // 1536 rows 4096 -> 4096: the call 92 us against 100; x W^T the same, small
+      // tiles 2% slower)
+      if constexpr (TRANS && BM == 128) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int ni = 0; ni < NI; ++ni)
 #pragma unroll
         for (int mi = 0; mi < MI; ++mi)
           acc[ni][mi] = mfma_bf16_16x16x32(wf[ni], xf[mi], acc[ni][mi]);
+      if constexpr (TRANS && BM == 128) __builtin_amdgcn_s_setprio(0);
     }
   }
   wait_vm<0>();  // the loads past the end, of zeros

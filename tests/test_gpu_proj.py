@@ -494,6 +494,28 @@ def test_on_another_stream():
     assert np.array_equal(c.body(out, c.m, c.os), want)
 
 
+def test_two_calls_at_once():
+    """Gradients of two projections on two streams, each with its own workspace: the
+    bits of the same calls one after the other."""
+    cases = [Case(1300, 264, 392, 32, 2, seed=41), Case(150, 1032, 264, 64, 5, seed=42)]
+    want = [c.grad() for c in cases]
+    runs = []
+    for c in cases:
+        c.tables()
+        need = R.rld_proj_grad_workspace_bytes(c.n, c.k, c.m, c.r, c.slots)
+        runs.append((c, c.scratch(need), c.out_rows(c.xs), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, ws, dx, s in runs:
+            with torch.cuda.stream(s):
+                R.check(c.call_grad(dx, ws), "rld_proj_grad")
+    torch.cuda.synchronize()
+    for (c, ws, dx, s), (dx0, da0, db0) in zip(runs, want):
+        da, db = c.slot_gradients()
+        assert np.array_equal(c.body(dx, c.k, c.xs), dx0)
+        assert np.array_equal(da, da0) and np.array_equal(db, db0)
+
+
 def test_far_rows():
     """Rows whose byte offsets pass 32 bits: a row stride of 2^21 elements and rows
     that reach 4 GiB behind the start, as projection and as gradient."""

@@ -164,21 +164,26 @@ def ptr(obj) -> int | None:
     raise TypeError(f"cannot pass {type(obj)} as a pointer")
 
 
-# torch's current stream of the current device as a handle: without the Stream
-# object, which takes 3 us to make, where torch offers it so
-try:
-    from torch._C import _cuda_getCurrentRawStream as _raw_stream
-    from torch.cuda import current_device as _current_device
-except ImportError:
-    _raw_stream = None
+_current_stream = None  # found at the first call that names no stream
+
+
+def _find_current_stream():
+    """torch's current stream as a handle: without the Stream object, which takes
+    3 us to make, where torch offers it so."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    device = torch.cuda.current_device
+    return lambda: raw(device())
 
 
 def stream_handle(stream) -> int | None:
+    global _current_stream
     if stream is None:
-        if _raw_stream is not None:
-            return _raw_stream(_current_device())
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _current_stream is None:
+            _current_stream = _find_current_stream()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

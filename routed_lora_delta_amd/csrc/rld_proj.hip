@@ -1403,20 +1403,25 @@ struct WgradArgs {
 };
 
 // The shape of a block for ranks up to 16 * RT: 128 columns of the wide operand,
-// its waves over the ranks (WR) and the columns.  A stage holds 64 positions of
-// both operands.
+// its waves over the ranks (WR) and the columns.  A stage holds kStep positions of
+// both operands: 32 where that lets more blocks into a CU and they pay, two for one
+// above rank 64 (4096 rows 4096 -> 4096, rank 128: dA and dB 91 us against 107) and
+// five for two, mostly of finish, up to 32 (2050 rows 2048 -> 768: the call 43.7 us
+// against 45.5); up to 16 and 64, 64 (with 32: 23.3 for 22.9 us of 333 rows 4096 ->
+// 1024, and 452 for 450 of 4096 rows 12288 -> 4096).
 template <int RT>
 struct WgradShape {
   static constexpr int RP = 16 * RT;              // ranks of a row in LDS
   static constexpr int WR = RT >= 4 ? 2 : 1, WC = 4 / WR;
   static constexpr int MT = RT / WR, NT = 8 / WC;  // 16 x 16 blocks of a wave
-  static constexpr int kWide = 64 * 256, kLow = 64 * RP * 2;
+  static constexpr int kStep = RT == 2 || RT == 8 ? 32 : 64;
+  static constexpr int kWide = kStep * 256, kLow = kStep * RP * 2;
   static constexpr int kStage = kWide + 3 * kLow;
-  static constexpr int kLds = 2 * kStage;          // 80 KB at rank 64: two blocks a CU
+  static constexpr int kLds = 2 * kStage > 32768 ? 2 * kStage : 32768;  // finish: 32 KB
 };
 
 // Slot s, 128 columns of the wide operand (x for dA, dy for dB): the sum over
-// the slot's positions of low[pos][r] * wide[row][col], 64 positions a step,
+// the slot's positions of low[pos][r] * wide[row][col], kStep positions a step,
 // two steps in LDS.  Both operands lie by position, as their rows do in memory,
 // and are read transposed.  The low values come in three bf16 parts, which
 // hold all 24 bits.  DB: the result is [col][R] instead of [R][col].  With few
@@ -1430,6 +1435,7 @@ __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, un
   using S = WgradShape<RT>;
   constexpr int kPairs = S::RP / 16;
   constexpr int LL = S::kLow / 1024, LP = (3 * LL + 3) / 4;  // 1 KB loads of a part; a wave's
+  constexpr int WL = S::kStep / 16;                          // and of the wide operand
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, c = lane & 15;
@@ -1449,12 +1455,12 @@ __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, un
   const uint32_t lrow = 3 * a.R * 2;
   const uint64_t parts = uniform64(a.parts_ + (uint64_t)begin * lrow);
 
-  // this lane's rows (four of a step) and column of the wide operand
-  uint32_t rw[4];
-  uint64_t vcol[4];
+  // this lane's rows (WL of a step) and column of the wide operand
+  uint32_t rw[WL];
+  uint64_t vcol[WL];
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    rw[p] = (wave * 4 + p) * 4 + (lane >> 4);
+  for (int p = 0; p < WL; ++p) {
+    rw[p] = (wave * WL + p) * 4 + (lane >> 4);
     const uint32_t h = tr_swap<8>(rw[p]);
     const uint32_t slot = lane & 15;
     const uint32_t col = col0 + (((slot >> 1) ^ h) * 2 + (slot & 1)) * 8;
@@ -1472,22 +1478,22 @@ __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, un
     const uint32_t r = (((slot >> 1) ^ h) * 2 + (slot & 1)) * 8;
     vl[j] = r < a.R ? k * lrow + ((i / LL) * a.R + r) * 2 : kOutside;
   }
-  uint32_t row[4];
+  uint32_t row[WL];
   auto rows_of = [&](uint32_t i0) {
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
+    for (int p = 0; p < WL; ++p) {
       const uint32_t i = i0 + rw[p];
       row[p] = i < cnt ? (uint32_t)order[i] : 0xffffffffu;
     }
   };
   auto issue = [&](uint32_t i0) {  // row: of these positions
-    const uint32_t st = lds0 + (i0 / 64 & 1) * S::kStage;
+    const uint32_t st = lds0 + (i0 / S::kStep & 1) * S::kStage;
 #pragma unroll
-    for (int p = 0; p < 4; ++p)
+    for (int p = 0; p < WL; ++p)
       dma16((row[p] != 0xffffffffu && vcol[p]) ? vcol[p] + (uint64_t)row[p] * a.vs * 2 : zeros,
-            st + (wave * 4 + p) * 1024);
+            st + (wave * WL + p) * 1024);
     const rsrc_t rl = buffer(parts + (uint64_t)i0 * lrow,
-                             i0 < cnt ? (uint64_t)min(cnt - i0, 64u) * lrow : 0);
+                             i0 < cnt ? (uint64_t)min(cnt - i0, (uint32_t)S::kStep) * lrow : 0);
 #pragma unroll
     for (int j = 0; j < LP; ++j)
       dma16(rl, st + S::kWide + min(wave + 4 * j, 3 * LL - 1) * 1024, vl[j], 0);
@@ -1501,16 +1507,16 @@ __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, un
 
   rows_of(0);
   issue(0);
-  rows_of(64);
-  for (uint32_t i0 = 0; i0 < cnt; i0 += 64) {
+  rows_of(S::kStep);
+  for (uint32_t i0 = 0; i0 < cnt; i0 += S::kStep) {
     wait_vm<0>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    issue(i0 + 64);
-    rows_of(i0 + 128);
-    const uint32_t st = lds0 + (i0 / 64 & 1) * S::kStage;
+    issue(i0 + S::kStep);
+    rows_of(i0 + 2 * S::kStep);
+    const uint32_t st = lds0 + (i0 / S::kStep & 1) * S::kStage;
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
+    for (int ks = 0; ks < S::kStep / 32; ++ks) {
       const uint32_t k = ks * 32 + 8 * g + (c >> 2);
       const int hw = tr_swap<8>(8 * g + (c >> 2)), hl = tr_swap<kPairs>(8 * g + (c >> 2));
       uint4 vf[S::NT];
@@ -1552,10 +1558,9 @@ __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, un
 // dA, dB and, behind them, the last part of dx in one launch: the first `ia`
 // blocks make dA, the next `ib` dB.
 template <int RT>
-__global__ void __launch_bounds__(256) end_kernel(WgradArgs da, WgradArgs db, FinishArgs fin,
+__global__ void __launch_bounds__(256, 2) end_kernel(WgradArgs da, WgradArgs db, FinishArgs fin,
                                                   uint32_t ia, uint32_t ib) {
   __shared__ __attribute__((aligned(1024))) unsigned char lds[WgradShape<RT>::kLds];
-  static_assert(sizeof(lds) >= 32768, "finish_item uses as much");
   constexpr int KS = RT < 2 ? 1 : RT / 2;
   if (blockIdx.x < ia) wgrad_item<RT, false>(da, blockIdx.x, lds);
   else if (blockIdx.x < ia + ib) wgrad_item<RT, true>(db, blockIdx.x - ia, lds);

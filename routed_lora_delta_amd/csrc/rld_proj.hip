@@ -1726,6 +1726,15 @@ static LowArgs low_args(const rld_route* r, bool trans, const void* x, uint32_t 
   a.kc = p.kc;
   a.nch = p.nch;
   a.tiles = div_ceil(n, kLowRows);
+  // Unsorted rows: a tile's slots are items too, and up to four chunks make one where
+  // they come to some 200 all the same (16 slots of rank 16, us with chunks of 512
+  // against these: 256 rows 4096 -> 4096 29.3 and 27.1, 384 rows 39.4 and 36.4; of 4
+  // slots, which stay, 256 rows 4096 -> 1024 22.3, and 24.8 with two in one).
+  const uint64_t pieces = (uint64_t)a.tiles * a.nch * std::min(r->max_loras, kLowRows);
+  if (!order && n > kLowRows && a.kc == kLowChunk && pieces >= 2 * 192) {
+    a.kc *= (uint32_t)std::min<uint64_t>(4, pieces / 192);
+    a.nch = div_ceil(a.K, a.kc);
+  }
   // few items: the slots of a tile go to several blocks
   const uint32_t items = a.tiles * a.nch;
   a.nz = items >= 1024u ? 1u : div_ceil(1024u, items ? items : 1u);
@@ -1920,13 +1929,13 @@ extern "C" int rld_proj(const rld_route* route, const void* w, uint32_t w_row_st
     sort_kernel<<<route->max_loras + 1, 256, 0, st>>>(sort);
     if ((e = launch_status())) return e;
   }
+  const LowArgs l = low_args(route, false, x, x_row_stride, n, first ? sort.order_ : 0,
+                             first ? sort.skey_ : seq, 2, parts, partial);
   // finish adds up the low rows' chunks itself while they are few: each of its
   // tiles of 64 columns reads them (4096 -> 1024 at rank 16, itself against summed
   // first: 1237 rows, 10 MB read so, 35.7 us and 37.6; 2048 rows, 17 MB, 48.2 and 44.5)
-  const uint64_t again = (uint64_t)div_ceil(N, 64) * n * R * 4 * p.nch;
+  const uint64_t again = (uint64_t)div_ceil(N, 64) * n * R * 4 * l.nch;
   const bool sum = again > (12ull << 20);
-  const LowArgs l = low_args(route, false, x, x_row_stride, n, first ? sort.order_ : 0,
-                             first ? sort.skey_ : seq, 2, parts, partial);
   StartArgs s;
   s.part = part_args<false>(t, w, w_row_stride, x, x_row_stride, n, K, N, sums);
   s.u = l;
@@ -1943,7 +1952,7 @@ extern "C" int rld_proj(const rld_route* route, const void* w, uint32_t w_row_st
   }
   const FinishArgs f =
       finish_args(route, false, t, sums, sorted ? sort.order_ : 0, sorted ? sort.skey_ : seq,
-                  sum ? parts : 0, partial, p.nch, first, out, out_row_stride, n);
+                  sum ? parts : 0, partial, l.nch, first, out, out_row_stride, n);
   // 64 positions a block where the low rows are summed already (adding up their
   // chunks takes longer for more rows a wave: 17 us against 10 for 1237 rows)
   return sum ? launch_finish<4>(f, 64, st) : launch_finish<1>(f, 16, st);

@@ -1744,7 +1744,7 @@ static LowArgs low_args(const rld_route* r, bool trans, const void* x, uint32_t 
   // sorted rows: the slots of a tile, if they have equally many rows (192 shuffled
   // rows, us with at most two against these: 64 slots, 4096 -> 4096, 63 and 36; 200
   // slots, 4096 -> 1024, 99 and 37)
-  const uint32_t named = 1 + div_ceil(std::min(r->max_loras, n) * kLowRows, n);
+  const uint32_t named = n ? 1 + div_ceil(std::min(r->max_loras, n) * kLowRows, n) : 1u;
   if (order && a.nz > named) a.nz = named;
   return a;
 }

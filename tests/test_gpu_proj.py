@@ -559,3 +559,76 @@ def test_far_rows_of_large_tiles():
     far[:, k:] = NAN16
     c.dyd, c.os = far, wide
     c.check_grads()
+
+
+def smaller(bits, e):
+    """The values times 2^-e (zero where that is below the normal range)."""
+    return np.where((bits >> 7 & 0xFF) > e, bits - (e << 7), 0).astype(np.uint16)
+
+
+@pytest.mark.parametrize("n,k,m,r", [
+    (40, 72, 264, 16),       # finish adds up the chunks
+    (700, 72, 2312, 128),    # low rows summed before finish
+    (2304, 72, 4616, 16),    # large tiles
+])
+def test_low_rows_next_to_the_largest_number(n, k, m, r):
+    """Low rows that are finite in fp32 and would round to an infinity in BF16 (1.998
+    2^127: the largest BF16 is 1.9921875 2^127): the outputs that they give are
+    ordinary numbers, forward and in dx and dA.  (dB's u would underflow: not made.)"""
+    say(f"case: proj low rows next to the largest number {n} {k} {m} {r}")
+    c = Case(n, k, m, r, 2, seed=51)
+    rows = c.rows_of(1)
+    c.scale[1] = 1.998
+    c.x[rows, :k] = 0
+    c.x[rows, 0] = 0x7F00  # 2^127
+    c.w[:, 0] = 0
+    c.a[1, :r, 0] = 0
+    c.a[1, 0, 0] = 0x3F80  # 1
+    c.b[1, :m] = smaller(c.b[1, :m], 100)
+    c.sd.copy_(torch.from_numpy(c.scale))
+    for t, v in ((c.xd, c.x), (c.wd, c.w), (c.ad, c.a), (c.bd, c.b)):
+        t.copy_(up(v, c.dev))
+    c.check_proj()
+    c = Case(n, m, k, r, 2, seed=52)  # dx [n, m] from dy [n, k]
+    rows = c.rows_of(1)
+    c.scale[1] = 1.998
+    c.dy[rows, :k] = 0
+    c.dy[rows, 0] = 0x7F00
+    c.w[0, :m] = 0
+    c.b[1, 0] = 0
+    c.b[1, 0, 0] = 0x3F80
+    c.a[1, :r] = smaller(c.a[1, :r], 100)
+    c.x[rows, :m] = smaller(c.x[rows, :m], 100)
+    c.sd.copy_(torch.from_numpy(c.scale))
+    for t, v in ((c.xd, c.x), (c.dyd, c.dy), (c.wd, c.w), (c.ad, c.a), (c.bd, c.b)):
+        t.copy_(up(v, c.dev))
+    c.tables()
+    dx = c.out_rows(c.xs)
+    need = R.rld_proj_grad_workspace_bytes(n, m, k, r, 2)
+    R.check(c.call_grad(dx, c.scratch(need), db=False), "rld_proj_grad")
+    torch.cuda.synchronize()
+    rx, ra, _ = c.gradients()
+    c.check_rounded(bf16_values(c.body(dx, m, c.xs)), *rx, k, "dx")
+    c.check_grad(c.slot_gradients()[0], *ra, k, max(len(c.rows_of(s)) for s in range(2)), "dA")
+
+
+@pytest.mark.parametrize("n,k,m,r", [(40, 72, 264, 16), (2304, 72, 4616, 16)])
+def test_infinite_low_rows(n, k, m, r):
+    """An infinity in x makes every value of a low row infinite: the outputs are the
+    infinities and NaN of the formula, not NaN throughout."""
+    say(f"case: proj infinite low rows {n} {k} {m} {r}")
+    c = Case(n, k, m, r, 2, seed=53)
+    rows = c.rows_of(1)
+    c.x[rows, 0] = 0x7F80
+    c.a[1, :r, 0] &= 0x7FFF
+    c.b[1, :m // 2] &= 0x7FFF  # of one sign: no infinity meets its negative
+    for t, v in ((c.xd, c.x), (c.ad, c.a), (c.bd, c.b)):
+        t.copy_(up(v, c.dev))
+    with np.errstate(invalid="ignore"):
+        want = c.forward()
+        got = bf16_values(c.proj())
+    assert np.isposinf(want[0][rows]).any() and np.isnan(want[0][rows]).any()
+    assert not np.isfinite(want[0][rows]).any()
+    assert np.array_equal(got[rows], want[0][rows], equal_nan=True)
+    rest = np.setdiff1d(np.arange(n), rows)
+    c.check_rounded(got[rest], *(v[rest] for v in want), k, "out")

@@ -527,8 +527,8 @@ size_t rld_moe_router_workspace_bytes(uint32_t num_tokens, uint32_t num_experts,
  * indices -1 and NaN weights, counts in N and makes the loss NaN.
  * num_tokens == 0 writes zero counts, offsets and loss.
  * RLD_EINVAL on top_k 0 or above num_experts; RLD_EUNSUPPORTED on num_experts
- * above 1024, top_k above 32, num_tokens * top_k of 2^31 or num_tokens of 2^26
- * and more. */
+ * above 1024, top_k above 32, num_tokens * top_k of 2^31 and more, or num_tokens
+ * above 2^26 - 4. */
 int rld_moe_router(const void* logits, int logits_f32, uint32_t logits_row_stride,
                    const int32_t* token_mask, uint32_t num_tokens, uint32_t num_experts,
                    uint32_t top_k, int norm_topk, int32_t* indices, float* weights,

@@ -35,6 +35,7 @@ constexpr uint32_t kPlaceThreads = 1024;
 constexpr uint32_t kPlaceWaves = kPlaceThreads / 64;
 constexpr uint32_t kScanBlocks = 32;    // token blocks above which the scan is worth a launch
 constexpr uint32_t kMaxExperts = 1024;
+constexpr uint32_t kMaxTokens = (1u << 26) - 4;
 constexpr uint32_t kMaxTopK = 32;
 
 struct RouterArgs {
@@ -696,8 +697,8 @@ static int check_router(const void* logits, int f32, uint32_t ls, uint32_t T, ui
                         uint32_t k) {
   if (E == 0 || k == 0 || k > E) return RLD_EINVAL;
   if (E > kMaxExperts || k > kMaxTopK) return RLD_EUNSUPPORTED;
-  if ((uint64_t)T * k >= (1ull << 31) || (uint64_t)T * 64 >= (1ull << 32))
-    return RLD_EUNSUPPORTED;
+  // a grid holds fewer than 2^32 threads: at most 64 a token, in blocks of 256
+  if ((uint64_t)T * k >= (1ull << 31) || T > kMaxTokens) return RLD_EUNSUPPORTED;
   if (T == 0) return RLD_OK;
   if (!logits || ls < E) return RLD_EINVAL;
   if ((uintptr_t)logits & (f32 ? 3u : 1u)) return RLD_EALIGN;

@@ -169,3 +169,10 @@ def test_workspace_for_the_largest_call_does_for_every_smaller_one():
         now = R.rld_moe_router_workspace_bytes(t, 128, 8)
         assert now >= last, t
         last = now
+
+
+@pytest.mark.parametrize("tokens", [(1 << 26) - 3, (1 << 26) - 1])
+def test_router_refuses_tokens_whose_grid_would_pass_32_bits(tokens):
+    """At 64 lanes a token, in blocks of 256, they are 2^32 threads."""
+    assert _router_grad(T=tokens, E=512, ls=512, os=512) == R.RLD_EUNSUPPORTED
+    assert _router(T=tokens, E=512, ls=512, k=2) == R.RLD_EUNSUPPORTED

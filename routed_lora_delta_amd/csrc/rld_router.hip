@@ -9,8 +9,9 @@
 //
 // The choice compares logits, not probabilities, so that it is exact.  A group
 // of LPT lanes serves one token, VPT logits a lane, in registers from the load
-// to the last use.  Probabilities, weights and sums are fp32; all sums run in
-// a fixed order (per lane over its tokens, over the lanes and waves of a
+// to the last use.  Probabilities, weights and a block's sums of probabilities (at
+// most 23 additions) are fp32, the sums over the blocks are 64 bits wide; all sums
+// run in a fixed order (per lane over its tokens, over the lanes and waves of a
 // block, over the blocks), so results do not change from run to run.
 //
 // One launch for up to 64 tokens, two otherwise: route (choices, and per block
@@ -473,24 +474,24 @@ __global__ void __launch_bounds__(THREADS) route_kernel(RouterArgs a) {
 // 257 blocks and 128 experts, of latency.
 __global__ void __launch_bounds__(1024) router_scan_kernel(RouterArgs a) {
   __shared__ int run[64][16];
-  __shared__ float frun[64][16];
+  __shared__ double frun[64][16];  // fp32 would drift: up to 2^13 blocks a run
   const int l = threadIdx.x & 15, part = threadIdx.x >> 4;
   const uint32_t e = blockIdx.x * 16 + l, w = a.E + 1;
   const uint32_t per = (a.nblk + 63) / 64, b0 = min(part * per, a.nblk), b1 = min(b0 + per, a.nblk);
   RLD_GLOBAL int32_t* cnt = gp<int32_t>(a.cnt_);
   int n = 0;
-  float ps = 0.f;
+  double ps = 0.0;
 #pragma unroll 8
   for (uint32_t b = b0; b < b1; ++b) {
     n += e < w ? cnt[(uint64_t)b * w + e] : 0;
-    ps += e < a.E ? gp<const float>(a.psum_)[(uint64_t)b * a.E + e] : 0.f;
+    ps += (double)(e < a.E ? gp<const float>(a.psum_)[(uint64_t)b * a.E + e] : 0.f);
   }
   run[part][l] = n;
   frun[part][l] = ps;
   __syncthreads();
   if (e >= w) return;
   int at = 0, total = 0;
-  float ptotal = 0.f;
+  double ptotal = 0.0;
 #pragma unroll 16
   for (int i = 0; i < 64; ++i) {
     at += i < part ? run[i][l] : 0;
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(1024) router_scan_kernel(RouterArgs a) {
   }
   if (part == 0) {
     gp<int32_t>(a.total_)[e] = total;
-    if (e < a.E) gp<float>(a.ptotal_)[e] = ptotal;
+    if (e < a.E) gp<float>(a.ptotal_)[e] = (float)ptotal;  // one rounding
   }
 }
 
@@ -521,7 +522,7 @@ __global__ void __launch_bounds__(1024) router_scan_kernel(RouterArgs a) {
 __global__ void __launch_bounds__(kPlaceThreads) router_place_kernel(RouterArgs a) {
   __shared__ PlaceSmem sm;
   __shared__ int all[kMaxExperts + 1], early[kMaxExperts + 1];
-  __shared__ float ps[kPlaceThreads];
+  __shared__ double ps[kPlaceThreads];
   const uint32_t w = a.E + 1, blk = blockIdx.x;
   for (uint32_t e = threadIdx.x; e < w; e += kPlaceThreads) {
     all[e] = early[e] = 0;
@@ -538,7 +539,7 @@ __global__ void __launch_bounds__(kPlaceThreads) router_place_kernel(RouterArgs 
   } else {
     if (part < parts) {
       int n = 0, m = 0;
-      float p = 0.f;
+      double p = 0.0;
 #pragma unroll 16
       for (uint32_t b = part; b < a.nblk; b += parts) {
         const int c = cnt[(uint64_t)b * w + e1];
@@ -548,7 +549,7 @@ __global__ void __launch_bounds__(kPlaceThreads) router_place_kernel(RouterArgs 
       if (blk == 0) {
 #pragma unroll 16
         for (uint32_t b = part; b < a.nblk; b += parts)
-          p += gp<const float>(a.psum_)[(uint64_t)b * a.E + e1];
+          p += (double)gp<const float>(a.psum_)[(uint64_t)b * a.E + e1];
       }
       ps[threadIdx.x] = p;
       atomicAdd(&all[e1], n);  // whole numbers: any order gives the same sum
@@ -572,8 +573,8 @@ __global__ void __launch_bounds__(kPlaceThreads) router_place_kernel(RouterArgs 
   place_rows(
       a, blk, sm, [&](uint32_t e) { return all[e]; },
       [&](uint32_t e) {
-        if (a.scanned) return gp<const float>(a.ptotal_)[e];
-        float p = ps[e];
+        if (a.scanned) return (double)gp<const float>(a.ptotal_)[e];
+        double p = ps[e];
         for (uint32_t i = 1; i < parts; ++i) p += ps[i * a.E + e];
         return p;
       },

@@ -428,6 +428,34 @@ def test_same_bits_every_run_and_graph_replays():
                 assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("x", [0.5, 0.75, 1.25])
+def test_loss_of_very_many_tokens(x):
+    """2^22 equal tokens, one expert preferred by x: loss = E p.  An fp32 sum over the
+    32768 blocks of tokens would drift by 70 to 100 units (each addition rounds the
+    same way).  Bound: a probability's error, the at most 2 + 3 + 8 additions inside a
+    block and the roundings of the sum and the loss."""
+    say(f"case: router loss of very many tokens {x}")
+    dev = require_gpu()
+    T, E = 1 << 22, 8
+    row = np.zeros((1, E), np.float32)
+    row[0, 3] = x
+    logits = torch.from_numpy(row).to(dev).repeat(T, 1)
+    idx = torch.zeros((T, 1), dtype=torch.int32, device=dev)
+    w, loss = torch.zeros((T, 1), device=dev), torch.zeros(1, device=dev)
+    cnt = torch.zeros(E + 1, dtype=torch.int32, device=dev)
+    need = R.rld_moe_router_workspace_bytes(T, E, 1)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=dev)
+    R.check(R.rld_moe_router(logits, True, E, None, T, E, 1, False, idx, w, cnt, None, None, None,
+                             loss, ws, need), "rld_moe_router")
+    torch.cuda.synchronize()
+    want = np.zeros(E + 1, np.int64)
+    want[3] = want[E] = T
+    assert np.array_equal(cnt.cpu().numpy(), want) and bool((idx == 3).all())
+    p = np.exp(x) / (np.exp(x) + E - 1)
+    tol = rel_p(row.astype(np.float64))[0, 0] + 15 * U
+    assert abs(float(loss[0]) / (E * p) - 1) <= tol
+
+
 # ------------------------------------------------------ used together ----
 
 def test_router_tables_drive_the_grouped_fold():

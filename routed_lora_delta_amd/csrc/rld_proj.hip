@@ -231,7 +231,7 @@ __device__ __forceinline__ void dma16(const rsrc_t& r, uint32_t to, uint32_t vof
       "buffer_load_dwordx4 %1, %2, %3 offen lds"
       :
       : "s"(to), "v"(voff), "s"(r), "s"(soff)
-      : "memory");
+      : "m0", "memory");
 }
 
 // The same from a 64-bit address of each lane.
@@ -242,7 +242,7 @@ __device__ __forceinline__ void dma16(uint64_t from, uint32_t to) {
       "global_load_lds_dwordx4 %1, off"
       :
       : "s"(to), "v"(from)
-      : "memory");
+      : "m0", "memory");
 }
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {

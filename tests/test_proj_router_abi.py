@@ -1,6 +1,10 @@
 """rld_proj, rld_proj_grad, rld_moe_router and rld_moe_router_grad on the CPU: the
 refusals, each before any launch, and the workspace sizes.  Every call here fails
 validation or is an empty batch that launches nothing."""
+import glob
+import os
+import re
+
 import pytest
 
 import routed_lora_delta_amd as R
@@ -176,3 +180,16 @@ def test_router_refuses_tokens_whose_grid_would_pass_32_bits(tokens):
     """At 64 lanes a token, in blocks of 256, they are 2^32 threads."""
     assert _router_grad(T=tokens, E=512, ls=512, os=512) == R.RLD_EUNSUPPORTED
     assert _router(T=tokens, E=512, ls=512, k=2) == R.RLD_EUNSUPPORTED
+
+
+def test_inline_assembly_declares_m0():
+    """A statement that writes m0 says so: the compiler may hold a value there."""
+    csrc = os.path.join(os.path.dirname(R.library_path()), "csrc")
+    found = 0
+    for path in glob.glob(os.path.join(csrc, "*.h*")):
+        with open(path) as f:
+            for stmt in re.findall(r"\basm\b[^;]*;", f.read()):
+                if re.search(r"s_mov_b32 m0\b", stmt):
+                    found += 1
+                    assert '"m0"' in stmt.rsplit(":", 1)[1], (path, stmt)
+    assert found

@@ -50,33 +50,25 @@ __device__ uint4 g_zero16[1];
 
 // ------------------------------------------------------------- bf16 parts ----
 
-// Two values' next bf16 parts; a and b are left with what remains of them.  Rounding
-// to nearest makes the remainder exact in fp32 (it fits the 24 - 8 bits left).  A
-// finite value that would round to infinity (above 1.996 2^127) is cut to the largest
-// bf16 instead, and of an infinity nothing remains: one less another would be a NaN.
-__device__ __forceinline__ uint32_t bf16_part(float& a, float& b) {
-  uint32_t w = pack_bf16x2(a, b);
-  if ((w & 0x7f80u) == 0x7f80u && a == a) w = (w & 0xffff0000u) | __float_as_uint(a) >> 16;
-  if ((w & 0x7f800000u) == 0x7f800000u && b == b)
-    w = (w & 0xffffu) | (__float_as_uint(b) & 0xffff0000u);
-  const float pa = bf16_to_f32(w & 0xffffu), pb = bf16_to_f32(w >> 16);
-  a = a == pa ? 0.f : a - pa;
-  b = b == pb ? 0.f : b - pb;
-  return w;
+// v as the sum of two bf16 values, the larger first, to 2^-17.  Rounding to nearest
+// makes the remainder exact in fp32 (it fits the 24 - 8 bits left).  The first part is
+// kept finite (a value above 1.996 2^127 would round to infinity, and one infinity
+// less another is a NaN); an infinity is the second part.
+__device__ __forceinline__ float first_part(float v) {
+  const float top = __uint_as_float(0x7f7f0000u);  // the largest bf16
+  return __builtin_amdgcn_fmed3f(v, -top, top);
 }
 
-// v as the sum of two bf16 values, the larger first, to 2^-17.
 __device__ __forceinline__ void bf16_parts(const float (&v)[8], uint4 (&out)[2]) {
-  float r[8];
+  uint32_t w[4], r[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) r[e] = v[e];
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = bf16_part(r[2 * e], r[2 * e + 1]);
-    out[p] = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int e = 0; e < 4; ++e) {
+    w[e] = pack_bf16x2(first_part(v[2 * e]), first_part(v[2 * e + 1]));
+    r[e] = pack_bf16x2(v[2 * e] - bf16_to_f32(w[e] & 0xffffu),
+                       v[2 * e + 1] - bf16_to_f32(w[e] >> 16));
   }
+  out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  out[1] = make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // ------------------------------------------------------------------- sort ----
@@ -327,10 +319,15 @@ __device__ __forceinline__ void store_low(const LowArgs& a, uint32_t from, uint3
   uint2v part[3];
 #pragma unroll
   for (int p = 0; p < 3; ++p) {
-    float r[4] = {v[0], v[1], v[2], v[3]};
-    part[p].x = bf16_part(r[0], r[1]);
-    part[p].y = bf16_part(r[2], r[3]);
-    v = floatx4{r[0], r[1], r[2], r[3]};
+    const floatx4 f = p ? v
+                        : floatx4{first_part(v[0]), first_part(v[1]), first_part(v[2]),
+                                  first_part(v[3])};
+    part[p] = uint2v{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])};
+    const floatx4 is = {bf16_to_f32(part[p].x & 0xffffu), bf16_to_f32(part[p].x >> 16),
+                        bf16_to_f32(part[p].y & 0xffffu), bf16_to_f32(part[p].y >> 16)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // of an infinite second part nothing remains
+      v[i] = p == 1 && v[i] == is[i] ? 0.f : v[i] - is[i];
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {

@@ -474,7 +474,8 @@ __global__ void __launch_bounds__(THREADS) route_kernel(RouterArgs a) {
 // 257 blocks and 128 experts, of latency.
 __global__ void __launch_bounds__(1024) router_scan_kernel(RouterArgs a) {
   __shared__ int run[64][16];
-  __shared__ double frun[64][16];  // fp32 would drift: up to 2^13 blocks a run
+  __shared__ double fsum[16][16];  // of a wave's four runs (fp32 would drift: a run may
+                                   // have 2^13 blocks)
   const int l = threadIdx.x & 15, part = threadIdx.x >> 4;
   const uint32_t e = blockIdx.x * 16 + l, w = a.E + 1;
   const uint32_t per = (a.nblk + 63) / 64, b0 = min(part * per, a.nblk), b1 = min(b0 + per, a.nblk);
@@ -487,16 +488,16 @@ __global__ void __launch_bounds__(1024) router_scan_kernel(RouterArgs a) {
     ps += (double)(e < a.E ? gp<const float>(a.psum_)[(uint64_t)b * a.E + e] : 0.f);
   }
   run[part][l] = n;
-  frun[part][l] = ps;
+#pragma unroll
+  for (int o = 16; o < 64; o <<= 1) ps += __shfl_xor(ps, o);
+  if ((part & 3) == 0) fsum[part >> 2][l] = ps;
   __syncthreads();
   if (e >= w) return;
   int at = 0, total = 0;
-  double ptotal = 0.0;
 #pragma unroll 16
   for (int i = 0; i < 64; ++i) {
     at += i < part ? run[i][l] : 0;
     total += run[i][l];
-    ptotal += frun[i][l];
   }
   for (uint32_t b = b0; b < b1; b += 8) {
     int c[8];
@@ -511,6 +512,9 @@ __global__ void __launch_bounds__(1024) router_scan_kernel(RouterArgs a) {
   }
   if (part == 0) {
     gp<int32_t>(a.total_)[e] = total;
+    double ptotal = 0.0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) ptotal += fsum[i][l];
     if (e < a.E) gp<float>(a.ptotal_)[e] = (float)ptotal;  // one rounding
   }
 }

@@ -195,6 +195,17 @@ __device__ __forceinline__ void wait_vm() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// The block meets: every wave's LDS reads so far have their data, so what they read may
+// be loaded over behind this, and of its loads from memory at most N are in flight.
+// (The barrier itself waits for nothing, and the compiler may leave a wait for an LDS
+// read, with the matrix instruction that needs it, behind the barrier.)
+template <int N>
+__device__ __forceinline__ void meet() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 typedef int rsrc_t __attribute__((ext_vector_type(4)));
 
 // The size of the largest buffer, and so an offset behind every buffer.
@@ -471,9 +482,7 @@ __device__ __forceinline__ void low_item(const LowArgs& a, uint32_t item, unsign
 #pragma unroll
       for (int t = 0; t < kLowStages - 1; ++t) issue(t);
       for (uint32_t t = 0; t < nk; ++t) {
-        wait_vm<(kLowStages - 2) * 4>();
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
+        meet<(kLowStages - 2) * 4>();
         issue(t + kLowStages - 1);
         const uint32_t st = lds0 + (t % kLowStages) * 16384;
 #pragma unroll
@@ -499,9 +508,7 @@ __device__ __forceinline__ void low_item(const LowArgs& a, uint32_t item, unsign
               acc[j][i] = mfma_bf16_16x16x32(mf[j], xf[i], acc[j][i]);
         }
       }
-      wait_vm<0>();  // the loads past the end, of zeros
-      __builtin_amdgcn_s_barrier();  // everyone has read: the places may be loaded again
-      asm volatile("" ::: "memory");
+      meet<0>();  // the loads past the end too, of zeros: the places may be loaded again
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t r = wr * 32 + i * 16 + c;
@@ -754,9 +761,7 @@ __device__ __forceinline__ void part_item(const PartArgs& a, uint32_t item, unsi
   for (int t = 0; t < STAGES - 1; ++t) issue(t);
 
   for (uint32_t kt = 0; kt < nk; ++kt) {
-    wait_vm<(STAGES - 2) * PL>();
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    meet<(STAGES - 2) * PL>();
     issue(kt + STAGES - 1);
     const uint32_t st = lds0 + (kt % STAGES) * kStageB;
 #pragma unroll
@@ -950,9 +955,7 @@ __device__ __forceinline__ void finish_item(const FinishArgs& a, uint32_t item,
         }
       }
       if constexpr (TRANS) {
-        wait_vm<0>();
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
+        meet<0>();
       }
 #pragma unroll
       for (int b = 0; b < SB; ++b) {
@@ -978,8 +981,7 @@ __device__ __forceinline__ void finish_item(const FinishArgs& a, uint32_t item,
         }
       }
       if constexpr (TRANS) {
-        __builtin_amdgcn_s_barrier();  // everyone has read: the next slots may come
-        asm volatile("" ::: "memory");
+        meet<0>();  // the next slots may come
       }
     }
   }
@@ -1213,7 +1215,7 @@ __device__ __forceinline__ void big_tile_body(const TileArgs& a) {
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(1);
   };
-  auto meet = [&]() {
+  auto next_phase = [&]() {
     __builtin_amdgcn_s_setprio(0);
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_barrier();
@@ -1228,22 +1230,22 @@ __device__ __forceinline__ void big_tile_body(const TileArgs& a) {
     LAST ? load_e(0, e0, 0, buf) : load_w(0, t + 2, buf);
     settle();
     multiply(0, 0, w0);
-    meet();
+    next_phase();
     read_w(1, buf, wf[1]);
     LAST ? load_low(0, buf, 0, buf) : load_x(0, t + 2, buf);
     settle();
     multiply(0, 1, wf[1]);
-    meet();
+    next_phase();
     read_x(1, buf);
     LAST ? load_e(1, e0, 0, buf) : load_w(1, t + 2, buf);
     settle();
     multiply(1, 1, wf[1]);
-    meet();
+    next_phase();
     read_w(0, buf ^ 1, w0next);
     LAST ? load_low(1, buf, 0, buf) : load_x(1, t + 2, buf);
     settle();
     multiply(1, 0, w0);
-    meet();
+    next_phase();
   };
 
   if (steps) {
@@ -1321,18 +1323,12 @@ __device__ __forceinline__ void big_tile_body(const TileArgs& a) {
     for (int j = 0; j < 4; ++j) left[j] = left[j] == s ? -1 : left[j];
     return s;
   };
-  auto landed = [&]() {  // this wave's loads, then everyone's
-    wait_vm<0>();
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-  };
   for (uint32_t k0 = 0; k0 < a.R; k0 += 64) {
     all_rows();
     int s = next_slot();
     if (s < 0) break;
     if (k0 != 0) {
-      __builtin_amdgcn_s_barrier();  // everyone has read what is overwritten
-      asm volatile("" ::: "memory");
+      meet<0>();  // everyone has read what is overwritten
 #pragma unroll
       for (int lo = 0; lo < 2; ++lo) {
         load_low(0, lo, k0, lo);
@@ -1341,11 +1337,11 @@ __device__ __forceinline__ void big_tile_body(const TileArgs& a) {
     }
     if (k0 != 0 || s != slot0) {  // not loaded behind K
       const uint64_t e = uniform64(gp<const uint64_t>(a.etab_)[s]);
-      if (k0 == 0) landed();  // what was loaded there has landed
+      if (k0 == 0) meet<0>();  // what was loaded there has landed
       load_e(0, e, k0, 0);
       load_e(1, e, k0, 0);
     }
-    landed();
+    meet<0>();
     for (int buf = 0; s >= 0; buf ^= 1) {
       const int following = next_slot();
       if (following >= 0) {
@@ -1389,7 +1385,7 @@ __device__ __forceinline__ void big_tile_body(const TileArgs& a) {
         }
       }
       s = following;
-      landed();
+      meet<0>();
     }
   }
   wait_vm<0>();
@@ -1517,9 +1513,7 @@ __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, un
   issue(0);
   rows_of(S::kStep);
   for (uint32_t i0 = 0; i0 < cnt; i0 += S::kStep) {
-    wait_vm<0>();
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    meet<0>();
     issue(i0 + S::kStep);
     rows_of(i0 + 2 * S::kStep);
     const uint32_t st = lds0 + (i0 / S::kStep & 1) * S::kStage;

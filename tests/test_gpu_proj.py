@@ -632,3 +632,53 @@ def test_infinite_low_rows(n, k, m, r):
     assert np.array_equal(got[rows], want[0][rows], equal_nan=True)
     rest = np.setdiff1d(np.arange(n), rows)
     c.check_rounded(got[rest], *(v[rest] for v in want), k, "out")
+
+
+@pytest.mark.parametrize("n,k,m,r,slots,layout", [
+    (2400, 128, 4104, 8, 2, "runs"),      # two steps
+    (2500, 256, 4360, 16, 3, "runs"),     # four
+    (2100, 264, 4872, 40, 6, "mixed"),    # four and an eighth
+    (2600, 1024, 4104, 64, 4, "runs"),    # 16, the low rows in two chunks
+    (2300, 1096, 4104, 128, 3, "mixed"),  # 17 and an eighth, three chunks
+    (2304, 4096, 4104, 64, 4, "runs"),    # 64, eight chunks
+    (4100, 40, 2568, 16, 3, "mixed"),     # no whole step
+])
+def test_many_tiles_of_every_depth(n, k, m, r, slots, layout):
+    """Large tiles of even and odd numbers of steps with and without a tail, and of
+    low rows that are summed from chunks before, in both directions."""
+    say(f"case: proj many tiles of every depth {n} {k} {m} {r} {layout}")
+    Case(n, k, m, r, slots, layout, 8, 16, 8, seed=61).check_proj()
+    Case(n, m, k, r, slots, layout, 8, 16, 8, seed=62).check_grads()
+
+
+def test_far_rows_of_large_tiles_in_chunks():
+    """Rows in their own order (too far for 32-bit offsets), low rows of three chunks."""
+    say("case: proj far rows, large tiles, chunks")
+    n, k, m, r = 2060, 1032, 4616, 24
+    wide = 1 << 18
+    assert n * wide * 2 > 1 << 30
+    c = Case(n, k, m, r, 5, "mixed", seed=63)
+    far = torch.full((n, wide), NAN16, dtype=torch.int16, device=c.dev)
+    far[:, :k] = c.xd[:, :k]
+    c.xd, c.xs = far, wide
+    c.check_proj()
+    c = Case(n, m, k, r, 5, "mixed", seed=64)
+    far[:, :k] = c.dyd[:, :k]
+    far[:, k:] = NAN16
+    c.dyd, c.os = far, wide
+    c.check_grads()
+
+
+@pytest.mark.parametrize("n,k,m,r,slots", [
+    # sorted first, low rows summed before finish: ranks up to 32, 64, 128
+    (1030, 4104, 1000, 24, 16), (1030, 4104, 1032, 64, 16), (700, 2056, 1032, 128, 24),
+    # sorted first, finish adds up the chunks
+    (1030, 4104, 520, 16, 16),
+    # sorted beside the product, summed before finish: ranks up to 32, 128
+    (1100, 1032, 2056, 32, 4), (900, 520, 2056, 128, 4),
+])
+@pytest.mark.parametrize("layout", ["mixed", "runs"])
+def test_proj_of_many_slots_and_rows(n, k, m, r, slots, layout):
+    """Every way that the low rows of a split product take."""
+    say(f"case: proj of many slots and rows {n} {k} {m} {r} {slots} {layout}")
+    Case(n, k, m, r, slots, layout, 8, 0, 8, seed=65).check_proj()

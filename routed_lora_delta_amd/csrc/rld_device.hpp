@@ -73,10 +73,6 @@ __device__ __forceinline__ void store16(RLD_GLOBAL uint16_t* p, const uint4& v) 
   *reinterpret_cast<RLD_GLOBAL u32x4*>(p) = w;
 }
 
-__device__ __forceinline__ uint32_t div_ceil_dev(uint32_t a, uint32_t b) {
-  return a / b + (a % b != 0u ? 1u : 0u);
-}
-
 __device__ __forceinline__ uint4 zero16() { return make_uint4(0u, 0u, 0u, 0u); }
 
 // Compiler-level memory barrier: the loads written before it are issued

@@ -457,8 +457,8 @@ size_t rld_proj_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t n_out, uint3
  *            must not overlap w or x
  * n == 0 is a no-op.  RLD_EUNSUPPORTED for row strides above 2^21,
  * n above 2^26, k_in or n_out above 2^21, and from 2^23 tiles of 64 rows by 64
- * columns (of k_in or n_out, the wider), 2^21 pairs of a slot and 64 columns, or
- * n * max_rank of 2^32 on.
+ * columns (of k_in or n_out, the wider), 2^21 pairs of a slot and 64 columns,
+ * n * max_rank of 2^32 or n * max_loras of 2^38 on.
  * Results do not change from run to run; a row's summation order may depend on
  * n (the tile shape does). */
 int rld_proj(const rld_route* route, const void* w, uint32_t w_row_stride, const void* x,

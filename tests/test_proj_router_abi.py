@@ -193,3 +193,12 @@ def test_inline_assembly_declares_m0():
                     found += 1
                     assert '"m0"' in stmt.rsplit(":", 1)[1], (path, stmt)
     assert found
+
+
+def test_sorts_of_minutes_are_refused():
+    """The sort by slot reads n ids for each of max_loras slots."""
+    wide = dict(k_in=64, n_out=64)
+    many = _route(max_loras=1 << 20, **wide)
+    assert _proj(many, n=1 << 18, os=64) == R.RLD_EUNSUPPORTED
+    assert _grad(many, n=1 << 18, dys=64) == R.RLD_EUNSUPPORTED
+    assert _proj(many, n=(1 << 18) - 1, os=64, wb=64) == R.RLD_ENOSPACE  # the next check

@@ -445,10 +445,13 @@ size_t rld_proj_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t n_out, uint3
 
 /* The shared projection with each row's adapter, in one output rounding:
  *   out_i = bf16(x_i W^T + scale_s (x_i A_s^T) B_s^T),  s = seq_slot[i],
- * and out_i = bf16(x_i W^T) for base rows.  Products and sums are fp32 (the
- * low-rank row stays fp32; it is not rounded to BF16 as the folds above round
- * xa and delta, so results differ from a projection followed by rld_bgmv by
- * those roundings).  Overwrites out; unlike the folds it writes base rows.
+ * and out_i = bf16(x_i W^T) for base rows.  Products and sums are fp32.  The
+ * low-rank row is summed and scaled in fp32 and enters its second product as
+ * the sum of two BF16 values, which leaves out at most 2^-17 of it (the folds
+ * above round xa and delta to one BF16 each, so results differ from a
+ * projection followed by rld_bgmv by those roundings).  An infinity in B_s may
+ * make an output NaN where the formula has an infinity.  Overwrites out; unlike
+ * the folds it writes base rows.
  *   w        device BF16 [n_out, k_in] row-major, row j at w + j*w_row_stride
  *   x        device BF16, row i at x + i*x_row_stride, k_in elements read
  *   seq_slot device int32 [n]; contents may change between calls
@@ -460,7 +463,9 @@ size_t rld_proj_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t n_out, uint3
  * columns (of k_in or n_out, the wider), 2^21 pairs of a slot and 64 columns,
  * n * max_rank of 2^32 or n * max_loras of 2^38 on.
  * Results do not change from run to run; a row's summation order may depend on
- * n (the tile shape does). */
+ * n (the tile shape does).  max_loras should be the pool's slots, not a bound on
+ * them: more than 64 rows (in rld_proj_grad, any) are sorted by slot, by reading n
+ * ids for each slot, some 3 10^11 a second. */
 int rld_proj(const rld_route* route, const void* w, uint32_t w_row_stride, const void* x,
              uint32_t x_row_stride, const int32_t* seq_slot, uint32_t n, void* out,
              uint32_t out_row_stride, void* workspace, size_t workspace_bytes, void* stream);
@@ -472,7 +477,10 @@ size_t rld_proj_grad_workspace_bytes(uint32_t n, uint32_t k_in, uint32_t n_out,
                                      uint32_t max_rank, uint32_t max_loras);
 
 /* Gradient of rld_proj with W frozen.  With u_i = scale_s x_i A_s^T and
- * g_i = scale_s dy_i B_s (fp32):
+ * g_i = scale_s dy_i B_s (fp32 sums; in dx g enters as the sum of two BF16 values
+ * as above, in dA and dB g and u as the sum of three, all of their 24 bits; an
+ * infinity in A_s, x or dy may make a result NaN where the formula has an
+ * infinity):
  *   dx_i = bf16(dy_i W + g_i A_s)                          (base rows: dy_i W)
  *   dA_s = sum of g_i^T x_i, dB_s = sum of dy_i^T u_i over the rows i of slot s
  *   dy       device BF16, row i at dy + i*dy_row_stride, n_out elements read
@@ -520,7 +528,11 @@ size_t rld_moe_router_workspace_bytes(uint32_t num_tokens, uint32_t num_experts,
  *            indices; -1 from expert_offsets[num_experts] on; or NULL
  *   loss     fp32 [1]: num_experts / (top_k N^2) * sum_e counts[e] * sum_t p_te
  *            with N = counts[num_experts], 1 for an even load, 0 if N is 0; or
- *            NULL
+ *            NULL.  (Where a model's loss is not divided by top_k, its
+ *            coefficient times top_k belongs to this one.)
+ * A probability is exp(l - max) times the reciprocal of the sum, in fp32, the
+ * exponential to about 2 units: within some 10^-7 of the softmax, and not the bits
+ * of a division.
  * An expert whose logit is -Inf is never chosen; places left over hold index -1
  * and weight 0.  A token that is masked, or whose logits are all -Inf, is empty:
  * indices -1, weights 0, in no count.  A token with a NaN or +Inf logit gets
@@ -537,7 +549,8 @@ int rld_moe_router(const void* logits, int logits_f32, uint32_t logits_row_strid
                    void* stream);
 
 /* Gradient of rld_moe_router to the logits, from its indices and counts:
- *   dweights fp32 [num_tokens, top_k], the gradient of weights; NULL: none
+ *   dweights fp32 [num_tokens, top_k], the gradient of weights (the combine is
+ *            the caller's, and so is its gradient); NULL: none
  *            (indices may then be NULL); entries at index -1 are not read into it
  *   dloss    fp32 [1] on the device, the gradient of loss; NULL: none (counts
  *            may then be NULL).  The counts themselves have no gradient

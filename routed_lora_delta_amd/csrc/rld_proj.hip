@@ -679,7 +679,8 @@ struct PartArgs {
 // The product is computed transposed (W as the first operand), so a lane
 // holds four consecutive output columns of one row.
 // Bound by reading W where rows are few (64 rows 4096 -> 4096 with their low rows in
-// 9.5 us, 36 MB at 3.8 TB/s; 256 rows 4096 -> 12288 in 43 us, 143 MB at 3.3), else by
+// 9.5 us, 36 MB at 3.8 TB/s; 256 rows 4096 -> 12288 in 43.4 us, 144 MB of W, 31 slots' A,
+// x and the sums at 3.3 TB/s, of which the counters see 190 MB, 4.4 TB/s), else by
 // how far the two blocks of a CU overlap their LDS and matrix work: 1792 rows 4096 ->
 // 4096 in 67 us, 900 TFLOP/s, and no faster where all loads hit the cache; 450 with
 // one block a CU (1237 rows 4096 -> 1024 in 23 us).  Three stages, so one block a CU,
@@ -1040,8 +1041,8 @@ __global__ void __launch_bounds__(256, 2) start_kernel(StartArgs a) {
 // of either): while one half multiplies, the other reads.
 //
 // Bound by the matrix cores' rate under these loads: 4096 x 12288 x 4096 with 64
-// ranks of low rows 330-340 us, 1.23 PFLOP/s (a library's product alone: 318-322);
-// dy W 325-345.  The whole call took 495 us with 128 x 128 tiles of four waves, now 347.
+// ranks of low rows 310-340 us, 1.23 PFLOP/s (a library's product without them: 270);
+// dy W 320-345 (310).  The whole call took 495 us with 128 x 128 tiles of four waves, now 345.
 //
 // What makes it safe.  Every phase is
 //   reads, loads, wait (reads done; all but 12 loads landed), barrier,
@@ -1434,8 +1435,8 @@ struct WgradShape {
 // hold all 24 bits.  DB: the result is [col][R] instead of [R][col].  With few
 // slots and columns the positions are split as well (wgrad_splits).
 // Bound by the latency of a step's loads beside three times the matrix work: 4096
-// rows in four slots, 12288 and 4096 columns, rank 64, 56 us, 134 MB at 2.4 TB/s and
-// 460 TFLOP/s of bf16 parts.  (Rows' numbers in scalar registers, which spares waits,
+// rows in four slots, 12288 and 4096 columns, rank 64, 55 to 60 us, 134 MB at 2.3 TB/s
+// and 440 TFLOP/s of bf16 parts.  (Rows' numbers in scalar registers, which spares waits,
 // or a third stage in one block a CU: 15% longer.)
 template <int RT, bool DB>
 __device__ __forceinline__ void wgrad_item(const WgradArgs& a, uint32_t item, unsigned char* lds) {

@@ -255,6 +255,43 @@ def test_every_width_of_the_choice(E, k, f32):
     Router(l, f32).check(k, True)
 
 
+@pytest.mark.parametrize("f32", [False, True], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("T,E,k", [(1, 513, 1), (1, 1024, 32), (64, 1024, 32), (63, 1000, 9),
+                                   (64, 400, 8)])
+def test_one_block_of_many_experts(T, E, k, f32):
+    """Batches of one launch at the widest tables, and their gradients."""
+    say(f"case: router one block {T} {E} {k} f32={f32}")
+    rng = np.random.default_rng(E + T)
+    Router(logits_of(rng, T, E), f32).check_grad(k, True)
+
+
+def test_gradient_in_place_bf16():
+    rng = np.random.default_rng(18)
+    l = logits_of(rng, 90, 257)
+    a = Router(l, False, pad=3).check_grad(8, False)
+    b = Router(l, False, pad=3).check_grad(8, False, in_place=True)
+    assert np.array_equal(a, b)
+
+
+def test_two_routers_at_once():
+    """Two batches on two streams, each with its own tables and workspace: the tables
+    of the same calls one after the other."""
+    rng = np.random.default_rng(19)
+    runs = [Router(logits_of(rng, 5000, 128), True), Router(logits_of(rng, 300, 64), False)]
+    want = [r.check(k, True)[0] for r, k in zip(runs, (8, 4))]
+    streams = [torch.cuda.Stream() for _ in runs]
+    for r, k in zip(runs, (8, 4)):
+        r.buffers(k)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for r, s in zip(runs, streams):
+            with torch.cuda.stream(s):
+                R.check(r.launch(True), "rld_moe_router")
+    for r, w in zip(runs, want):
+        for key, got in r.results().items():
+            assert np.array_equal(got, w[key]), key
+
+
 @pytest.mark.parametrize("T", [64, 65, 128, 1025, 8192, 8193, 16385])
 def test_batches_around_the_blocks_of_tokens(T):
     """Where the blocks become larger, or one more: the tables are those of the

@@ -113,6 +113,34 @@ typedef struct rld_adapter_entry {
   int32_t use_rslora; /* nonzero: scale = alpha/sqrt(rank); else alpha/rank      */
 } rld_adapter_entry;
 
+/* One gradient of a list: count elements, contiguous, fp32 or BF16. */
+typedef struct rld_grad_entry {
+  uint64_t addr;     /* device address, 16-byte aligned; may be 0 if count is 0       */
+  uint64_t out_addr; /* where the clipped gradient goes, 16-byte aligned; 0: in place */
+  uint64_t count;    /* elements, any number                                          */
+  uint32_t group;    /* whose norm it counts in (an adapter slot), < num_groups       */
+  int32_t bf16;      /* nonzero: BF16; else fp32                                      */
+} rld_grad_entry;
+
+/* A piece of a gradient, as rld_grad_pack leaves it. */
+typedef struct rld_grad_chunk {
+  uint64_t addr;
+  uint64_t out_addr;
+  uint32_t count; /* elements, at most 8192 bytes of them */
+  uint32_t group;
+  uint32_t bf16;
+  uint32_t zero;
+} rld_grad_chunk;
+
+/* A packed list of gradients: device arrays that the caller uploads once, as
+ * long as the gradients keep their addresses. */
+typedef struct rld_grad_list {
+  const rld_grad_chunk* chunks; /* device [num_chunks], 16-byte aligned */
+  const uint32_t* group_starts; /* device [num_groups + 1]              */
+  uint32_t num_chunks;
+  uint32_t num_groups;
+} rld_grad_list;
+
 /* ---------------------------------------------------------------- host ---- */
 
 /* LoraPair scale (lora_delta.rs, LoraPair doc comment): alpha/rank, or
@@ -179,6 +207,19 @@ uint32_t rld_gather_row_token(uint32_t row, uint32_t top_k);
  * arguments, so a captured graph's shape is fixed.  (The shapes are this
  * library's own, not the page's 4-outputs-per-block grids.) */
 int rld_gather_grids(uint32_t max_rank, uint32_t n_out, uint32_t n_rows, uint32_t out[12]);
+
+/* *num_chunks = the chunks of these gradients.  RLD_EUNSUPPORTED above 2^30. */
+int rld_grad_chunks(const rld_grad_entry* entries, size_t n_entries, uint32_t* num_chunks);
+
+/* The list that rld_grad_norm and rld_grad_clip take, in host arrays for the
+ * caller to upload: chunks (rld_grad_chunks of them), the groups' in ascending
+ * order and a group's in the order of its entries, and group_starts
+ * [num_groups + 1], each group's first chunk.  RLD_EINVAL on a group >=
+ * num_groups, num_groups 0, or address 0 with a count; RLD_EALIGN on an address
+ * that is not 16-byte aligned; RLD_ENOSPACE on more than max_chunks;
+ * RLD_EUNSUPPORTED on more than 2^20 groups or 2^30 chunks. */
+int rld_grad_pack(const rld_grad_entry* entries, size_t n_entries, uint32_t num_groups,
+                  rld_grad_chunk* chunks, uint32_t max_chunks, uint32_t* group_starts);
 
 /* -------------------------------------------------------------- device ---- */
 
@@ -563,6 +604,101 @@ int rld_moe_router_grad(const void* logits, int logits_f32, uint32_t logits_row_
                         uint32_t top_k, int norm_topk, const int32_t* indices,
                         const int32_t* counts, const float* dweights, const float* dloss,
                         void* dlogits, uint32_t dlogits_row_stride, void* stream);
+
+/* MoE token movement.  A flat row f = t*top_k + j is choice j of token t.  In
+ * the four calls below
+ *   rows_f32     nonzero: rows, x, out and their gradients are fp32; else BF16
+ *   width        elements of a row, a multiple of 8 as are the row strides
+ *   sorted_rows  int32 [num_tokens * top_k], rld_moe_router's: the flat row of each
+ *                expert-sorted row.  Entries outside [0, num_tokens * top_k) (the
+ *                router's -1) name none; no flat row may be named twice
+ *   places       int32 [num_tokens * top_k], rld_moe_dispatch's: the sorted row of
+ *                each flat row
+ * Row p belongs to flat row f if places[f] is p and sorted_rows[p] is f.  An entry
+ * of places that the dispatch did not write may hold anything: it finds no row.
+ * RLD_EINVAL on top_k or width 0; RLD_EUNSUPPORTED on top_k above 32,
+ * num_tokens * top_k of 2^31 and more, num_tokens of 2^24 - 1 and more, or from
+ * 2^26 - 3 pieces of 4 KB (dispatch) or 1 KB on.  num_tokens == 0 is a no-op.
+ *
+ * rld_moe_dispatch: tokens to the experts' order,
+ *   rows[p] = x[f / top_k], places[f] = p  for every sorted row p that names f.
+ *   x        device, row t at x + t*x_row_stride
+ *   rows     device [num_tokens * top_k] rows; rows that name no flat row, and what
+ *            lies behind width in each, are left as they were.  Must not overlap x
+ *   places   entries of flat rows that are not named are left as they were
+ * A flat row that is named twice against the rule is copied twice, and places holds
+ * one of the two. */
+int rld_moe_dispatch(const void* x, int rows_f32, uint32_t x_row_stride, uint32_t num_tokens,
+                     uint32_t top_k, uint32_t width, const int32_t* sorted_rows, void* rows,
+                     uint32_t rows_row_stride, int32_t* places, void* stream);
+
+/* Gradient of rld_moe_dispatch: dx[t] = add[t] + sum_j drows[p], p the row of
+ * (t, j), over the choices that have one: fp32, add first and j ascending, rounded
+ * once.
+ *   add      device, row t at add + t*add_row_stride; NULL: zeros.  May be dx, at
+ *            its stride
+ *   dx       must not overlap drows */
+int rld_moe_dispatch_grad(const void* drows, int rows_f32, uint32_t drows_row_stride,
+                          const int32_t* sorted_rows, const int32_t* places, uint32_t num_tokens,
+                          uint32_t top_k, uint32_t width, const void* add,
+                          uint32_t add_row_stride, void* dx, uint32_t dx_row_stride,
+                          void* stream);
+
+/* The experts' rows back to their tokens: out[t] = add[t] + sum_j weights[t, j] *
+ * row, over the choices that have a row; summed as rld_moe_dispatch_grad.  A choice
+ * without a row counts for nothing, whatever its weight (the router's NaN weights
+ * included).
+ *   sorted_rows, places  both NULL: rows are in the flat order that rld_moe_gather
+ *            leaves, and a choice has one if indices[t, j] >= 0 (indices NULL:
+ *            every choice).  Otherwise indices is not read
+ *   weights  fp32 [num_tokens, top_k]
+ *   add      the residual stream, say; as above, with out for dx
+ * RLD_EINVAL on one table without the other. */
+int rld_moe_combine(const void* rows, int rows_f32, uint32_t rows_row_stride,
+                    const int32_t* indices, const int32_t* sorted_rows, const int32_t* places,
+                    const float* weights, uint32_t num_tokens, uint32_t top_k, uint32_t width,
+                    const void* add, uint32_t add_row_stride, void* out, uint32_t out_row_stride,
+                    void* stream);
+
+/* Gradient of rld_moe_combine (add's is dout itself): for every choice with a row
+ *   drows[p] = weights[t, j] * dout[t],  dweights[t, j] = rows[p] . dout[t] in fp32
+ *   drows    rows of no choice are left as they were.  NULL: not wanted (weights
+ *            may then be NULL).  May be rows, at its stride; else must not overlap it
+ *   dweights fp32 [num_tokens, top_k], 0 for a choice without a row; what
+ *            rld_moe_router_grad takes.  NULL: not wanted (rows may then be NULL)
+ * RLD_EINVAL if neither is wanted.  Results do not change from run to run. */
+int rld_moe_combine_grad(const void* rows, int rows_f32, uint32_t rows_row_stride,
+                         const int32_t* indices, const int32_t* sorted_rows,
+                         const int32_t* places, const float* weights, const void* dout,
+                         uint32_t dout_row_stride, uint32_t num_tokens, uint32_t top_k,
+                         uint32_t width, void* drows, uint32_t drows_row_stride, float* dweights,
+                         void* stream);
+
+/* Bytes of workspace rld_grad_norm needs, under the contract of rld_proj's. */
+size_t rld_grad_norm_workspace_bytes(const rld_grad_list* list);
+
+/* norms[g] = the square root of the sum of the squares of group g's gradients, 0
+ * for a group without any.  With one group for each adapter slot these are the
+ * norms by which each adapter's own training is clipped; with one group in all, the
+ * global norm.  Squares and sums in 64 bits, in a fixed order: no overflow short of
+ * the norm's own, and the same bits every run.
+ *   norms    fp32 [num_groups]
+ *   squares  fp64 [num_groups], the sums before the root (to add up over ranks), or
+ *            NULL
+ * num_groups == 0 is a no-op.  RLD_EUNSUPPORTED on more than 2^20 groups or 2^30
+ * chunks. */
+int rld_grad_norm(const rld_grad_list* list, float* norms, double* squares, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/* Every gradient x of group g becomes x * min(1, limits[g] / (norms[g] + 1e-6)) at
+ * its out_addr; gradients that stay in place and whose factor is 1 are neither read
+ * nor written.  fp32 products, rounded once.
+ *   norms    fp32 [num_groups], rld_grad_norm's
+ *   limits   fp32 [num_groups] on the device; a group whose limit is negative or NaN
+ *            is not clipped.  A NaN norm makes a clipped group's gradients NaN; an
+ *            infinite one zeros, NaN where they are infinite */
+int rld_grad_clip(const rld_grad_list* list, const float* norms, const float* limits,
+                  void* stream);
 
 /* ------------------------------------------------------------ diagnostics -- */
 

@@ -73,11 +73,27 @@ class rld_adapter_entry(ctypes.Structure):
                 ("use_rslora", c_int32)]
 
 
+class rld_grad_entry(ctypes.Structure):
+    _fields_ = [("addr", c_uint64), ("out_addr", c_uint64), ("count", c_uint64),
+                ("group", c_uint32), ("bf16", c_int32)]
+
+
+class rld_grad_chunk(ctypes.Structure):
+    _fields_ = [("addr", c_uint64), ("out_addr", c_uint64), ("count", c_uint32),
+                ("group", c_uint32), ("bf16", c_uint32), ("zero", c_uint32)]
+
+
+class rld_grad_list(ctypes.Structure):
+    _fields_ = [("chunks", c_void_p), ("group_starts", c_void_p), ("num_chunks", c_uint32),
+                ("num_groups", c_uint32)]
+
+
 _P = c_void_p
 _R = POINTER(rld_route)
 _M = POINTER(rld_moe_route)
 _L = POINTER(rld_pair)
 _E = POINTER(rld_adapter_entry)
+_G = POINTER(rld_grad_list)
 _u32p = POINTER(c_uint32)
 
 _SIGS = {
@@ -133,6 +149,19 @@ _SIGS = {
     "rld_moe_grouped_pair": (c_int, [_M, _M, _P, c_uint32, c_int, c_uint32, _P, c_uint32, _P,
                                      _P, c_uint32, c_uint32, _P, c_uint32, _P, c_uint32, _P, _P,
                                      c_uint32, _P, c_size_t, _P]),
+    "rld_moe_dispatch": (c_int, [_P, c_int, c_uint32, c_uint32, c_uint32, c_uint32, _P, _P,
+                                 c_uint32, _P, _P]),
+    "rld_moe_dispatch_grad": (c_int, [_P, c_int, c_uint32, _P, _P, c_uint32, c_uint32, c_uint32,
+                                      _P, c_uint32, _P, c_uint32, _P]),
+    "rld_moe_combine": (c_int, [_P, c_int, c_uint32, _P, _P, _P, _P, c_uint32, c_uint32, c_uint32,
+                                _P, c_uint32, _P, c_uint32, _P]),
+    "rld_moe_combine_grad": (c_int, [_P, c_int, c_uint32, _P, _P, _P, _P, _P, c_uint32, c_uint32,
+                                     c_uint32, c_uint32, _P, c_uint32, _P, _P]),
+    "rld_grad_chunks": (c_int, [_P, c_size_t, _u32p]),
+    "rld_grad_pack": (c_int, [_P, c_size_t, c_uint32, _P, c_uint32, _P]),
+    "rld_grad_norm_workspace_bytes": (c_size_t, [_G]),
+    "rld_grad_norm": (c_int, [_G, _P, _P, _P, c_size_t, _P]),
+    "rld_grad_clip": (c_int, [_G, _P, _P, _P]),
     "rld_status_string": (ctypes.c_char_p, [c_int]),
     "rld_last_hip_error": (c_int, []),
     "rld_version": (ctypes.c_char_p, []),
@@ -162,6 +191,13 @@ def ptr(obj) -> int | None:
     if hasattr(obj, "ctypes"):  # numpy array (host helpers)
         return obj.ctypes.data
     raise TypeError(f"cannot pass {type(obj)} as a pointer")
+
+
+def _host(obj) -> int | None:
+    """ptr(), or the address of a ctypes array or structure."""
+    if isinstance(obj, (ctypes.Array, ctypes.Structure)):
+        return ctypes.addressof(obj)
+    return ptr(obj)
 
 
 _current_stream = None  # found at the first call that names no stream
@@ -237,6 +273,16 @@ def rld_gather_row_token(row, top_k):
 
 def rld_gather_grids(max_rank, n_out, n_rows, out):
     return _lib.rld_gather_grids(max_rank, n_out, n_rows, ptr(out))
+
+
+def rld_grad_chunks(entries, n_entries, num_chunks):
+    """entries: an rld_grad_entry array, or a host array of that layout."""
+    return _lib.rld_grad_chunks(_host(entries), n_entries, num_chunks)
+
+
+def rld_grad_pack(entries, n_entries, num_groups, chunks, max_chunks, group_starts):
+    return _lib.rld_grad_pack(_host(entries), n_entries, num_groups, _host(chunks), max_chunks,
+                              ptr(group_starts))
 
 
 def rld_bgmv_workspace_bytes(n, k_in, max_rank, max_loras):
@@ -450,6 +496,53 @@ def rld_moe_grouped_pair(route_a, route_b, x, x_row_stride, x_gather, num_tokens
                                      row_end, ptr(base_a), os_a, ptr(base_b), os_b, ptr(xa_a),
                                      ptr(xa_b), xa_rows_cap, ptr(workspace), workspace_bytes,
                                      stream_handle(stream))
+
+
+def rld_moe_dispatch(x, rows_f32, x_row_stride, num_tokens, top_k, width, sorted_rows, rows,
+                     rows_row_stride, places, stream=None):
+    return _lib.rld_moe_dispatch(ptr(x), int(rows_f32), x_row_stride, num_tokens, top_k, width,
+                                 ptr(sorted_rows), ptr(rows), rows_row_stride, ptr(places),
+                                 stream_handle(stream))
+
+
+def rld_moe_dispatch_grad(drows, rows_f32, drows_row_stride, sorted_rows, places, num_tokens,
+                          top_k, width, add, add_row_stride, dx, dx_row_stride, stream=None):
+    return _lib.rld_moe_dispatch_grad(ptr(drows), int(rows_f32), drows_row_stride,
+                                      ptr(sorted_rows), ptr(places), num_tokens, top_k, width,
+                                      ptr(add), add_row_stride, ptr(dx), dx_row_stride,
+                                      stream_handle(stream))
+
+
+def rld_moe_combine(rows, rows_f32, rows_row_stride, indices, sorted_rows, places, weights,
+                    num_tokens, top_k, width, add, add_row_stride, out, out_row_stride,
+                    stream=None):
+    return _lib.rld_moe_combine(ptr(rows), int(rows_f32), rows_row_stride, ptr(indices),
+                                ptr(sorted_rows), ptr(places), ptr(weights), num_tokens, top_k,
+                                width, ptr(add), add_row_stride, ptr(out), out_row_stride,
+                                stream_handle(stream))
+
+
+def rld_moe_combine_grad(rows, rows_f32, rows_row_stride, indices, sorted_rows, places, weights,
+                         dout, dout_row_stride, num_tokens, top_k, width, drows,
+                         drows_row_stride, dweights, stream=None):
+    return _lib.rld_moe_combine_grad(ptr(rows), int(rows_f32), rows_row_stride, ptr(indices),
+                                     ptr(sorted_rows), ptr(places), ptr(weights), ptr(dout),
+                                     dout_row_stride, num_tokens, top_k, width, ptr(drows),
+                                     drows_row_stride, ptr(dweights), stream_handle(stream))
+
+
+def rld_grad_norm_workspace_bytes(grads):
+    return _lib.rld_grad_norm_workspace_bytes(ctypes.byref(grads))
+
+
+def rld_grad_norm(grads, norms, squares, workspace, workspace_bytes, stream=None):
+    return _lib.rld_grad_norm(ctypes.byref(grads), ptr(norms), ptr(squares), ptr(workspace),
+                              workspace_bytes, stream_handle(stream))
+
+
+def rld_grad_clip(grads, norms, limits, stream=None):
+    return _lib.rld_grad_clip(ctypes.byref(grads), ptr(norms), ptr(limits),
+                              stream_handle(stream))
 
 
 def library_path() -> str:

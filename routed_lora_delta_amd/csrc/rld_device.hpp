@@ -73,6 +73,18 @@ __device__ __forceinline__ void store16(RLD_GLOBAL uint16_t* p, const uint4& v) 
   *reinterpret_cast<RLD_GLOBAL u32x4*>(p) = w;
 }
 
+// 16 bytes at a device address.
+__device__ __forceinline__ u32x4 load_unit(uint64_t at) {
+  return *gp<const u32x4>(at);
+}
+
+__device__ __forceinline__ void store_unit(uint64_t at, const u32x4& v) { *gp<u32x4>(at) = v; }
+
+// A value that is the same in every lane, in a scalar register.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+  return __builtin_amdgcn_readfirstlane(v);
+}
+
 __device__ __forceinline__ uint4 zero16() { return make_uint4(0u, 0u, 0u, 0u); }
 
 // Compiler-level memory barrier: the loads written before it are issued

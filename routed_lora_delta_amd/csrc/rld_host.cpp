@@ -190,6 +190,64 @@ extern "C" int rld_gather_grids(uint32_t max_rank, uint32_t n_out, uint32_t n_ro
   return RLD_OK;
 }
 
+static uint32_t grad_chunk_elems(const rld_grad_entry& e) { return kGradChunk / (e.bf16 ? 2u : 4u); }
+
+extern "C" int rld_grad_chunks(const rld_grad_entry* entries, size_t n_entries,
+                               uint32_t* num_chunks) {
+  if (!num_chunks || (n_entries && !entries)) return RLD_EINVAL;
+  *num_chunks = 0;
+  uint64_t n = 0;
+  for (size_t i = 0; i < n_entries; ++i) {
+    const uint64_t c = entries[i].count, per = grad_chunk_elems(entries[i]);
+    n += c / per + (c % per ? 1 : 0);
+    if (n > kMaxGradChunks) return RLD_EUNSUPPORTED;
+  }
+  *num_chunks = (uint32_t)n;
+  return RLD_OK;
+}
+
+extern "C" int rld_grad_pack(const rld_grad_entry* entries, size_t n_entries, uint32_t num_groups,
+                             rld_grad_chunk* chunks, uint32_t max_chunks, uint32_t* group_starts) {
+  uint32_t total = 0;
+  const int st = rld_grad_chunks(entries, n_entries, &total);
+  if (st) return st;
+  if (num_groups > kMaxGradGroups) return RLD_EUNSUPPORTED;
+  if (num_groups == 0 || !group_starts || (total && !chunks)) return RLD_EINVAL;
+  for (size_t i = 0; i < n_entries; ++i) {
+    const rld_grad_entry& e = entries[i];
+    if (e.group >= num_groups) return RLD_EINVAL;
+    if (e.count && e.addr == 0) return RLD_EINVAL;
+    if ((e.addr & 15u) || (e.out_addr & 15u)) return RLD_EALIGN;
+  }
+  if (total > max_chunks) return RLD_ENOSPACE;
+  // a stable counting sort by group: group_starts first counts, then gives each
+  // group's next place, and in the end is moved back by one group
+  for (uint32_t g = 0; g <= num_groups; ++g) group_starts[g] = 0;
+  for (size_t i = 0; i < n_entries; ++i) {
+    const uint64_t c = entries[i].count, per = grad_chunk_elems(entries[i]);
+    group_starts[entries[i].group + 1] += (uint32_t)(c / per + (c % per ? 1 : 0));
+  }
+  for (uint32_t g = 0; g < num_groups; ++g) group_starts[g + 1] += group_starts[g];
+  for (size_t i = 0; i < n_entries; ++i) {
+    const rld_grad_entry& e = entries[i];
+    const uint32_t per = grad_chunk_elems(e);
+    const uint64_t to = e.out_addr ? e.out_addr : e.addr;
+    for (uint64_t done = 0; done < e.count; done += per) {
+      rld_grad_chunk& c = chunks[group_starts[e.group]++];
+      const uint64_t at = done * (e.bf16 ? 2u : 4u);
+      c.addr = e.addr + at;
+      c.out_addr = to + at;
+      c.count = e.count - done < per ? (uint32_t)(e.count - done) : per;
+      c.group = e.group;
+      c.bf16 = e.bf16 ? 1u : 0u;
+      c.zero = 0;
+    }
+  }
+  for (uint32_t g = num_groups; g > 0; --g) group_starts[g] = group_starts[g - 1];
+  group_starts[0] = 0;
+  return RLD_OK;
+}
+
 extern "C" const char* rld_status_string(int status) {
   switch (status) {
     case RLD_OK: return "ok";

@@ -129,6 +129,12 @@ constexpr uint32_t kGwGrid = 256;
 // Output columns per block of the gather expand (two per thread).
 constexpr uint32_t kGatherCols = 512;
 
+// Bytes of a whole chunk of a gradient list, of which a lane of one wave takes
+// kGradChunk / 1024 units of 16 bytes.
+constexpr uint32_t kGradChunk = 8192;
+constexpr uint32_t kMaxGradChunks = 1u << 30;
+constexpr uint32_t kMaxGradGroups = 1u << 20;
+
 // Grid padded to a multiple of 8 for the XCD remap.
 inline uint32_t xcd_grid(uint32_t total) { return 8u * div_ceil(total, 8u); }
 

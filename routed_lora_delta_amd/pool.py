@@ -15,9 +15,10 @@ from typing import Sequence
 import numpy as np
 import torch
 
-from . import (check, rld_adapter_entry, rld_f16_to_bf16_host, rld_grouped_windows,
-               rld_moe_route, rld_moe_tables_pack, rld_pad_adapter_host, rld_pair, rld_route,
-               rld_route_pack, rld_scale)
+from . import (check, rld_adapter_entry, rld_f16_to_bf16_host, rld_grad_chunk, rld_grad_chunks,
+               rld_grad_entry, rld_grad_list, rld_grad_pack, rld_grouped_windows, rld_moe_route,
+               rld_moe_tables_pack, rld_pad_adapter_host, rld_pair, rld_route, rld_route_pack,
+               rld_scale)
 
 _ALIGN_ELEMS = 128  # 256 bytes of BF16
 
@@ -144,6 +145,25 @@ class MoeRoute:
         self.route = rld_moe_route(self.a_table.data_ptr(), self.b_table.data_ptr(),
                                    self.scale_table.data_ptr(), max_loras, num_experts, k_in,
                                    n_out, max_rank)
+
+
+class GradList:
+    """Gradients to be clipped by the norms of their groups (rld_grad_list), each
+    given as (address, where the clipped one goes or 0 for in place, elements,
+    group, BF16?).  The gradients' own memory stays the caller's."""
+
+    def __init__(self, entries: Sequence, num_groups: int, device="cuda"):
+        host = np.array([tuple(e) for e in entries], np.dtype(rld_grad_entry))
+        n = ctypes.c_uint32(0)
+        check(rld_grad_chunks(host, len(host), ctypes.byref(n)), "rld_grad_chunks")
+        chunks = np.zeros(max(1, n.value), np.dtype(rld_grad_chunk))
+        starts = np.zeros(num_groups + 1, np.uint32)
+        check(rld_grad_pack(host, len(host), num_groups, chunks, n.value, starts),
+              "rld_grad_pack")
+        self.chunks = torch.from_numpy(chunks.view(np.uint8).copy()).to(device)
+        self.group_starts = torch.from_numpy(starts.view(np.int32).copy()).to(device)
+        self.list = rld_grad_list(self.chunks.data_ptr(), self.group_starts.data_ptr(), n.value,
+                                  num_groups)
 
 
 def grouped_windows(total_rows: int, cap: int):

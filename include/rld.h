@@ -113,7 +113,8 @@ typedef struct rld_adapter_entry {
   int32_t use_rslora; /* nonzero: scale = alpha/sqrt(rank); else alpha/rank      */
 } rld_adapter_entry;
 
-/* One gradient of a list: count elements, contiguous, fp32 or BF16. */
+/* One gradient of a list: count elements, contiguous, fp32 or BF16.  Two gradients
+ * share no memory, nor does where one goes with another. */
 typedef struct rld_grad_entry {
   uint64_t addr;     /* device address, 16-byte aligned; may be 0 if count is 0       */
   uint64_t out_addr; /* where the clipped gradient goes, 16-byte aligned; 0: in place */
@@ -616,9 +617,9 @@ int rld_moe_router_grad(const void* logits, int logits_f32, uint32_t logits_row_
  *                each flat row
  * Row p belongs to flat row f if places[f] is p and sorted_rows[p] is f.  An entry
  * of places that the dispatch did not write may hold anything: it finds no row.
- * RLD_EINVAL on top_k or width 0; RLD_EUNSUPPORTED on top_k above 32,
- * num_tokens * top_k of 2^31 and more, num_tokens of 2^24 - 1 and more, or from
- * 2^26 - 3 pieces of 4 KB (dispatch) or 1 KB on.  num_tokens == 0 is a no-op.
+ * RLD_EINVAL on top_k or width 0; RLD_EUNSUPPORTED on top_k above 32, width above
+ * 2^21, num_tokens * top_k of 2^31 and more, from 2^26 - 3 pieces of 1 KB of rows
+ * (dispatch) or tokens (its gradient, combine), or 2^24 tokens (combine_grad) on.  num_tokens == 0 is a no-op.
  *
  * rld_moe_dispatch: tokens to the experts' order,
  *   rows[p] = x[f / top_k], places[f] = p  for every sorted row p that names f.
@@ -626,14 +627,14 @@ int rld_moe_router_grad(const void* logits, int logits_f32, uint32_t logits_row_
  *   rows     device [num_tokens * top_k] rows; rows that name no flat row, and what
  *            lies behind width in each, are left as they were.  Must not overlap x
  *   places   entries of flat rows that are not named are left as they were
- * A flat row that is named twice against the rule is copied twice, and places holds
- * one of the two. */
+ * Of a flat row that is named twice against the rule, places holds one row, and the
+ * other may be left as it was. */
 int rld_moe_dispatch(const void* x, int rows_f32, uint32_t x_row_stride, uint32_t num_tokens,
                      uint32_t top_k, uint32_t width, const int32_t* sorted_rows, void* rows,
                      uint32_t rows_row_stride, int32_t* places, void* stream);
 
-/* Gradient of rld_moe_dispatch: dx[t] = add[t] + sum_j drows[p], p the row of
- * (t, j), over the choices that have one: fp32, add first and j ascending, rounded
+/* Gradient of rld_moe_dispatch: dx[t] = sum_j drows[p] + add[t], p the row of
+ * (t, j), over the choices that have one: fp32, j ascending and add last, rounded
  * once.
  *   add      device, row t at add + t*add_row_stride; NULL: zeros.  May be dx, at
  *            its stride
@@ -644,8 +645,8 @@ int rld_moe_dispatch_grad(const void* drows, int rows_f32, uint32_t drows_row_st
                           uint32_t add_row_stride, void* dx, uint32_t dx_row_stride,
                           void* stream);
 
-/* The experts' rows back to their tokens: out[t] = add[t] + sum_j weights[t, j] *
- * row, over the choices that have a row; summed as rld_moe_dispatch_grad.  A choice
+/* The experts' rows back to their tokens: out[t] = sum_j weights[t, j] * row
+ * + add[t], over the choices that have a row; summed as rld_moe_dispatch_grad.  A choice
  * without a row counts for nothing, whatever its weight (the router's NaN weights
  * included).
  *   sorted_rows, places  both NULL: rows are in the flat order that rld_moe_gather
@@ -694,8 +695,8 @@ int rld_grad_norm(const rld_grad_list* list, float* norms, double* squares, void
  * its out_addr; gradients that stay in place and whose factor is 1 are neither read
  * nor written.  fp32 products, rounded once.
  *   norms    fp32 [num_groups], rld_grad_norm's
- *   limits   fp32 [num_groups] on the device; a group whose limit is negative or NaN
- *            is not clipped.  A NaN norm makes a clipped group's gradients NaN; an
+ *   limits   fp32 [num_groups] on the device; a group whose limit is negative, NaN or
+ *            infinite is not clipped.  A NaN norm makes a clipped group's gradients NaN; an
  *            infinite one zeros, NaN where they are infinite */
 int rld_grad_clip(const rld_grad_list* list, const float* norms, const float* limits,
                   void* stream);

@@ -619,7 +619,8 @@ int rld_moe_router_grad(const void* logits, int logits_f32, uint32_t logits_row_
  * of places that the dispatch did not write may hold anything: it finds no row.
  * RLD_EINVAL on top_k or width 0; RLD_EUNSUPPORTED on top_k above 32, width above
  * 2^21, num_tokens * top_k of 2^31 and more, from 2^26 - 3 pieces of 1 KB of rows
- * (dispatch) or tokens (its gradient, combine), or 2^24 tokens (combine_grad) on.  num_tokens == 0 is a no-op.
+ * (dispatch) or tokens (its gradient, combine), or 2^24 tokens (combine_grad) on.
+ * num_tokens == 0 is a no-op.
  *
  * rld_moe_dispatch: tokens to the experts' order,
  *   rows[p] = x[f / top_k], places[f] = p  for every sorted row p that names f.
@@ -645,10 +646,9 @@ int rld_moe_dispatch_grad(const void* drows, int rows_f32, uint32_t drows_row_st
                           uint32_t add_row_stride, void* dx, uint32_t dx_row_stride,
                           void* stream);
 
-/* The experts' rows back to their tokens: out[t] = sum_j weights[t, j] * row
- * + add[t], over the choices that have a row; summed as rld_moe_dispatch_grad.  A choice
- * without a row counts for nothing, whatever its weight (the router's NaN weights
- * included).
+/* The experts' rows back to their tokens: out[t] = sum_j weights[t, j] * row + add[t]
+ * over the choices that have a row, summed as rld_moe_dispatch_grad.  A choice without
+ * a row counts for nothing, whatever its weight (the router's NaN weights included).
  *   sorted_rows, places  both NULL: rows are in the flat order that rld_moe_gather
  *            leaves, and a choice has one if indices[t, j] >= 0 (indices NULL:
  *            every choice).  Otherwise indices is not read
@@ -696,8 +696,8 @@ int rld_grad_norm(const rld_grad_list* list, float* norms, double* squares, void
  * nor written.  fp32 products, rounded once.
  *   norms    fp32 [num_groups], rld_grad_norm's
  *   limits   fp32 [num_groups] on the device; a group whose limit is negative, NaN or
- *            infinite is not clipped.  A NaN norm makes a clipped group's gradients NaN; an
- *            infinite one zeros, NaN where they are infinite */
+ *            infinite is not clipped.  A NaN norm makes a clipped group's gradients
+ *            NaN; an infinite one zeros, NaN where they are infinite */
 int rld_grad_clip(const rld_grad_list* list, const float* norms, const float* limits,
                   void* stream);
 

@@ -12,10 +12,14 @@
 //   combine_grad   drows[p(t, j)] = w[t, j] dout[t],  dw[t, j] = rows[p(t, j)] . dout[t]
 //
 // All of them are bound by memory.  A lane holds 16 bytes of a row (a unit): a
-// wave's access is 1 KB of one row, contiguous.  What is read once and what is written
-// passes the caches by (load_once, store_once), which also serves who reads the result
-// next: dispatch of 4096 tokens to 8 rows of 2048 BF16 each and a pass over the rows
-// take 65.3 us so, 68.9 otherwise; of 16384 237 and 286.
+// wave's access is 1 KB of one row, contiguous, or 256 bytes of each of four where a
+// row has up to 16 units (128 MB of 8 rows of 64 BF16 a token, combine 29 us and its
+// gradient 56; with a wave a token 60 and 131).  What is read once and what is written
+// passes the caches by (load_once, store_once), which costs a reader of the result
+// nothing and still finds what a writer before left in them:
+// dispatch of 4096 tokens to 8 rows of 2048 BF16 each and a pass over the rows take
+// 65.3 us so, 68.9 otherwise; of 16384 237 and 286; a copy into 64 MB of rows and
+// their combine 36.8 and 37.8.
 #include "rld_device.hpp"
 #include "rld_internal.hpp"
 
@@ -23,6 +27,7 @@ namespace rld {
 
 constexpr uint32_t kMaxMoveTopK = 32;
 constexpr uint32_t kMaxMoveWidth = 1u << 21;  // a row's bytes fit 32 bits
+constexpr int kNarrow = 16;                   // units of a narrow row, at most
 
 // What 16 bytes hold: 8 BF16 or 4 fp32.
 template <bool F32>
@@ -48,6 +53,35 @@ struct Unit {
   }
 };
 
+// A group of G lanes works on one token (or row): the whole wave, or 16 lanes of it.
+// What the group has in common is in scalar registers if it is the wave.  Branches
+// around from() and vote() are the same for a whole group.
+template <int G>
+struct Group {
+  uint32_t base, lane;  // the group's first lane; this lane within it
+  __device__ __forceinline__ Group() {
+    const uint32_t l = threadIdx.x & 63;
+    base = G == 64 ? 0u : l & ~(uint32_t)(G - 1);
+    lane = l - base;
+  }
+  __device__ __forceinline__ uint32_t same(uint32_t v) const { return G == 64 ? uniform(v) : v; }
+  template <class T>
+  __device__ __forceinline__ T from(T v, int lane) const {
+    return G == 64 ? from_lane(v, lane) : __shfl(v, base + lane);
+  }
+  // the group's bits of a vote
+  __device__ __forceinline__ uint64_t vote(bool v) const {
+    const uint64_t m = __ballot(v);
+    return G == 64 ? m : m >> base & ((1ull << (G & 63)) - 1);
+  }
+};
+
+// Threads of a block in groups: the number of this thread's.
+template <int G>
+__device__ __forceinline__ uint32_t group_number() {
+  return (blockIdx.x * blockDim.x + threadIdx.x) / G;
+}
+
 // ---------------------------------------------------------------- dispatch ----
 
 struct DispatchArgs {
@@ -56,26 +90,27 @@ struct DispatchArgs {
   uint32_t T, n, k, units, slices;
 };
 
-// A wave copies kRowUnits units a lane of one sorted row.
+// A group copies kRowUnits units a lane of one sorted row.
 constexpr int kRowUnits = 2;
 
+template <int G>
 __global__ void __launch_bounds__(256) dispatch_rows_kernel(DispatchArgs a) {
-  const uint32_t lane = threadIdx.x & 63;
-  const uint32_t item = uniform(blockIdx.x * 4u + (threadIdx.x >> 6));
-  const uint32_t p = item / a.slices, slice = item - p * a.slices;
+  const Group<G> g;
+  const uint32_t item = g.same(group_number<G>());
+  const uint32_t p = G < 64 ? item : item / a.slices, slice = G < 64 ? 0 : item - p * a.slices;
   if (p >= a.n) return;
-  const uint32_t f = uniform((uint32_t)gp<const int32_t>(a.sorted_)[p]);
+  const uint32_t f = g.same((uint32_t)gp<const int32_t>(a.sorted_)[p]);
   if (f >= a.n) return;
-  if (slice == 0 && lane == 0) gp<int32_t>(a.places_)[f] = (int32_t)p;
-  const uint32_t u0 = slice * (64u * kRowUnits) + lane;
+  if (slice == 0 && g.lane == 0) gp<int32_t>(a.places_)[f] = (int32_t)p;
+  const uint32_t u0 = slice * (64u * kRowUnits) + g.lane;
   const uint64_t from = a.x_ + (f / a.k) * a.xs, to = a.rows_ + p * a.rs;
   u32x4 v[kRowUnits];
 #pragma unroll
   for (int i = 0; i < kRowUnits; ++i)
-    if (u0 + 64u * i < a.units) v[i] = load_unit(from, (u0 + 64u * i) * 16u);
+    if (u0 + G * i < a.units) v[i] = load_unit(from, (u0 + G * i) * 16u);
 #pragma unroll
   for (int i = 0; i < kRowUnits; ++i)
-    if (u0 + 64u * i < a.units) store_once(to, (u0 + 64u * i) * 16u, v[i]);
+    if (u0 + G * i < a.units) store_once(to, (u0 + G * i) * 16u, v[i]);
 }
 
 __global__ void __launch_bounds__(256) dispatch_places_kernel(DispatchArgs a) {
@@ -85,25 +120,30 @@ __global__ void __launch_bounds__(256) dispatch_places_kernel(DispatchArgs a) {
   if (f < a.n) gp<int32_t>(a.places_)[f] = (int32_t)p;
 }
 
-// The second launch of large calls: a wave reads 64 units of a token once and writes
+// The second launch of large calls: a group reads G units of a token once and writes
 // them to each of its rows.
+template <int G>
 __global__ void __launch_bounds__(256) dispatch_tokens_kernel(DispatchArgs a) {
-  const uint32_t lane = threadIdx.x & 63;
-  const uint32_t item = uniform(blockIdx.x * 4u + (threadIdx.x >> 6));
-  const uint32_t t = item / a.slices, slice = item - t * a.slices;
+  const Group<G> g;
+  const uint32_t item = g.same(group_number<G>());
+  const uint32_t t = G < 64 ? item : item / a.slices, slice = G < 64 ? 0 : item - t * a.slices;
   if (t >= a.T) return;
-  const uint32_t u = slice * 64u + lane;
+  const uint32_t u = slice * 64u + g.lane;
   const uint32_t at = min(u, a.units - 1u) * 16u;
   const u32x4 v = load_unit(a.x_ + t * a.xs, at);
-  const uint32_t f = t * a.k + min(lane, a.k - 1u);
-  uint32_t p = (uint32_t)gp<const int32_t>(a.places_)[f];
-  const bool have = lane < a.k && p < a.n;
-  p = have ? p : 0u;
-  uint64_t own = __ballot(have && (uint32_t)gp<const int32_t>(a.sorted_)[p] == f);
-  while (own) {
-    const int j = __builtin_ctzll(own);
-    own &= own - 1;
-    if (u < a.units) store_once(a.rows_ + from_lane(p, j) * a.rs, at, v);
+  for (uint32_t j0 = 0; j0 < a.k; j0 += G) {
+    const bool in = j0 + g.lane < a.k;
+    const uint32_t f = t * a.k + (in ? j0 + g.lane : j0);
+    uint32_t p = (uint32_t)gp<const int32_t>(a.places_)[f];
+    const bool have = in && p < a.n;
+    p = have ? p : 0u;
+    uint64_t own = g.vote(have && (uint32_t)gp<const int32_t>(a.sorted_)[p] == f);
+    while (own) {
+      const int j = __builtin_ctzll(own);
+      own &= own - 1;
+      const uint64_t row = a.rows_ + g.from(p, j) * a.rs;
+      if (u < a.units) store_once(row, at, v);
+    }
   }
 }
 
@@ -115,25 +155,27 @@ struct CombineArgs {
   uint32_t T, n, k, units, slices;
 };
 
-// The rows of a token's choices j0 .. j0 + 7: lane j holds choice j0 + j.  `have`
-// has a bit for each row that can be read; own() one for each of them that belongs
-// to its choice, which takes one load more: called once the rows' loads are out.
+// The rows of a token's choices j0 .. j0 + KB - 1: lane j of the group holds choice
+// j0 + j.  `have` has a bit for each row that can be read; own() one for each of them
+// that belongs to its choice, which takes one load more: called once the rows' loads
+// are out.
+template <int G>
 struct Choices {
   uint32_t row, back, f;
   uint64_t have;
-  __device__ __forceinline__ uint64_t own() {
+  __device__ __forceinline__ uint64_t own(const Group<G>& g) {
     asm volatile("" : "+v"(back) : : "memory");  // the comparison stays behind those loads
-    return have & __ballot(back == f);
+    return have & g.vote(back == f);
   }
 };
 
 // Loads without a branch, from clamped places.
-template <bool SORTED, class A>
-__device__ __forceinline__ Choices find_choices(const A& a, uint32_t t, uint32_t j0,
-                                                uint32_t lane) {
-  const bool in = lane < 8u && j0 + lane < a.k;
-  Choices c;
-  c.f = t * a.k + (in ? j0 + lane : j0);
+template <bool SORTED, int KB, int G, class A>
+__device__ __forceinline__ Choices<G> find_choices(const A& a, const Group<G>& g, uint32_t t,
+                                                   uint32_t j0) {
+  const bool in = g.lane < KB && j0 + g.lane < a.k;
+  Choices<G> c;
+  c.f = t * a.k + (in ? j0 + g.lane : j0);
   c.row = c.back = c.f;
   bool have = in;
   if (SORTED) {
@@ -145,20 +187,22 @@ __device__ __forceinline__ Choices find_choices(const A& a, uint32_t t, uint32_t
     const int32_t e = gp<const int32_t>(a.indices_)[c.f];
     have = in && e >= 0;
   }
-  c.have = __ballot(have);
+  c.have = g.vote(have);
   return c;
 }
 
-// A wave adds up one slice of 64 units of a token's rows, in fp32, j ascending: eight
+// A group adds up one slice of G units of a token's rows, in fp32, j ascending: eight
 // rows' loads at a time, the places before them, the check and the weights beside
 // them.  32771 tokens of 8 rows of 2048 BF16, onto a residual: 209 us, 5.9 TB/s, in
 // blocks of one wave (214 in blocks of four).
-template <bool F32, bool SORTED>
+template <bool F32, bool SORTED, int G>
 __global__ void __launch_bounds__(64) combine_kernel(CombineArgs a) {
   constexpr int N = Unit<F32>::N;
-  const uint32_t lane = threadIdx.x;
-  const uint32_t t = blockIdx.x / a.slices, slice = blockIdx.x - t * a.slices;
-  const uint32_t u = slice * 64u + lane;
+  const Group<G> g;
+  const uint32_t item = g.same(group_number<G>());
+  const uint32_t t = G < 64 ? item : item / a.slices, slice = G < 64 ? 0 : item - t * a.slices;
+  if (t >= a.T) return;
+  const uint32_t u = slice * 64u + g.lane;
   const uint32_t at = min(u, a.units - 1u) * 16u;  // lanes past the row load its last unit
   u32x4 last = {0u, 0u, 0u, 0u};
   if (a.add_) last = load_once(a.add_ + t * a.as, at);
@@ -167,20 +211,20 @@ __global__ void __launch_bounds__(64) combine_kernel(CombineArgs a) {
   for (int i = 0; i < N; ++i) acc[i] = 0.f;
 #pragma nounroll
   for (uint32_t j0 = 0; j0 < a.k; j0 += 8) {
-    Choices c = find_choices<SORTED>(a, t, j0, lane);
+    Choices<G> c = find_choices<SORTED, 8>(a, g, t, j0);
     float w = 1.f;
     if (a.weights_) w = gp<const float>(a.weights_)[c.f];
     u32x4 r[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       r[j] = u32x4{0u, 0u, 0u, 0u};
-      if ((c.have >> j) & 1u) r[j] = load_once(a.rows_ + from_lane(c.row, j) * a.rs, at);
+      if ((c.have >> j) & 1u) r[j] = load_once(a.rows_ + g.from(c.row, j) * a.rs, at);
     }
-    const uint64_t own = c.own();
+    const uint64_t own = c.own(g);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if ((own >> j) & 1u) {
-        const float wj = from_lane(w, j);
+        const float wj = g.from(w, j);
         float v[N];
         Unit<F32>::open(r[j], v);
 #pragma unroll
@@ -200,14 +244,17 @@ __global__ void __launch_bounds__(64) combine_kernel(CombineArgs a) {
 struct CombineGradArgs {
   uint64_t rows_, indices_, sorted_, places_, weights_, dout_, drows_, dweights_;
   uint64_t rs, ds, os;  // bytes of a row of rows, dout, drows
-  uint32_t T, n, k, units;
+  uint32_t T, n, k, units, waves;
 };
 
-// Sums of eight values over a wave, for ten exchanges: each of the first three
-// halves the values that a lane holds.  Lane 8 i gets the sum of v[i].
-__device__ __forceinline__ float sum8(float* v, uint32_t lane) {
+// Sums of KB values over a group: each of the first exchanges halves the values that
+// a lane holds (10 exchanges for eight over a wave).  Lane G / KB * i of the group
+// gets the sum of v[i].
+template <int KB, int G>
+__device__ __forceinline__ float sum_each(float* v, uint32_t lane) {
+  int m = G / 2;
 #pragma unroll
-  for (int half = 4, m = 32; half >= 1; half >>= 1, m >>= 1) {
+  for (int half = KB / 2; half >= 1; half >>= 1, m >>= 1) {
     const bool up = (lane & m) != 0;
 #pragma unroll
     for (int i = 0; i < half; ++i) {
@@ -217,83 +264,102 @@ __device__ __forceinline__ float sum8(float* v, uint32_t lane) {
     }
   }
   float s = v[0];
-  s += __shfl_xor(s, 4);
-  s += __shfl_xor(s, 2);
-  s += __shfl_xor(s, 1);
+#pragma unroll
+  for (; m >= 1; m >>= 1) s += __shfl_xor(s, m);
   return s;
 }
 
-// WPT waves share a token's columns; 256 / (64 WPT) tokens a block.  A row's unit
-// is read before the same thread writes it, so drows may be rows.  16387 tokens of 8
-// rows of 2048 BF16: 204 us, 5.05 TB/s, where a copy reaches 5.2 (212 with two waves a
-// token, 222 with one; more waves a CU, by fewer registers, spill).
-template <bool F32, bool SORTED, int WPT>
-__global__ void __launch_bounds__(256) combine_grad_kernel(CombineGradArgs a) {
-  constexpr int N = Unit<F32>::N;
-  __shared__ float part[4][8];
-  const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const uint32_t w0 = wave % WPT;
-  const uint32_t t = blockIdx.x * (4u / WPT) + wave / WPT;
+// Units of a row that a lane of combine_grad takes at a time, by the rows it takes: 62500
+// tokens of one row of 2048 BF16 118 us with two, 123 with one or four.
+__host__ __device__ constexpr uint32_t units_per_lane(uint32_t rows) { return rows > 2 ? 1 : 2; }
+
+// `waves` groups share a token's columns (one, if groups are narrow).  A group takes KB
+// of its rows and UPL units a lane of each at a time.  A row's unit is read before the
+// same thread writes it, so drows may be rows.  16387 tokens of 8 rows of 2048 BF16: 204
+// us, 5.05 TB/s, where a copy reaches 5.2 (more waves a CU, by fewer registers, spill).
+template <bool F32, bool SORTED, int KB, int G>
+__global__ void __launch_bounds__(1024) combine_grad_kernel(CombineGradArgs a) {
+  constexpr int N = Unit<F32>::N, UPL = units_per_lane(KB);
+  __shared__ float part[16][KB];
+  const Group<G> g;
+  const uint32_t waves = G < 64 ? 1u : a.waves;
+  const uint32_t wave = uniform(threadIdx.x >> 6), w0 = wave & (waves - 1u), first = wave - w0;
+  const uint32_t t = g.same(group_number<G>()) / waves;
   const bool on = t < a.T;
 #pragma nounroll
-  for (uint32_t j0 = 0; j0 < a.k; j0 += 8) {
-    float dot[8];
+  for (uint32_t j0 = 0; j0 < a.k; j0 += KB) {
+    float dot[KB];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dot[j] = 0.f;
+    for (int j = 0; j < KB; ++j) dot[j] = 0.f;
     uint64_t own = 0;
     if (on) {
-      Choices c = find_choices<SORTED>(a, t, j0, lane);
+      Choices<G> c = find_choices<SORTED, KB>(a, g, t, j0);
       float w = 0.f;
       if (a.drows_) w = gp<const float>(a.weights_)[c.f];
-      own = c.own();
-      for (uint32_t u = w0 * 64u + lane; u < a.units; u += 64u * WPT) {
-        const uint32_t at = u * 16u;
-        float d[N];
-        u32x4 r[8];
-        const u32x4 dv = load_once(a.dout_ + t * a.ds, at);
+      own = c.own(g);
+      // a wave's lanes past the row leave the loop; a narrow group stays together, once
+      for (uint32_t u0 = w0 * (G * UPL) + g.lane; G < 64 ? u0 == g.lane : u0 < a.units;
+           u0 += G * UPL * waves) {
+        const auto in = [&](int q) { return (G == 64 && q == 0) || u0 + G * q < a.units; };
+        u32x4 dv[UPL], r[UPL][KB];
+#pragma unroll
+        for (int q = 0; q < UPL; ++q)
+          dv[q] = load_once(a.dout_ + t * a.ds, min(u0 + G * q, a.units - 1u) * 16u);
         if (a.dweights_) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            r[j] = u32x4{0u, 0u, 0u, 0u};
-            if ((c.have >> j) & 1u) r[j] = load_once(a.rows_ + from_lane(c.row, j) * a.rs, at);
+          for (int j = 0; j < KB; ++j) {
+#pragma unroll
+            for (int q = 0; q < UPL; ++q) r[q][j] = u32x4{0u, 0u, 0u, 0u};
+            if ((c.have >> j) & 1u) {
+              const uint64_t row = a.rows_ + g.from(c.row, j) * a.rs;
+#pragma unroll
+              for (int q = 0; q < UPL; ++q)
+                if (in(q)) r[q][j] = load_once(row, (u0 + G * q) * 16u);
+            }
           }
         }
-        Unit<F32>::open(dv, d);
-        if (a.dweights_) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float v[N];
-            Unit<F32>::open(r[j], v);
+        for (int q = 0; q < UPL; ++q) {
+          float d[N];
+          Unit<F32>::open(dv[q], d);
+          if (a.dweights_) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) dot[j] += d[i] * v[i];
-          }
-        }
-        if (a.drows_) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if ((own >> j) & 1u) {
-              const float wj = from_lane(w, j);
+            for (int j = 0; j < KB; ++j) {
               float v[N];
+              Unit<F32>::open(r[q][j], v);
 #pragma unroll
-              for (int i = 0; i < N; ++i) v[i] = wj * d[i];
-              store_once(a.drows_ + from_lane(c.row, j) * a.os, at, Unit<F32>::close(v));
+              for (int i = 0; i < N; ++i) dot[j] += d[i] * v[i];
+            }
+          }
+          if (a.drows_) {
+#pragma unroll
+            for (int j = 0; j < KB; ++j) {
+              if ((own >> j) & 1u) {
+                const float wj = g.from(w, j);
+                const uint64_t row = a.drows_ + g.from(c.row, j) * a.os;
+                float v[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] = wj * d[i];
+                if (in(q))
+                  store_once(row, (u0 + G * q) * 16u, Unit<F32>::close(v));
+              }
             }
           }
         }
       }
     }
     if (!a.dweights_) continue;
-    float s = sum8(dot, lane);
-    const uint32_t j = lane >> 3;
-    if (WPT > 1) {
+    float s = sum_each<KB, G>(dot, g.lane);
+    const uint32_t j = g.lane / (G / KB);
+    const bool mine = g.lane % (G / KB) == 0;
+    if (waves > 1) {
       if (j0) __syncthreads();
-      if ((lane & 7u) == 0) part[wave][j] = s;
+      if (mine) part[wave][j] = s;
       __syncthreads();
-      s = part[wave - w0][j];
-#pragma unroll
-      for (int v = 1; v < WPT; ++v) s += part[wave - w0 + v][j];
+      s = part[first][j];
+      for (uint32_t v = 1; v < waves; ++v) s += part[first + v][j];
     }
-    if (on && w0 == 0 && (lane & 7u) == 0 && j0 + j < a.k)
+    if (on && w0 == 0 && mine && j0 + j < a.k)
       gp<float>(a.dweights_)[(uint64_t)t * a.k + j0 + j] = ((own >> j) & 1u) ? s : 0.f;
   }
 }
@@ -319,6 +385,14 @@ static int check_tables(const int32_t* indices, const int32_t* sorted_rows,
                         const int32_t* places) {
   if ((sorted_rows == nullptr) != (places == nullptr)) return RLD_EINVAL;
   return aligned4(indices) && aligned4(sorted_rows) && aligned4(places) ? RLD_OK : RLD_EALIGN;
+}
+
+template <bool F32, bool SORTED>
+static void launch_combine(const CombineArgs& a, hipStream_t s) {
+  if (a.units <= kNarrow)
+    combine_kernel<F32, SORTED, kNarrow><<<div_ceil(a.T, 64 / kNarrow), 64, 0, s>>>(a);
+  else
+    combine_kernel<F32, SORTED, 64><<<a.T * a.slices, 64, 0, s>>>(a);
 }
 
 static int combine(const void* rows, int f32, uint32_t rs, const int32_t* indices,
@@ -350,20 +424,37 @@ static int combine(const void* rows, int f32, uint32_t rs, const int32_t* indice
   a.units = units_of(width, f32);
   a.slices = div_ceil(a.units, 64);
   if (too_many((uint64_t)T * a.slices)) return RLD_EUNSUPPORTED;
-  const uint32_t blocks = T * a.slices;
   hipStream_t s = (hipStream_t)stream;
-  if (a.places_) f32 ? combine_kernel<true, true><<<blocks, 64, 0, s>>>(a)
-                     : combine_kernel<false, true><<<blocks, 64, 0, s>>>(a);
-  else f32 ? combine_kernel<true, false><<<blocks, 64, 0, s>>>(a)
-           : combine_kernel<false, false><<<blocks, 64, 0, s>>>(a);
+  if (f32) a.places_ ? launch_combine<true, true>(a, s) : launch_combine<true, false>(a, s);
+  else a.places_ ? launch_combine<false, true>(a, s) : launch_combine<false, false>(a, s);
   return launch_status();
 }
 
-template <bool F32, bool SORTED>
+template <bool F32, bool SORTED, int KB>
 static void launch_combine_grad(const CombineGradArgs& a, hipStream_t s) {
-  if (a.units <= 64) combine_grad_kernel<F32, SORTED, 1><<<div_ceil(a.T, 4), 256, 0, s>>>(a);
-  else if (a.units <= 128) combine_grad_kernel<F32, SORTED, 2><<<div_ceil(a.T, 2), 256, 0, s>>>(a);
-  else combine_grad_kernel<F32, SORTED, 4><<<a.T, 256, 0, s>>>(a);
+  if (a.units <= kNarrow) {
+    combine_grad_kernel<F32, SORTED, KB, kNarrow><<<div_ceil(a.T, 256 / kNarrow), 256, 0, s>>>(a);
+    return;
+  }
+  const uint32_t threads = a.waves < 4 ? 256 : 64 * a.waves;
+  combine_grad_kernel<F32, SORTED, KB, 64>
+      <<<div_ceil(a.T, threads / (64 * a.waves)), threads, 0, s>>>(a);
+}
+
+// Waves of a token: as many as take its columns at once, up to 8; 16 where 8 would take
+// more than twice as long.  (us with 4, 8 and 16, 256 MB of 8 rows a token: 4096 BF16
+// 91, 88 and 89, 8192 BF16 97, 93 and 97, 8192 fp32 98, 94 and 92; of 7 tokens of 8192
+// BF16 9.0, 7.5 and 7.6, of 3 of fp32 17.7, 11.9 and 9.9.)
+template <bool F32, bool SORTED>
+static void launch_combine_grad(CombineGradArgs a, hipStream_t s) {
+  const uint32_t units = 64 * units_per_lane(a.k);
+  a.waves = 1;
+  while (a.waves < 8 && a.waves * units < a.units) a.waves *= 2;
+  if (2 * 8 * units < a.units) a.waves = 16;
+  if (a.k > 4) launch_combine_grad<F32, SORTED, 8>(a, s);
+  else if (a.k > 2) launch_combine_grad<F32, SORTED, 4>(a, s);
+  else if (a.k > 1) launch_combine_grad<F32, SORTED, 2>(a, s);
+  else launch_combine_grad<F32, SORTED, 1>(a, s);
 }
 
 }  // namespace rld
@@ -398,13 +489,25 @@ extern "C" int rld_moe_dispatch(const void* x, int rows_f32, uint32_t x_row_stri
   // Reading a token once saves top_k - 1 reads of it, from the caches mostly, and
   // costs a launch: us with one launch and with two, 2048 BF16 a row, top_k 8: 512
   // tokens 5.2 and 6.4, 1024 (29 MB saved) 9.0 and 9.1, 4096 33.3 and 27.2, 16384 136
-  // and 98; rows of 4096, top_k 2: 1024 6.1 and 6.8, 4096 (34 MB) 18.9 and 18.1.
-  if ((uint64_t)(a.n - a.T) * width * size < (32u << 20)) {
-    a.slices = div_ceil(a.units, 64u * kRowUnits);
-    dispatch_rows_kernel<<<div_ceil(a.n * a.slices, 4), 256, 0, s>>>(a);
-  } else {
+  // and 98; rows of 4096, top_k 2: 1024 6.1 and 6.8, 4096 (34 MB) 18.9 and 18.1.  Rows
+  // that share cache lines are better written in order, so that their parts meet: 1000
+  // BF16, top_k 6, 106 MB saved 34.7 and 35.8, 333 MB 110 and 105; 72, top_k 8, 350 MB
+  // saved 169 and 254.
+  const uint64_t saved = (uint64_t)(a.n - a.T) * width * size;
+  const bool lines = ((a.rows_ | a.rs | width * size) & 127u) == 0;
+  const bool twice = lines ? saved >= (32u << 20)
+                           : a.units > kNarrow && saved >= (128u << 20);
+  const uint32_t groups = 256 / (a.units <= kNarrow ? kNarrow : 64);
+  if (twice) {
     dispatch_places_kernel<<<div_ceil(a.n, 256), 256, 0, s>>>(a);
-    dispatch_tokens_kernel<<<div_ceil(a.T * a.slices, 4), 256, 0, s>>>(a);
+    const uint32_t blocks = div_ceil(a.T * a.slices, groups);
+    if (a.units <= kNarrow) dispatch_tokens_kernel<kNarrow><<<blocks, 256, 0, s>>>(a);
+    else dispatch_tokens_kernel<64><<<blocks, 256, 0, s>>>(a);
+  } else {
+    a.slices = div_ceil(a.units, 64u * kRowUnits);
+    const uint32_t blocks = div_ceil(a.n * a.slices, groups);
+    if (a.units <= kNarrow) dispatch_rows_kernel<kNarrow><<<blocks, 256, 0, s>>>(a);
+    else dispatch_rows_kernel<64><<<blocks, 256, 0, s>>>(a);
   }
   return launch_status();
 }

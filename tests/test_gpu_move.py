@@ -173,7 +173,7 @@ def check_grad(r, width, f32, pad, flat, want_rows=True, want_w=True, in_place=F
 # units a lane, whole and partial ones; choices below, at and above a batch of eight
 SHAPES = [(1, 1, 8, 0), (1, 8, 2048, 0), (2, 32, 72, 8), (3, 5, 520, 8), (33, 8, 512, 0),
           (64, 2, 1000, 64), (129, 9, 1032, 0), (257, 4, 4104, 8), (333, 17, 64, 0),
-          (1500, 8, 2048, 0)]
+          (70, 1, 2048, 8), (5, 3, 8200, 0), (67, 32, 128, 8), (1500, 8, 2048, 0)]
 
 
 @pytest.mark.parametrize("f32", [False, True])
@@ -190,14 +190,17 @@ def test_every_operator(T, k, width, pad, f32):
     check_grad(r, width, f32, pad, True)
 
 
-@pytest.mark.parametrize("T,k,width", [(2500, 8, 1024), (4700, 2, 4096), (1100, 32, 520)])
-def test_dispatch_in_two_launches(T, k, width):
-    """Above 32 MB of reads saved, with gaps behind the rows."""
-    say(f"case: dispatch in two launches T={T} k={k} width={width}")
-    r = Routing(T, T, k, missing=0.05)
-    assert r.T * (k - 1) * width * 2 >= 32 << 20
-    check_dispatch(r, width, False, 8)
-    check_dispatch(r, width, True, 0)
+@pytest.mark.parametrize("T,k,width,pad,f32", [
+    (2500, 8, 1024, 64, False), (2500, 8, 1024, 0, True), (1100, 32, 576, 0, False),
+    (40000, 8, 64, 64, False), (9000, 32, 64, 0, False), (9000, 32, 32, 0, True),
+    (5000, 8, 2056, 8, False), (3500, 11, 1000, 0, True)])
+def test_dispatch_in_two_launches(T, k, width, pad, f32):
+    """Rows of whole cache lines above 32 MB of reads saved, others above 128 MB."""
+    say(f"case: dispatch in two launches T={T} k={k} width={width} pad={pad} f32={f32}")
+    size = 4 if f32 else 2
+    lines = width * size % 128 == 0 and pad * size % 128 == 0
+    assert T * (k - 1) * width * size >= (32 if lines else 128) << 20
+    check_dispatch(Routing(T, T, k, missing=0.05), width, f32, pad)
 
 
 @pytest.mark.parametrize("masked,missing", [(1.0, 0.0), (0.0, 1.0), (0.0, 0.0), (0.5, 0.5)])

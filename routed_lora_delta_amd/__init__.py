@@ -182,12 +182,14 @@ def header_symbols():
 
 def ptr(obj) -> int | None:
     """Marshal a pointer argument: int address, None, or an object with data_ptr()."""
-    if obj is None:
-        return None
+    if obj is None or obj.__class__ is int:
+        return obj
+    try:
+        return obj.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(obj, int):
         return obj
-    if hasattr(obj, "data_ptr"):
-        return obj.data_ptr()
     if hasattr(obj, "ctypes"):  # numpy array (host helpers)
         return obj.ctypes.data
     raise TypeError(f"cannot pass {type(obj)} as a pointer")
@@ -210,7 +212,8 @@ def _find_current_stream():
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     if raw is None:
         return lambda: torch.cuda.current_stream().cuda_stream
-    device = torch.cuda.current_device
+    torch.cuda.current_device()  # sets torch's GPU side up, which the two below do not
+    device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     return lambda: raw(device())
 
 

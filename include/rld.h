@@ -618,8 +618,8 @@ int rld_moe_router_grad(const void* logits, int logits_f32, uint32_t logits_row_
  * Row p belongs to flat row f if places[f] is p and sorted_rows[p] is f.  An entry
  * of places that the dispatch did not write may hold anything: it finds no row.
  * RLD_EINVAL on top_k or width 0; RLD_EUNSUPPORTED on top_k above 32, width above
- * 2^21, num_tokens * top_k of 2^31 and more, from 2^26 - 3 pieces of 1 KB of rows
- * (dispatch) or tokens (its gradient, combine), or 2^24 tokens (combine_grad) on.
+ * 2^21, num_tokens * top_k of 2^31 and more, and from 2^26 - 3 pieces of 1 KB of rows
+ * (dispatch) or of tokens (its gradient, combine), or tokens (combine_grad) on.
  * num_tokens == 0 is a no-op.
  *
  * rld_moe_dispatch: tokens to the experts' order,

@@ -451,6 +451,7 @@ static void launch_combine_grad(CombineGradArgs a, hipStream_t s) {
   a.waves = 1;
   while (a.waves < 8 && a.waves * units < a.units) a.waves *= 2;
   if (2 * 8 * units < a.units) a.waves = 16;
+  while (too_many((uint64_t)a.T * a.waves)) a.waves /= 2;
   if (a.k > 4) launch_combine_grad<F32, SORTED, 8>(a, s);
   else if (a.k > 2) launch_combine_grad<F32, SORTED, 4>(a, s);
   else if (a.k > 1) launch_combine_grad<F32, SORTED, 2>(a, s);
@@ -566,8 +567,7 @@ extern "C" int rld_moe_combine_grad(const void* rows, int rows_f32, uint32_t row
   a.n = num_tokens * top_k;
   a.k = top_k;
   a.units = units_of(width, rows_f32);
-  // blocks of 256 threads, as many as tokens at most
-  if (num_tokens >= (1u << 24)) return RLD_EUNSUPPORTED;
+  if (too_many(num_tokens)) return RLD_EUNSUPPORTED;
   hipStream_t s = (hipStream_t)stream;
   if (places) rows_f32 ? launch_combine_grad<true, true>(a, s) : launch_combine_grad<false, true>(a, s);
   else rows_f32 ? launch_combine_grad<true, false>(a, s) : launch_combine_grad<false, false>(a, s);

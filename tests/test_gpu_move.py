@@ -380,6 +380,36 @@ def test_far_rows():
     assert bool((rows[:r.routed] == 0.25).all()) and bool((rows[r.routed:] == 77.25).all())
 
 
+@pytest.mark.parametrize("T,k,width", [((1 << 24) + 5, 2, 8), ((1 << 22) + 3, 2, 136)])
+def test_very_many_tokens(T, k, width):
+    """Small whole numbers, so that every value is exact: a token's rows are its row of
+    x, their sum with weights 1/2 and 2 is 5/2 of it."""
+    say(f"case: {T} tokens of {k} rows of {width}")
+    dev, n = require_gpu(), T * k
+    srows = torch.randperm(n, device=dev, dtype=torch.int32)
+    places = torch.zeros_like(srows)
+    x = (torch.arange(T, device=dev)[:, None] % 61 + torch.arange(width, device=dev) % 7
+         ).to(torch.bfloat16)
+    rows = torch.zeros((n, width), dtype=torch.bfloat16, device=dev)
+    R.check(R.rld_moe_dispatch(x, False, width, T, k, width, srows, rows, width, places),
+            "dispatch")
+    assert torch.equal(srows[places.long()], torch.arange(n, device=dev, dtype=torch.int32))
+    assert torch.equal(rows, x[torch.div(srows.long(), k, rounding_mode="floor")])
+    w = torch.tensor([0.5, 2.0], device=dev).repeat(T, 1)
+    out, dw = torch.zeros_like(x), torch.zeros_like(w)
+    R.check(R.rld_moe_combine(rows, False, width, None, srows, places, w, T, k, width, None, 0,
+                              out, width), "combine")
+    assert torch.equal(out, (x.float() * 2.5).to(torch.bfloat16))
+    dout = torch.ones_like(x)
+    R.check(R.rld_moe_combine_grad(rows, False, width, None, srows, places, w, dout, width, T, k,
+                                   width, rows, width, dw), "combine_grad")
+    assert torch.equal(dw, x.float().sum(1, keepdim=True).expand(T, k))
+    assert torch.equal(rows[:, 0].float(), w.reshape(-1)[srows.long()])
+    R.check(R.rld_moe_dispatch_grad(rows, False, width, srows, places, T, k, width, x, width, out,
+                                    width), "dispatch_grad")
+    assert torch.equal(out, (x.float() + 2.5).to(torch.bfloat16))
+
+
 def test_gradient_against_differences():
     """out is linear in the rows and in the weights: central differences of the 64-bit
     combine agree to the rounding of the gradient itself."""

@@ -66,7 +66,7 @@ def test_grids_past_32_bits_are_refused():
     assert _dispatch(T=T // 8 + 1, k=1, f=1, h=2048, xs=2048, rs=2048) == EUNSUPPORTED
     assert _combine(T=T, k=1) == EUNSUPPORTED
     assert _dispatch_grad(T=T, k=1) == EUNSUPPORTED
-    assert _combine_grad(T=1 << 24, k=1) == EUNSUPPORTED
+    assert _combine_grad(T=T, k=1) == EUNSUPPORTED
 
 
 @pytest.mark.parametrize("kw,status", [

@@ -18,7 +18,7 @@ constexpr uint32_t kGradWaves = 4096;  // of a launch at most: all of them run a
 // Clipping walks each run backwards, so it begins with what the norm read last: the
 // last kKeep chunks of a run, 256 MB over all waves, are read through the 256 MB
 // cache behind the L2s and found there.  The rest passes it by.  Norm and clipping of
-// 415 MB, out of place, with kKeep 0 / 4 / 8 / 12: 175, 162, 151 and 156 us; the norm
+// 311 MB, out of place, with kKeep 0 / 4 / 8 / 12: 175, 162, 151 and 156 us; the norm
 // alone of 785 MB 124.5, 125.3, 128.5 and 131.3.
 constexpr uint32_t kKeep = 8;
 constexpr float kClipEps = 1e-6f;

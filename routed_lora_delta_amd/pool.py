@@ -153,15 +153,15 @@ class GradList:
     group, BF16?).  The gradients' own memory stays the caller's."""
 
     def __init__(self, entries: Sequence, num_groups: int, device="cuda"):
-        host = np.array([tuple(e) for e in entries], np.dtype(rld_grad_entry))
+        host = np.fromiter(map(tuple, entries), np.dtype(rld_grad_entry), len(entries))
         n = ctypes.c_uint32(0)
         check(rld_grad_chunks(host, len(host), ctypes.byref(n)), "rld_grad_chunks")
-        chunks = np.zeros(max(1, n.value), np.dtype(rld_grad_chunk))
-        starts = np.zeros(num_groups + 1, np.uint32)
+        chunks = np.empty(max(1, n.value), np.dtype(rld_grad_chunk))
+        starts = np.empty(num_groups + 1, np.uint32)
         check(rld_grad_pack(host, len(host), num_groups, chunks, n.value, starts),
               "rld_grad_pack")
-        self.chunks = torch.from_numpy(chunks.view(np.uint8).copy()).to(device)
-        self.group_starts = torch.from_numpy(starts.view(np.int32).copy()).to(device)
+        self.chunks = torch.from_numpy(chunks.view(np.uint8)).to(device)
+        self.group_starts = torch.from_numpy(starts.view(np.int32)).to(device)
         self.list = rld_grad_list(self.chunks.data_ptr(), self.group_starts.data_ptr(), n.value,
                                   num_groups)
 

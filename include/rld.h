@@ -648,7 +648,8 @@ int rld_moe_dispatch_grad(const void* drows, int rows_f32, uint32_t drows_row_st
 
 /* The experts' rows back to their tokens: out[t] = sum_j weights[t, j] * row + add[t]
  * over the choices that have a row, summed as rld_moe_dispatch_grad.  A choice without
- * a row counts for nothing, whatever its weight (the router's NaN weights included).
+ * a row counts for nothing, whatever its weight (the router's NaN weights included); a
+ * token without any gets add, or zeros.
  *   sorted_rows, places  both NULL: rows are in the flat order that rld_moe_gather
  *            leaves, and a choice has one if indices[t, j] >= 0 (indices NULL:
  *            every choice).  Otherwise indices is not read

@@ -16,10 +16,9 @@
 // row has up to 16 units (128 MB of 8 rows of 64 BF16 a token, combine 29 us and its
 // gradient 56; with a wave a token 60 and 131).  What is read once and what is written
 // passes the caches by (load_once, store_once), which costs a reader of the result
-// nothing and still finds what a writer before left in them:
-// dispatch of 4096 tokens to 8 rows of 2048 BF16 each and a pass over the rows take
-// 65.3 us so, 68.9 otherwise; of 16384 237 and 286; a copy into 64 MB of rows and
-// their combine 36.8 and 37.8.
+// nothing and still finds what a writer before left in them: dispatch of 4096 tokens
+// to 8 rows of 2048 BF16 each and a pass over the rows take 65.3 us so, 68.9 otherwise;
+// of 16384 237 and 286; a copy into 64 MB of rows and their combine 36.8 and 37.8.
 #include "rld_device.hpp"
 #include "rld_internal.hpp"
 
@@ -340,8 +339,7 @@ __global__ void __launch_bounds__(1024) combine_grad_kernel(CombineGradArgs a) {
                 float v[N];
 #pragma unroll
                 for (int i = 0; i < N; ++i) v[i] = wj * d[i];
-                if (in(q))
-                  store_once(row, (u0 + G * q) * 16u, Unit<F32>::close(v));
+                if (in(q)) store_once(row, (u0 + G * q) * 16u, Unit<F32>::close(v));
               }
             }
           }
@@ -370,7 +368,8 @@ static bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 static int check_move(uint32_t T, uint32_t k, uint32_t width) {
   if (k == 0 || width == 0) return RLD_EINVAL;
-  if (k > kMaxMoveTopK || width > kMaxMoveWidth || (uint64_t)T * k >= (1ull << 31)) return RLD_EUNSUPPORTED;
+  if (k > kMaxMoveTopK || width > kMaxMoveWidth || (uint64_t)T * k >= (1ull << 31))
+    return RLD_EUNSUPPORTED;
   if (!mult8(width)) return RLD_EALIGN;
   return RLD_OK;
 }
@@ -425,8 +424,10 @@ static int combine(const void* rows, int f32, uint32_t rs, const int32_t* indice
   a.slices = div_ceil(a.units, 64);
   if (too_many((uint64_t)T * a.slices)) return RLD_EUNSUPPORTED;
   hipStream_t s = (hipStream_t)stream;
-  if (f32) a.places_ ? launch_combine<true, true>(a, s) : launch_combine<true, false>(a, s);
-  else a.places_ ? launch_combine<false, true>(a, s) : launch_combine<false, false>(a, s);
+  if (f32)
+    places ? launch_combine<true, true>(a, s) : launch_combine<true, false>(a, s);
+  else
+    places ? launch_combine<false, true>(a, s) : launch_combine<false, false>(a, s);
   return launch_status();
 }
 
@@ -569,7 +570,9 @@ extern "C" int rld_moe_combine_grad(const void* rows, int rows_f32, uint32_t row
   a.units = units_of(width, rows_f32);
   if (too_many(num_tokens)) return RLD_EUNSUPPORTED;
   hipStream_t s = (hipStream_t)stream;
-  if (places) rows_f32 ? launch_combine_grad<true, true>(a, s) : launch_combine_grad<false, true>(a, s);
-  else rows_f32 ? launch_combine_grad<true, false>(a, s) : launch_combine_grad<false, false>(a, s);
+  if (rows_f32)
+    places ? launch_combine_grad<true, true>(a, s) : launch_combine_grad<true, false>(a, s);
+  else
+    places ? launch_combine_grad<false, true>(a, s) : launch_combine_grad<false, false>(a, s);
   return launch_status();
 }

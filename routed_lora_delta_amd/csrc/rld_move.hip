@@ -192,10 +192,9 @@ __device__ __forceinline__ Choices<G> find_choices(const A& a, const Group<G>& g
 
 // A group adds up one slice of G units of a token's rows, in fp32, j ascending: eight
 // rows' loads at a time, the places before them, the check and the weights beside
-// them.  32771 tokens of 8 rows of 2048 BF16, onto a residual: 209 us, 5.9 TB/s, in
-// blocks of one wave (214 in blocks of four).
+// them.  32771 tokens of 8 rows of 2048 BF16, onto a residual: 209 us, 5.9 TB/s.
 template <bool F32, bool SORTED, int G>
-__global__ void __launch_bounds__(64) combine_kernel(CombineArgs a) {
+__global__ void __launch_bounds__(256) combine_kernel(CombineArgs a) {
   constexpr int N = Unit<F32>::N;
   const Group<G> g;
   const uint32_t item = g.same(group_number<G>());
@@ -386,12 +385,19 @@ static int check_tables(const int32_t* indices, const int32_t* sorted_rows,
   return aligned4(indices) && aligned4(sorted_rows) && aligned4(places) ? RLD_OK : RLD_EALIGN;
 }
 
+// Blocks of one wave, but of four where rows share cache lines, which the waves of one
+// block then find in their CU (us with one and four, rows of 2048 BF16, top_k 8: 32771
+// tokens in whole lines 209 and 214, 256 MB of rows 16 bytes apart 58 and 54; of 768 66
+// and 56).
 template <bool F32, bool SORTED>
 static void launch_combine(const CombineArgs& a, hipStream_t s) {
+  const uint32_t threads = ((a.rows_ | a.rs) & 127u) == 0 ? 64 : 256;
   if (a.units <= kNarrow)
-    combine_kernel<F32, SORTED, kNarrow><<<div_ceil(a.T, 64 / kNarrow), 64, 0, s>>>(a);
+    combine_kernel<F32, SORTED, kNarrow>
+        <<<div_ceil(a.T, threads / kNarrow), threads, 0, s>>>(a);
   else
-    combine_kernel<F32, SORTED, 64><<<a.T * a.slices, 64, 0, s>>>(a);
+    combine_kernel<F32, SORTED, 64>
+        <<<div_ceil(a.T * a.slices, threads / 64), threads, 0, s>>>(a);
 }
 
 static int combine(const void* rows, int f32, uint32_t rs, const int32_t* indices,

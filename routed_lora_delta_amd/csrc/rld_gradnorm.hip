@@ -167,23 +167,28 @@ __global__ void __launch_bounds__(256) grad_squares_kernel(GradArgs a) {
   s.leave(a, w, lane);
 }
 
-// One block a group adds its waves' sums, in a fixed order.
-__global__ void __launch_bounds__(256) grad_norms_kernel(GradArgs a) {
-  __shared__ double part[4];
+// One block a group adds its waves' sums, in a fixed order.  (Of 256 threads: 0.9 us
+// more for 1024 sums a group, 0.1 less for 64.)
+constexpr uint32_t kNormThreads = 512;
+
+__global__ void __launch_bounds__(kNormThreads) grad_norms_kernel(GradArgs a) {
+  __shared__ double part[kNormThreads / 64];
   const uint32_t g = blockIdx.x;
   const uint32_t c0 = gp<const uint32_t>(a.starts_)[g], c1 = gp<const uint32_t>(a.starts_)[g + 1];
   double s = 0.;
   if (c0 < c1 && c1 <= a.num_chunks) {
     const uint64_t p1 = wave_of(c1 - 1, a.num_chunks, a.waves) + (uint64_t)g;
     for (uint64_t p = wave_of(c0, a.num_chunks, a.waves) + (uint64_t)g + threadIdx.x; p <= p1;
-         p += 256)
+         p += kNormThreads)
       s += gp<const double>(a.partial_)[p];
   }
   s = wave_sum(s);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
   __syncthreads();
   if (threadIdx.x != 0) return;
-  s = part[0] + part[1] + part[2] + part[3];
+  s = 0.;
+#pragma unroll
+  for (uint32_t i = 0; i < kNormThreads / 64; ++i) s += part[i];
   gp<float>(a.norms_)[g] = (float)sqrt(s);
   if (a.squares_) gp<double>(a.squares_)[g] = s;
 }
@@ -301,7 +306,7 @@ extern "C" int rld_grad_norm(const rld_grad_list* list, float* norms, double* sq
   a.norms_ = (uint64_t)norms;
   a.squares_ = (uint64_t)squares;
   if (a.waves) grad_squares_kernel<<<div_ceil(a.waves, 4), 256, 0, (hipStream_t)stream>>>(a);
-  grad_norms_kernel<<<a.num_groups, 256, 0, (hipStream_t)stream>>>(a);
+  grad_norms_kernel<<<a.num_groups, kNormThreads, 0, (hipStream_t)stream>>>(a);
   return launch_status();
 }
 

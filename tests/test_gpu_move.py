@@ -380,6 +380,40 @@ def test_far_rows():
     assert bool((rows[:r.routed] == 0.25).all()) and bool((rows[r.routed:] == 77.25).all())
 
 
+@pytest.mark.parametrize("T,k,width", [(90, 4, 136), (2500, 8, 1024), (40000, 8, 64)])
+def test_flat_rows_named_twice(T, k, width):
+    """Against the rule, in one launch and in two: each of the two rows holds the token
+    or what it held, the one that places names holds the token, and the other finds
+    nobody."""
+    say(f"case: flat rows named twice T={T} k={k} width={width}")
+    r = Routing(50 + k, T, k)
+    twice = r.rng.choice(r.routed // 2, r.routed // 10, replace=False)
+    r.srows_h[twice + r.routed // 2] = r.srows_h[twice]
+    srows = r.i32(r.srows_h)
+    x = r.randn((T, width), False)
+    rows, places = spoiled((r.n, width), False, r.dev), torch.full_like(r.places, -1)
+    R.check(R.rld_moe_dispatch(x, False, width, T, k, width, srows, rows, width, places), "twice")
+    p, f = places.cpu().numpy(), r.srows_h
+    named = np.unique(f[f >= 0])
+    assert np.array_equal(f[p[named]], named) and (np.delete(p, named) == -1).all()
+    token = torch.from_numpy(np.where(f >= 0, f // k, 0)).to(r.dev)
+    same = (rows == x[token]).all(1).cpu().numpy()
+    left = (rows == 77.25).all(1).cpu().numpy()
+    assert same[p[named]].all() and (same | left)[f >= 0].all() and left[f < 0].all()
+    w, dw = r.randn((T, k), True), torch.zeros((T, k), device=r.dev)
+    out = spoiled((T, width), False, r.dev)
+    R.check(R.rld_moe_combine(rows, False, width, None, srows, places, w, T, k, width, None, 0,
+                              out, width), "combine")
+    r.places_h = p
+    total, size = sum_of(rows, r.rows_of(False), w, None, width)
+    assert_sum(out, width, total, size, k, False)
+    drows = spoiled((r.n, width), False, r.dev)
+    R.check(R.rld_moe_combine_grad(rows, False, width, None, srows, places, w, x, width, T, k,
+                                   width, drows, width, dw), "combine_grad")
+    other = np.setdiff1d(np.nonzero(f >= 0)[0], p[named])
+    assert len(other) and bool((drows[torch.from_numpy(other).to(r.dev)] == 77.25).all())
+
+
 @pytest.mark.parametrize("T,k,width", [((1 << 24) + 5, 2, 8), ((1 << 22) + 3, 2, 136)])
 def test_very_many_tokens(T, k, width):
     """Small whole numbers, so that every value is exact: a token's rows are its row of

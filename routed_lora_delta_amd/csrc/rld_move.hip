@@ -12,13 +12,16 @@
 //   combine_grad   drows[p(t, j)] = w[t, j] dout[t],  dw[t, j] = rows[p(t, j)] . dout[t]
 //
 // All of them are bound by memory.  A lane holds 16 bytes of a row (a unit): a
-// wave's access is 1 KB of one row, contiguous, or 256 bytes of each of four where a
-// row has up to 16 units (128 MB of 8 rows of 64 BF16 a token, combine 29 us and its
-// gradient 56; with a wave a token 60 and 131).  What is read once and what is written
-// passes the caches by (load_once, store_once), which costs a reader of the result
-// nothing and still finds what a writer before left in them: dispatch of 4096 tokens
-// to 8 rows of 2048 BF16 each and a pass over the rows take 65.3 us so, 68.9 otherwise;
-// of 16384 237 and 286; a copy into 64 MB of rows and their combine 36.8 and 37.8.
+// wave's access is 1 KB of one row, contiguous, or 512 bytes of each of two where a row
+// has up to 32 units, 256 of each of four where it has up to 16.  (us so and with a wave
+// for each row: 128 MB of 8 rows of 64 BF16 a token, combine 29 and 60, its gradient 56
+// and 131, dispatch 37 and 46; 200 MB of 2 rows of 192 64 and 87, 92 and 147, 60 and 80;
+// of 8 rows of 256 41 and 41, 76 and 78, 41 and 41.)  What is read once and what is
+// written passes the caches by (load_once, store_once), which costs a reader of the
+// result nothing and still finds what a writer before left in them: dispatch of 4096
+// tokens to 8 rows of 2048 BF16 each and a pass over the rows take 65.3 us so, 68.9
+// otherwise; of 16384 237 and 286; a copy into 64 MB of rows and their combine 36.8 and
+// 37.8.
 #include "rld_device.hpp"
 #include "rld_internal.hpp"
 
@@ -26,7 +29,6 @@ namespace rld {
 
 constexpr uint32_t kMaxMoveTopK = 32;
 constexpr uint32_t kMaxMoveWidth = 1u << 21;  // a row's bytes fit 32 bits
-constexpr int kNarrow = 16;                   // units of a narrow row, at most
 
 // What 16 bytes hold: 8 BF16 or 4 fp32.
 template <bool F32>
@@ -52,7 +54,8 @@ struct Unit {
   }
 };
 
-// A group of G lanes works on one token (or row): the whole wave, or 16 lanes of it.
+// A group of G lanes works on one token (or row): the whole wave, or 16 or 32 lanes of
+// it.
 // What the group has in common is in scalar registers if it is the wave.  Branches
 // around from() and vote() are the same for a whole group.
 template <int G>
@@ -378,6 +381,19 @@ static uint32_t units_of(uint32_t width, int f32) { return width / (f32 ? 4u : 8
 // One wave for each item, in a grid of fewer than 2^32 threads.
 static bool too_many(uint64_t items) { return items > (1ull << 26) - 4; }
 
+// Lanes of a group by a row's units, and a launch by them.
+template <int G>
+struct Lanes {
+  static constexpr int N = G;
+};
+
+template <class F>
+static void by_lanes(uint32_t units, F launch) {
+  if (units <= 16) launch(Lanes<16>());
+  else if (units <= 32) launch(Lanes<32>());
+  else launch(Lanes<64>());
+}
+
 // Where the rows of the choices are: both tables, or neither (flat order).
 static int check_tables(const int32_t* indices, const int32_t* sorted_rows,
                         const int32_t* places) {
@@ -392,12 +408,11 @@ static int check_tables(const int32_t* indices, const int32_t* sorted_rows,
 template <bool F32, bool SORTED>
 static void launch_combine(const CombineArgs& a, hipStream_t s) {
   const uint32_t threads = ((a.rows_ | a.rs) & 127u) == 0 ? 64 : 256;
-  if (a.units <= kNarrow)
-    combine_kernel<F32, SORTED, kNarrow>
-        <<<div_ceil(a.T, threads / kNarrow), threads, 0, s>>>(a);
-  else
-    combine_kernel<F32, SORTED, 64>
-        <<<div_ceil(a.T * a.slices, threads / 64), threads, 0, s>>>(a);
+  by_lanes(a.units, [&](auto lanes) {
+    constexpr int G = decltype(lanes)::N;
+    const uint32_t blocks = div_ceil(a.T * (G < 64 ? 1 : a.slices), threads / G);
+    combine_kernel<F32, SORTED, G><<<blocks, threads, 0, s>>>(a);
+  });
 }
 
 static int combine(const void* rows, int f32, uint32_t rs, const int32_t* indices,
@@ -439,13 +454,12 @@ static int combine(const void* rows, int f32, uint32_t rs, const int32_t* indice
 
 template <bool F32, bool SORTED, int KB>
 static void launch_combine_grad(const CombineGradArgs& a, hipStream_t s) {
-  if (a.units <= kNarrow) {
-    combine_grad_kernel<F32, SORTED, KB, kNarrow><<<div_ceil(a.T, 256 / kNarrow), 256, 0, s>>>(a);
-    return;
-  }
-  const uint32_t threads = a.waves < 4 ? 256 : 64 * a.waves;
-  combine_grad_kernel<F32, SORTED, KB, 64>
-      <<<div_ceil(a.T, threads / (64 * a.waves)), threads, 0, s>>>(a);
+  by_lanes(a.units, [&](auto lanes) {
+    constexpr int G = decltype(lanes)::N;
+    const uint32_t group = G < 64 ? G : 64 * a.waves, threads = group > 256 ? group : 256;
+    combine_grad_kernel<F32, SORTED, KB, G>
+        <<<div_ceil(a.T, threads / group), threads, 0, s>>>(a);
+  });
 }
 
 // Waves of a token: as many as take its columns at once, up to 8; 16 where 8 would take
@@ -503,20 +517,15 @@ extern "C" int rld_moe_dispatch(const void* x, int rows_f32, uint32_t x_row_stri
   // saved 169 and 254.
   const uint64_t saved = (uint64_t)(a.n - a.T) * width * size;
   const bool lines = ((a.rows_ | a.rs | width * size) & 127u) == 0;
-  const bool twice = lines ? saved >= (32u << 20)
-                           : a.units > kNarrow && saved >= (128u << 20);
-  const uint32_t groups = 256 / (a.units <= kNarrow ? kNarrow : 64);
-  if (twice) {
-    dispatch_places_kernel<<<div_ceil(a.n, 256), 256, 0, s>>>(a);
-    const uint32_t blocks = div_ceil(a.T * a.slices, groups);
-    if (a.units <= kNarrow) dispatch_tokens_kernel<kNarrow><<<blocks, 256, 0, s>>>(a);
-    else dispatch_tokens_kernel<64><<<blocks, 256, 0, s>>>(a);
-  } else {
-    a.slices = div_ceil(a.units, 64u * kRowUnits);
-    const uint32_t blocks = div_ceil(a.n * a.slices, groups);
-    if (a.units <= kNarrow) dispatch_rows_kernel<kNarrow><<<blocks, 256, 0, s>>>(a);
-    else dispatch_rows_kernel<64><<<blocks, 256, 0, s>>>(a);
-  }
+  const bool twice = lines ? saved >= (32u << 20) : a.units > 16 && saved >= (128u << 20);
+  if (twice) dispatch_places_kernel<<<div_ceil(a.n, 256), 256, 0, s>>>(a);
+  else a.slices = div_ceil(a.units, 64u * kRowUnits);
+  by_lanes(a.units, [&](auto lanes) {
+    constexpr int G = decltype(lanes)::N;
+    const uint32_t blocks = div_ceil((twice ? a.T : a.n) * a.slices, 256 / G);
+    if (twice) dispatch_tokens_kernel<G><<<blocks, 256, 0, s>>>(a);
+    else dispatch_rows_kernel<G><<<blocks, 256, 0, s>>>(a);
+  });
   return launch_status();
 }
 

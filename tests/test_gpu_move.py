@@ -173,7 +173,8 @@ def check_grad(r, width, f32, pad, flat, want_rows=True, want_w=True, in_place=F
 # units a lane, whole and partial ones; choices below, at and above a batch of eight
 SHAPES = [(1, 1, 8, 0), (1, 8, 2048, 0), (2, 32, 72, 8), (3, 5, 520, 8), (33, 8, 512, 0),
           (64, 2, 1000, 64), (129, 9, 1032, 0), (257, 4, 4104, 8), (333, 17, 64, 0),
-          (70, 1, 2048, 8), (5, 3, 8200, 0), (67, 32, 128, 8), (1500, 8, 2048, 0)]
+          (70, 1, 2048, 8), (5, 3, 8200, 0), (67, 32, 128, 8), (301, 7, 200, 8),
+          (95, 2, 256, 0), (1500, 8, 2048, 0)]
 
 
 @pytest.mark.parametrize("f32", [False, True])
@@ -193,6 +194,8 @@ def test_every_operator(T, k, width, pad, f32):
 @pytest.mark.parametrize("T,k,width,pad,f32", [
     (2500, 8, 1024, 64, False), (2500, 8, 1024, 0, True), (1100, 32, 576, 0, False),
     (40000, 8, 64, 64, False), (9000, 32, 64, 0, False), (9000, 32, 32, 0, True),
+    (20000, 8, 128, 0, True),
+    (50000, 8, 200, 0, False),
     (5000, 8, 2056, 8, False), (3500, 11, 1000, 0, True)])
 def test_dispatch_in_two_launches(T, k, width, pad, f32):
     """Rows of whole cache lines above 32 MB of reads saved, others above 128 MB."""

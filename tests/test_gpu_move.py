@@ -635,3 +635,43 @@ def test_training_step_of_an_moe_layer():
     for got, want in ((out, ref.detach()), (ls, loss.detach()[None]), (dx, X.grad),
                       (dlg.T @ xd, WG.grad), (dw1, W1.grad), (dw2, W2.grad)):
         assert float((got.cpu().double() - want).abs().max()) <= 2000 * U * float(want.abs().max())
+
+
+# rows of fewer than 16 units and of 17 to 31, which lanes of a group do not fill, whole
+# ones beside them; a wave's lanes with one unit and with two, the last round partly full;
+# one wave a token and several
+@pytest.mark.parametrize("k,width,f32", [
+    (4, 64, False), (3, 104, False), (12, 24, False), (1, 8, False), (5, 128, False),
+    (8, 200, False), (1, 136, False), (2, 256, False), (2, 1000, False), (1, 520, False),
+    (2, 1544, False), (1, 8200, False), (1, 2048, False), (9, 1032, False), (8, 2048, False),
+    (4, 40, True), (8, 104, True), (2, 200, True), (2, 1032, True), (4, 2056, True)])
+@pytest.mark.parametrize("flat", [False, True])
+def test_gradient_of_values_that_are_not_finite(k, width, f32, flat):
+    """Infinities and NaN among the last 16 bytes of a token's dout, and of a row: an
+    infinite weight's gradient with the sign of its product, NaN where NaN is, and the
+    other tokens as ever."""
+    say(f"case: dout not finite k={k} width={width} f32={f32} flat={flat}")
+    T, n = 37, 4 if f32 else 8
+    r = Routing(60 + k, T, k, masked=0.0)
+    rows, dout, w = r.randn((r.n, width), f32), r.randn((T, width), f32), r.randn((T, k), True)
+    rows = torch.where(rows.abs() < 0.01, 0.5, rows.float()).to(dtype(f32))
+    w = torch.where(w.abs() < 0.01, 0.5, w)
+    at = r.rows_of(flat)
+    dout[5, width - 1], dout[6, width - n], dout[20, width - 3] = np.inf, -np.inf, np.nan
+    rows[at[30, 0], width - 1], dout[30, width - 1] = np.inf, -2.0
+    drows, dw = spoiled((r.n, width), f32, r.dev), torch.zeros((T, k), device=r.dev)
+    s, p = r.tables(flat)
+    R.check(R.rld_moe_combine_grad(rows, f32, width, None, s, p, w, dout, width, T, k, width,
+                                   drows, width, dw), "combine_grad")
+    for t, c, sign in ((5, width - 1, 1.0), (6, width - n, -1.0)):
+        assert torch.equal(dw[t], sign * np.inf * torch.sign(rows[at[t], c].float())), t
+        for j in range(k):
+            assert float(drows[at[t, j], c]) == sign * np.inf * np.sign(float(w[t, j]))
+    assert bool(torch.isnan(dw[20]).all()) and bool(torch.isnan(drows[at[20], width - 3]).all())
+    assert float(dw[30, 0]) == -np.inf
+    assert int((~torch.isfinite(drows)).sum()) == 3 * k
+    rest = torch.ones((T, k), dtype=torch.bool, device=r.dev)
+    rest[[5, 6, 20]], rest[30, 0] = False, False
+    prod = rows[at.clamp(min=0)].double() * dout[:, None, :].double()
+    err = 2 * width * U * prod.abs().sum(2) + U * prod.sum(2).abs()
+    assert bool(((dw.double() - prod.sum(2)).abs() <= err)[rest].all())

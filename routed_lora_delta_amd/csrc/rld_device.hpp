@@ -85,10 +85,6 @@ __device__ __forceinline__ u32x4 load_unit(uint64_t base, uint32_t offset) {
   return *unit_at(base, offset);
 }
 
-__device__ __forceinline__ void store_unit(uint64_t base, uint32_t offset, const u32x4& v) {
-  *unit_at(base, offset) = v;
-}
-
 // Data that passes the chip once, past its caches.  A list of 785 MB is read at 6.3
 // TB/s so, 5.6 otherwise; 4 GB copied at 5.2 TB/s against 5.1.
 __device__ __forceinline__ u32x4 load_once(uint64_t base, uint32_t offset) {

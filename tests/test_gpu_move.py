@@ -675,3 +675,50 @@ def test_gradient_of_values_that_are_not_finite(k, width, f32, flat):
     prod = rows[at.clamp(min=0)].double() * dout[:, None, :].double()
     err = 2 * width * U * prod.abs().sum(2) + U * prod.sum(2).abs()
     assert bool(((dw.double() - prod.sum(2)).abs() <= err)[rest].all())
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("T,k,width", [(90, 5, 136), (301, 8, 64), (70, 2, 1000), (33, 9, 2056),
+                                       (2500, 8, 1024), (12000, 8, 1000)])
+def test_every_operand_with_a_stride_of_its_own(T, k, width, f32):
+    """Five strides that differ, in one launch of the dispatch and in two, in both orders."""
+    say(f"case: own strides T={T} k={k} width={width} f32={f32}")
+    r = Routing(80 + k, T, k, missing=0.05)
+    sx, sr, so, sd, sa = (width + 8 * v for v in (3, 1, 5, 0, 2))
+    x, add = r.randn((T, sx), f32), r.randn((T, sa), f32)
+    rows, w = spoiled((r.n, sr), f32, r.dev), r.randn((T, k), True)
+    places = torch.full((r.n,), -7, dtype=torch.int32, device=r.dev)
+    R.check(R.rld_moe_dispatch(x, f32, sx, T, k, width, r.srows, rows, sr, places), "dispatch")
+    want = spoiled((r.n, sr), f32, r.dev)
+    token = torch.from_numpy(r.srows_h[:r.routed] // k).to(r.dev)
+    want[:r.routed, :width] = x[token, :width]
+    assert torch.equal(rows, want)
+    assert np.array_equal(places.cpu().numpy(), np.where(r.places_h >= 0, r.places_h, -7))
+    rows, dout = r.randn((r.n, sr), f32), r.randn((T, sd), f32)
+    for flat in (False, True):
+        at, (s, p) = r.rows_of(flat), r.tables(flat)
+        out = spoiled((T, so), f32, r.dev)
+        R.check(R.rld_moe_combine(rows, f32, sr, r.indices, s, p, w, T, k, width, add, sa, out,
+                                  so), "combine")
+        assert_sum(out, width, *sum_of(rows, at, w, add, width), k, f32)
+        if not flat:
+            out = spoiled((T, so), f32, r.dev)
+            R.check(R.rld_moe_dispatch_grad(rows, f32, sr, s, p, T, k, width, add, sa, out, so),
+                    "dispatch_grad")
+            assert_sum(out, width, *sum_of(rows, at, None, add, width), k, f32)
+        drows, dw = spoiled((r.n, so), f32, r.dev), torch.full((T, k), 77.25, device=r.dev)
+        R.check(R.rld_moe_combine_grad(rows, f32, sr, r.indices, s, p, w, dout, sd, T, k, width,
+                                       drows, so, dw), "combine_grad")
+        want = spoiled((r.n, so), f32, r.dev).double()
+        for j in range(k):
+            t = (at[:, j] >= 0).nonzero().flatten()
+            want[at[t, j], :width] = w[t, j, None].double() * dout[t, :width].double()
+            prod = rows[at[t, j], :width].double() * dout[t, :width].double()
+            got, val = dw[t, j].double(), prod.sum(1)
+            err = 2 * width * U * prod.abs().sum(1) + U * val.abs()
+            assert bool(((got - val).abs() <= err).all())
+        assert bool((dw[at < 0] == 0).all())
+        err = U * want.abs()
+        off = (drows.double() - want).abs()
+        assert bool((off <= err + OUT[f32] * (want.abs() + err) + TINY).all())
+        assert bool((drows[want == 77.25] == 77.25).all())

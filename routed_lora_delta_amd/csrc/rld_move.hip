@@ -517,11 +517,13 @@ extern "C" int rld_moe_dispatch(const void* x, int rows_f32, uint32_t x_row_stri
   // tokens 5.2 and 6.4, 1024 (29 MB saved) 9.0 and 9.1, 4096 33.3 and 27.2, 16384 136
   // and 98; rows of 4096, top_k 2: 1024 6.1 and 6.8, 4096 (34 MB) 18.9 and 18.1.  Rows
   // that share cache lines are better written in order, so that their parts meet: 1000
-  // BF16, top_k 6, 106 MB saved 34.7 and 35.8, 333 MB 110 and 105; 72, top_k 8, 350 MB
-  // saved 169 and 254.
+  // BF16, top_k 6, 106 MB saved 34.7 and 35.8, 333 MB 110 and 105; 264, top_k 8, 147 MB
+  // 59.5 and 57.0, top_k 2, 131 and 105; but 2056, top_k 8, 46 and 51.  Of up to 32 units,
+  // which share a wave, they always are: 200, top_k 8, 147 MB saved 53 and 64, 315 MB 115
+  // and 132, top_k 2, 147 MB 111 and 118; 136, top_k 8, 57 and 74; 72, 350 MB 169 and 254.
   const uint64_t saved = (uint64_t)(a.n - a.T) * width * size;
   const bool lines = ((a.rows_ | a.rs | width * size) & 127u) == 0;
-  const bool twice = lines ? saved >= (32u << 20) : a.units > 16 && saved >= (128u << 20);
+  const bool twice = lines ? saved >= (32u << 20) : a.units > 32 && saved >= (128u << 20);
   if (twice) dispatch_places_kernel<<<div_ceil(a.n, 256), 256, 0, s>>>(a);
   else a.slices = div_ceil(a.units, 64u * kRowUnits);
   by_lanes(a.units, [&](auto lanes) {

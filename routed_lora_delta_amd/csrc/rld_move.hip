@@ -159,8 +159,9 @@ struct CombineArgs {
 
 // The rows of a token's choices j0 .. j0 + KB - 1: lane j of the group holds choice
 // j0 + j.  `have` has a bit for each row that can be read; own() one for each of them
-// that belongs to its choice, which takes one load more: called once the rows' loads
-// are out.
+// that belongs to its choice, which takes one load more.  The sums call it once the
+// rows' loads are out; combine's gradient, whose stores need it, before them, and waits
+// for it by itself.
 template <int G>
 struct Choices {
   uint32_t row, back, f;
@@ -271,7 +272,10 @@ __device__ __forceinline__ float sum_each(float* v, uint32_t lane) {
 }
 
 // Units of a row that a lane of combine_grad takes at a time, by the rows it takes: 62500
-// tokens of one row of 2048 BF16 118 us with two, 123 with one or four.
+// tokens of one row of 2048 BF16 118 us with two, 123 with one or four.  Two rows are
+// within 10 percent either way (us with two and one: 31250 tokens of 2048 BF16 104 and
+// 102, 64000 of 1000 121 and 113, 123076 of 520 129 and 133, 61538 of 520 fp32 115 and
+// 133).
 __host__ __device__ constexpr uint32_t units_per_lane(uint32_t rows) { return rows > 2 ? 1 : 2; }
 
 // `waves` groups share a token's columns (one, if groups are narrow).  A group takes KB
